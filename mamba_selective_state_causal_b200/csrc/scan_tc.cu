@@ -29,6 +29,7 @@
 
 #include <cuda.h>
 
+#include "scan_tc_util.cuh"
 #include "ssd_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -41,10 +42,6 @@ namespace {
 using namespace tc;
 
 constexpr int kQ = 128, kP = 64, kN = 128;
-constexpr uint32_t kBox = 128 * 64 * 2;   // one 128-row x 64-col bf16 TMA box (16 KB)
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
 struct Maps {
     CUtensorMap x, B, C, y;
     CUtensorMap ux;     // fused conv: x columns of the conv input u, boxes of 136 rows (8-row halo)
@@ -52,50 +49,6 @@ struct Maps {
 
 constexpr int kHaloRows = 8;                                   // rows before a chunk in a fused X box
 constexpr uint32_t kBoxX = kBox + kHaloRows * 128;             // a fused X box: 136 rows x 128 bytes
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Bounded wait whose outcome is the same for every lane of the warp, so that
-// the warp stays converged for the .sync.aligned TMEM instructions after it.
-__device__ __forceinline__ bool ewait(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns)
-{
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns));
-}
-
-// byte offset of 16-byte chunk c of row r in a 128B-swizzled tile of 128-byte rows
-__device__ __forceinline__ uint32_t swz(int r, int c)
-{
-    return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
-}
-
-__device__ __forceinline__ uint4 lds128(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
-__device__ __forceinline__ void sts128(uint8_t *p, uint4 v) { *reinterpret_cast<uint4 *>(p) = v; }
-
-
-// fp32 pair -> bf16x2 by integer rounding (half an ulp added, ties away from zero), on the
-// integer pipe so that it runs beside the conversion unit; inputs are finite
-__device__ __forceinline__ uint32_t pack_bf16x2_int(float lo, float hi)
-{
-    return __byte_perm(__float_as_uint(lo) + 0x8000u, __float_as_uint(hi) + 0x8000u, 0x7632);
-}
-
-__device__ __forceinline__ uint32_t scale_bf16x2_int(uint32_t v, float w)
-{
-    return pack_bf16x2_int(bf16_lo(v) * w, bf16_hi(v) * w);
-}
-
-// two fp32 products / fused multiply-adds in one instruction (sm_100 packed fp32, through the
-// CUDA float2 intrinsics, which leave the register pairing to the compiler); each lane rounds
-// exactly as the scalar instruction does
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
-
-__device__ __forceinline__ float2 unpack2(uint32_t v) { return make_float2(bf16_lo(v), bf16_hi(v)); }
 
 // Conv + SiLU of 8 channels (4 pairs) of one token: window m3 = u[t-3], m2, m1, cur = u[t],
 // weights w[pair][tap] and bias as channel pairs, both already halved, so that the sum is
@@ -124,13 +77,6 @@ __device__ __forceinline__ uint4 conv8(const float2 (&w)[4][4], const float2 (&b
 __device__ __forceinline__ void unpack8(uint4 v, float2 (&f)[4])
 {
     f[0] = unpack2(v.x); f[1] = unpack2(v.y); f[2] = unpack2(v.z); f[3] = unpack2(v.w);
-}
-
-// bf16 pair times w, rounded to nearest even (cvt)
-__device__ __forceinline__ uint32_t scale_bf16x2_rn(uint32_t v, float2 w2)
-{
-    const float2 p = mul2(unpack2(v), w2);
-    return pack_bf16x2(p.x, p.y);
 }
 
 __device__ __forceinline__ void raise_timeout(const ScanParams &p, volatile int *abort)
@@ -1119,39 +1065,6 @@ chunk_output_tc_kernel(const __grid_constant__ Maps maps, const ScanParams p)
 }
 
 // =============================================================== host side
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                  CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn()
-{
-    // looked up once per process (a function-local static is initialised thread-safely)
-    static const EncodeTiledFn fn = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeTiledFn>(f);
-        return (EncodeTiledFn) nullptr;
-    }();
-    return fn;
-}
-
-// [b][L][cols] view with element strides (rs, bs); box = 64 columns x 128 rows
-bool encode_bf16(EncodeTiledFn enc, CUtensorMap *m, const void *base, int64_t cols, int64_t L, int b,
-                 int64_t rs, int64_t bs, uint32_t box_rows = 128)
-{
-    if (b == 1) bs = rs * L;
-    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)L, (cuuint64_t)b};
-    const cuuint64_t strides[2] = {(cuuint64_t)rs * 2, (cuuint64_t)bs * 2};
-    const cuuint32_t box[3] = {64, box_rows, 1};
-    const cuuint32_t es[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 
 constexpr size_t kSmemA = sizeof(SmemA) + 1024;
 constexpr size_t kSmemC = sizeof(SmemC);   // no alignment pad: the base is checked in the kernel
