@@ -69,7 +69,8 @@ typedef enum ssd_status {
     SSD_ERR_UNSUPPORTED = 6, /* valid, but no GPU kernel for this shape */
     SSD_ERR_LAUNCH = 7,      /* CUDA launch or runtime error */
     SSD_ERR_TIMEOUT = 8,     /* a bounded device-side wait gave up (device status) */
-    SSD_ERR_WORKSPACE = 9    /* workspace missing or smaller than required */
+    SSD_ERR_WORKSPACE = 9,   /* workspace missing or smaller than required */
+    SSD_ERR_INDEX = 10       /* a sequence offset or slot was refused on the device (device status) */
 } ssd_status;
 
 /*
@@ -431,6 +432,264 @@ SSD_API int ssd_gated_rmsnorm_forward(const void *y, int64_t y_row_stride, const
                                       ssd_stream_t stream);
 
 /*
+ * Packed sequences: nseq sequences of any lengths laid end to end in the rows of tensors
+ * [total][...], sequence i in rows cu_seqlens[i] .. cu_seqlens[i+1]-1 (serving: the prompts
+ * of one step; training: documents in one row of tokens).  Their states and conv buffers live in
+ * pools of slots: h [n_slots][H][P][N] float, tail [n_slots][3][C_ch].
+ *
+ * ssd_packed_plan -- make the plan of a batch on the device: two launches, once per batch; every
+ * packed call on that batch (all layers, forward and backward) takes it.  Nothing is read
+ * back to the host, so the call can be captured, and replayed with other contents of the
+ * same buffers.
+ *   cu_seqlens [nseq + 1] int32, not decreasing, within 0 .. total; rows outside
+ *              [cu_seqlens[0], cu_seqlens[nseq]) belong to no sequence and are neither read
+ *              nor written by any packed call.  A sequence may be empty.
+ *   slots      [nseq] int32 or NULL (sequence i has slot i): 0 .. n_slots-1, or -1: the
+ *              sequence starts from zero and its state is not kept.  At most 16384
+ *              sequences when given.
+ *   resume     [nseq] int32 or NULL (all resume): 0 = the sequence starts from zero, whatever
+ *              its slot holds; else from its slot of h_in / tail_in, where those are given.
+ *   n_slots    slots of the pools; without slots 0 stands for nseq.
+ *   max_seqlen a bound of the lengths, or 0 (total): calls may choose their launches by it.
+ *   plan       device buffer of ssd_packed_plan_size(nseq, total) bytes, 16-byte aligned.
+ * What the host cannot see is checked on the device, and reported by ssd_sync_status() as
+ * SSD_ERR_INDEX: a sequence whose offsets decrease, overlap an earlier one, leave the rows or exceed
+ * max_seqlen is left out (its rows, state and buffer stay as they were); a slot out of range, or
+ * that an earlier sequence of the batch has, counts as -1.
+ */
+typedef struct ssd_packed_plan_args {
+    int nseq;
+    int64_t total;
+    const int32_t *cu_seqlens;
+    const int32_t *slots;
+    const int32_t *resume;
+    int n_slots;
+    int64_t max_seqlen;
+    void *plan;
+    size_t plan_bytes;
+} ssd_packed_plan_args;
+
+SSD_API int ssd_packed_plan(const ssd_packed_plan_args *args, ssd_stream_t stream);
+SSD_API size_t ssd_packed_plan_size(int nseq, int64_t total);
+
+/*
+ * ssd_packed_conv_forward -- ssd_conv_forward on each sequence of a packed batch: the rows
+ * before a sequence's first come from its slot of tail_in, or are zeros.
+ *   nseq, total, plan   as given to ssd_packed_plan (a plan of other sizes: SSD_ERR_INDEX
+ *                       from ssd_sync_status, nothing written)
+ *   u, v     [total][C_ch], row strides in elements; v must not overlap u
+ *   conv_w   [C_ch][4] float, conv_bias [C_ch] float or NULL
+ *   tail_in  [n_slots][3][C_ch] or NULL (zeros); tail_out the same layout or NULL; tail_out
+ *            may be tail_in.  Slots that the batch does not name stay as they were.
+ * C_ch a multiple of 8 (bf16) or 4 (f32); 16-byte aligned pointers and row strides.
+ */
+typedef struct ssd_packed_conv_args {
+    int dtype;
+    int nseq;
+    int64_t total;
+    int C_ch;
+    const void *plan;
+    const void *u;
+    int64_t u_row_stride;
+    const float *conv_w;
+    const float *conv_bias;
+    const void *tail_in;
+    void *tail_out;
+    void *v;
+    int64_t v_row_stride;
+} ssd_packed_conv_args;
+
+SSD_API int ssd_packed_conv_forward(const ssd_packed_conv_args *args, ssd_stream_t stream);
+
+/*
+ * ssd_packed_conv_backward -- gradients through ssd_packed_conv_forward, given those of v
+ * (float, contiguous, as ssd_packed_scan_backward returns them: dx [total][d_inner], dB and
+ * dC [total][d_bc], d_inner = H*P, d_bc = G*N, both multiples of 8) and dtail_out
+ * [nseq][3][C_ch] float or NULL (dLoss/d(tail_out), by SEQUENCE, not by slot).
+ * C_ch = d_inner + 2*d_bc.  Outputs, float, contiguous: du [total][C_ch]
+ * (rows of no sequence stay as they were); dtail_in [nseq][3][C_ch] or NULL (zero for a sequence
+ * that does not resume); dconv_w [C_ch][4]; dconv_bias [C_ch] or NULL.  The rounding of v to the
+ * I/O dtype is taken as the identity.  Sums are in a fixed order: the same result every time.
+ */
+typedef struct ssd_packed_conv_bwd_args {
+    int dtype;
+    int nseq;
+    int64_t total;
+    int d_inner, d_bc;
+    const void *plan;
+    const void *u;
+    int64_t u_row_stride;
+    const float *conv_w;
+    const float *conv_bias;
+    const void *tail_in;
+    const float *dx, *dB, *dC;
+    const float *dtail_out;
+    float *du, *dtail_in, *dconv_w, *dconv_bias;
+    void *workspace;
+    size_t workspace_bytes;
+} ssd_packed_conv_bwd_args;
+
+SSD_API int ssd_packed_conv_backward(const ssd_packed_conv_bwd_args *args, ssd_stream_t stream);
+SSD_API size_t ssd_packed_conv_backward_workspace_size(int nseq, int64_t total, int C_ch);
+
+/*
+ * ssd_packed_scan_forward -- the selective scan on each sequence of a packed batch.
+ *   x [total][H*P], B, C [total][G*N], y [total][H*P]: I/O dtype, row strides in elements
+ *       (x, B, C may be column slices of the conv output)
+ *   dt [total][H] float, contiguous, 8-byte aligned; A [H], D [H] or NULL; dt_bias,
+ *       dt_softplus, dt_min, dt_max as in ssd_scan_args
+ *   h_in  [n_slots][H][P][N] float or NULL (zeros): the state of a resumed sequence's slot
+ *   h_out the same layout or NULL (not kept); it may be h_in.  Slots that the batch does not
+ *       name stay as they were.  An empty sequence's state is its start.
+ *   max_seqlen as given to ssd_packed_plan
+ *   workspace  ssd_packed_scan_workspace_size() bytes, 256-byte aligned (NULL when that is 0)
+ * bf16 with P = 64, N = 128 and an even number of heads per group runs on the tensor cores.  States are
+ * float and exact to about 2^-17 of each term: the products that form them take the bf16 rounding of
+ * dt e^{..} x and what it leaves.  y is rounded once; within a chunk its terms are products of bf16
+ * operands accumulated in float.
+ */
+typedef struct ssd_packed_scan_args {
+    int dtype;
+    int nseq;
+    int64_t total;
+    int64_t max_seqlen;
+    int H, P, N, G;
+    const void *plan;
+    const void *x;
+    int64_t x_row_stride;
+    const void *B;
+    int64_t B_row_stride;
+    const void *C;
+    int64_t C_row_stride;
+    const float *dt;
+    const float *A;
+    const float *D;
+    const float *dt_bias;
+    int dt_softplus;
+    float dt_min, dt_max;
+    const float *h_in;
+    float *h_out;
+    void *y;
+    int64_t y_row_stride;
+    void *workspace;
+    size_t workspace_bytes;
+} ssd_packed_scan_args;
+
+SSD_API int ssd_packed_scan_forward(const ssd_packed_scan_args *args, ssd_stream_t stream);
+SSD_API size_t ssd_packed_scan_workspace_size(int nseq, int64_t total, int64_t max_seqlen, int H, int P, int N, int G,
+                                              int dtype);
+
+/*
+ * ssd_packed_scan_backward -- gradients through ssd_packed_scan_forward, the states rebuilt
+ * from h_in over each sequence.
+ *   x, B, C, dt, A, D, h_in as in the forward (dt the step the scan USED, as in ssd_scan_bwd_args)
+ *   dy [total][H*P] I/O dtype, row stride in elements: dLoss/dy
+ *   dh_out [nseq][H][P][N] float or NULL: dLoss/d(h_out), by SEQUENCE, not by slot
+ * Outputs, float, contiguous: dx [total][H][P]; dB, dC [total][G][N]; ddt [total][H] (rows of
+ * no sequence stay as they were); dA [H]; dD [H] or NULL; dh_in [nseq][H][P][N] or NULL
+ * (zero for a sequence that does not resume).  Sums are in a fixed order.
+ */
+typedef struct ssd_packed_scan_bwd_args {
+    int dtype;
+    int nseq;
+    int64_t total;
+    int H, P, N, G;
+    const void *plan;
+    const void *x;
+    int64_t x_row_stride;
+    const void *B;
+    int64_t B_row_stride;
+    const void *C;
+    int64_t C_row_stride;
+    const float *dt;
+    const float *A;
+    const float *D;
+    const float *h_in;
+    const void *dy;
+    int64_t dy_row_stride;
+    const float *dh_out;
+    float *dx, *dB, *dC, *ddt, *dA, *dD, *dh_in;
+    void *workspace;
+    size_t workspace_bytes;
+} ssd_packed_scan_bwd_args;
+
+SSD_API int ssd_packed_scan_backward(const ssd_packed_scan_bwd_args *args, ssd_stream_t stream);
+SSD_API size_t ssd_packed_scan_backward_workspace_size(int nseq, int64_t total, int H, int P, int N);
+
+/*
+ * ssd_decode_slots -- one token of b streams whose states and conv buffers are slots of a
+ * pool, in one launch: conv + SiLU from the slot's buffer, the state step, y.
+ *   slots    [b] int32: row i of the batch is the stream in slots[i]; -1 = an empty row (a batch
+ *            padded to a fixed size): its y is zero, nothing else is touched.  A slot out of
+ *            range, or that an earlier row has, is treated as empty and reported by
+ *            ssd_sync_status() as SSD_ERR_INDEX.
+ *   u [b][C_ch], y [b][H*P]: I/O dtype, row strides in elements; dt [b][H] float
+ *   tail_in, tail_out [n_slots][3][C_ch]; h_in, h_out [n_slots][H][P][N] float: the outputs may
+ *            be the inputs (updated in place); otherwise slots that the batch does not name
+ *            stay as they were in the outputs.
+ * The conv output is not rounded to the I/O dtype here (it is never stored).
+ */
+typedef struct ssd_decode_slots_args {
+    int dtype;
+    int b;
+    int n_slots;
+    int H, P, N, G;
+    const int32_t *slots;
+    const void *u;
+    int64_t u_batch_stride;
+    const float *conv_w;
+    const float *conv_bias;
+    const void *tail_in;
+    void *tail_out;
+    const float *dt;
+    const float *A;
+    const float *D;
+    const float *dt_bias;
+    int dt_softplus;
+    float dt_min, dt_max;
+    const float *h_in;
+    float *h_out;
+    void *y;
+    int64_t y_batch_stride;
+} ssd_decode_slots_args;
+
+SSD_API int ssd_decode_slots(const ssd_decode_slots_args *args, ssd_stream_t stream);
+
+/*
+ * ssd_gated_rmsnorm_backward -- gradients through ssd_gated_rmsnorm_forward:
+ *   with v = y silu(z), r = 1 / sqrt(mean_group v^2 + eps), g = dout * weight:
+ *   dv = r (g - v r^2 mean_group(g v)), dy = dv silu(z), dz = dv y silu'(z),
+ *   dweight[c] = sum over rows of dout v r.
+ *   dout, y, z, dy, dz: rows of d channels, I/O dtype, row strides in elements; dy may be
+ *   dout or y, dz may be z (same stride): a row is read before it is written.
+ *   dweight [d] float, summed in a fixed order.
+ *   workspace: ssd_gated_rmsnorm_backward_workspace_size() bytes, 256-byte aligned.
+ */
+typedef struct ssd_gated_rmsnorm_bwd_args {
+    int dtype;
+    int64_t rows;
+    int d, group_size;
+    float eps;
+    const void *dout;
+    int64_t dout_row_stride;
+    const void *y;
+    int64_t y_row_stride;
+    const void *z;
+    int64_t z_row_stride;
+    const float *weight;
+    void *dy;
+    int64_t dy_row_stride;
+    void *dz;
+    int64_t dz_row_stride;
+    float *dweight;
+    void *workspace;
+    size_t workspace_bytes;
+} ssd_gated_rmsnorm_bwd_args;
+
+SSD_API int ssd_gated_rmsnorm_backward(const ssd_gated_rmsnorm_bwd_args *args, ssd_stream_t stream);
+SSD_API size_t ssd_gated_rmsnorm_backward_workspace_size(int64_t rows, int d, int dtype);
+
+/*
  * ssd_scan_forward_static_scratch -- ssd_scan_forward for callers that cannot
  * allocate device memory.  (The pages have no counterpart: this is a
  * deployment aid of this library, not part of the layer they describe.)
@@ -458,8 +717,8 @@ SSD_API int ssd_scan_forward_static_scratch(const ssd_scan_args *args, ssd_strea
 /*
  * ssd_sync_status -- synchronise `stream`, then return SSD_ERR_LAUNCH if the
  * CUDA runtime reports an error, else the device status word latched by
- * this library's kernels on the current device (SSD_OK or SSD_ERR_TIMEOUT),
- * which it then clears.
+ * this library's kernels on the current device (SSD_OK, SSD_ERR_TIMEOUT, or SSD_ERR_INDEX
+ * from the packed calls), which it then clears.
  */
 SSD_API int ssd_sync_status(ssd_stream_t stream);
 

@@ -6,6 +6,7 @@ compiled library is missing, importing the binding's functions raises: there
 is no fallback implementation.
 """
 import ctypes
+import math
 import os
 
 import torch
@@ -16,7 +17,7 @@ LIB_PATH = os.path.join(HERE, "libssd.so")
 SSD_F32, SSD_BF16 = 0, 1
 STATUS = {0: "SSD_OK", 1: "SSD_ERR_NULL", 2: "SSD_ERR_SHAPE", 3: "SSD_ERR_ALIGN",
           4: "SSD_ERR_STRIDE", 5: "SSD_ERR_DTYPE", 6: "SSD_ERR_UNSUPPORTED",
-          7: "SSD_ERR_LAUNCH", 8: "SSD_ERR_TIMEOUT", 9: "SSD_ERR_WORKSPACE"}
+          7: "SSD_ERR_LAUNCH", 8: "SSD_ERR_TIMEOUT", 9: "SSD_ERR_WORKSPACE", 10: "SSD_ERR_INDEX"}
 
 _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
@@ -103,6 +104,63 @@ class LayerBwdArgs(ctypes.Structure):
                 ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class PackedPlanArgs(ctypes.Structure):
+    _fields_ = [("nseq", ctypes.c_int), ("total", _i64), ("cu_seqlens", _vp), ("slots", _vp), ("resume", _vp),
+                ("n_slots", ctypes.c_int), ("max_seqlen", _i64), ("plan", _vp), ("plan_bytes", ctypes.c_size_t)]
+
+
+class PackedConvArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("nseq", ctypes.c_int), ("total", _i64), ("C_ch", ctypes.c_int), ("plan", _vp),
+                ("u", _vp), ("u_row_stride", _i64), ("conv_w", _vp), ("conv_bias", _vp), ("tail_in", _vp),
+                ("tail_out", _vp), ("v", _vp), ("v_row_stride", _i64)]
+
+
+class PackedConvBwdArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("nseq", ctypes.c_int), ("total", _i64),
+                ("d_inner", ctypes.c_int), ("d_bc", ctypes.c_int), ("plan", _vp),
+                ("u", _vp), ("u_row_stride", _i64), ("conv_w", _vp), ("conv_bias", _vp), ("tail_in", _vp),
+                ("dx", _vp), ("dB", _vp), ("dC", _vp), ("dtail_out", _vp),
+                ("du", _vp), ("dtail_in", _vp), ("dconv_w", _vp), ("dconv_bias", _vp),
+                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class PackedScanArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("nseq", ctypes.c_int), ("total", _i64), ("max_seqlen", _i64),
+                ("H", ctypes.c_int), ("P", ctypes.c_int), ("N", ctypes.c_int), ("G", ctypes.c_int), ("plan", _vp),
+                ("x", _vp), ("x_row_stride", _i64), ("B", _vp), ("B_row_stride", _i64), ("C", _vp),
+                ("C_row_stride", _i64), ("dt", _vp), ("A", _vp), ("D", _vp), ("dt_bias", _vp),
+                ("dt_softplus", ctypes.c_int), ("dt_min", ctypes.c_float), ("dt_max", ctypes.c_float),
+                ("h_in", _vp), ("h_out", _vp), ("y", _vp), ("y_row_stride", _i64),
+                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class PackedScanBwdArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("nseq", ctypes.c_int), ("total", _i64),
+                ("H", ctypes.c_int), ("P", ctypes.c_int), ("N", ctypes.c_int), ("G", ctypes.c_int), ("plan", _vp),
+                ("x", _vp), ("x_row_stride", _i64), ("B", _vp), ("B_row_stride", _i64), ("C", _vp),
+                ("C_row_stride", _i64), ("dt", _vp), ("A", _vp), ("D", _vp), ("h_in", _vp),
+                ("dy", _vp), ("dy_row_stride", _i64), ("dh_out", _vp),
+                ("dx", _vp), ("dB", _vp), ("dC", _vp), ("ddt", _vp), ("dA", _vp), ("dD", _vp), ("dh_in", _vp),
+                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class DecodeSlotsArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("b", ctypes.c_int), ("n_slots", ctypes.c_int),
+                ("H", ctypes.c_int), ("P", ctypes.c_int), ("N", ctypes.c_int), ("G", ctypes.c_int),
+                ("slots", _vp), ("u", _vp), ("u_batch_stride", _i64), ("conv_w", _vp), ("conv_bias", _vp),
+                ("tail_in", _vp), ("tail_out", _vp), ("dt", _vp), ("A", _vp), ("D", _vp), ("dt_bias", _vp),
+                ("dt_softplus", ctypes.c_int), ("dt_min", ctypes.c_float), ("dt_max", ctypes.c_float),
+                ("h_in", _vp), ("h_out", _vp), ("y", _vp), ("y_batch_stride", _i64)]
+
+
+class GatedRmsnormBwdArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("rows", _i64), ("d", ctypes.c_int), ("group_size", ctypes.c_int),
+                ("eps", ctypes.c_float), ("dout", _vp), ("dout_row_stride", _i64), ("y", _vp), ("y_row_stride", _i64),
+                ("z", _vp), ("z_row_stride", _i64), ("weight", _vp), ("dy", _vp), ("dy_row_stride", _i64),
+                ("dz", _vp), ("dz_row_stride", _i64), ("dweight", _vp),
+                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _lib = None
 
 
@@ -142,6 +200,19 @@ def lib():
         L.ssd_scan_workspace_size.argtypes = [ctypes.c_int, _i64, ctypes.c_int, ctypes.c_int,
                                               ctypes.c_int, ctypes.c_int]
         L.ssd_scan_workspace_size.restype = ctypes.c_size_t
+        for name, args in (("ssd_packed_plan", PackedPlanArgs), ("ssd_packed_conv_forward", PackedConvArgs),
+                           ("ssd_packed_conv_backward", PackedConvBwdArgs), ("ssd_packed_scan_forward", PackedScanArgs),
+                           ("ssd_packed_scan_backward", PackedScanBwdArgs), ("ssd_decode_slots", DecodeSlotsArgs),
+                           ("ssd_gated_rmsnorm_backward", GatedRmsnormBwdArgs)):
+            getattr(L, name).argtypes = [ctypes.POINTER(args), _vp]
+            getattr(L, name).restype = ctypes.c_int
+        for name, args in (("ssd_packed_plan_size", [ctypes.c_int, _i64]),
+                           ("ssd_packed_conv_backward_workspace_size", [ctypes.c_int, _i64, ctypes.c_int]),
+                           ("ssd_packed_scan_workspace_size", [ctypes.c_int, _i64, _i64] + [ctypes.c_int] * 5),
+                           ("ssd_packed_scan_backward_workspace_size", [ctypes.c_int, _i64] + [ctypes.c_int] * 3),
+                           ("ssd_gated_rmsnorm_backward_workspace_size", [_i64, ctypes.c_int, ctypes.c_int])):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = ctypes.c_size_t
         L.ssd_sync_status.argtypes = [_vp]
         L.ssd_sync_status.restype = ctypes.c_int
         L.ssd_last_error_string.argtypes = []
@@ -505,3 +576,386 @@ def gated_rmsnorm(y, z, weight, eps=1e-5, group_size=0, out=None, stream=None):
                                          _stream(stream))
     _check(rc)
     return out
+
+
+# ---------------------------------------------------------------- packed sequences and slots
+def _same_device(dev, *ts):
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+
+
+def _shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _full(t, shape, dtype, name):
+    """Check for a contiguous tensor of this shape and type (or None)."""
+    if t is not None:
+        _shape(t, shape, name)
+        if t.dtype != dtype or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous {dtype} tensor")
+    return t
+
+
+def _rows2(t, width, dtype, name):
+    """Rows of `width` elements side by side in memory: (data pointer, row stride) of a [rows, width] view."""
+    if t.dim() != 2 or t.shape[1] != width:
+        raise ValueError(f"{name} must be [rows, {width}], got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    # a tensor of one row (or none) may carry any stride
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+
+
+def _launch(fn, a, dev, stream):
+    """Call a C entry point with `dev` current, on `stream` or the device's current stream."""
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            s = stream or torch.cuda.current_stream(dev)
+            _check(fn(ctypes.byref(a), s.cuda_stream))
+        return
+    s = stream or torch.cuda.current_stream(dev)
+    _check(fn(ctypes.byref(a), s.cuda_stream))
+
+
+def _bytes_on(dev, n):
+    return torch.empty(max(int(n), 1), dtype=torch.uint8, device=dev)
+
+
+def _ws(workspace, need, dev):
+    if workspace is None:
+        workspace = _bytes_on(dev, need)
+    _same_device(dev, workspace)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+class PackedPlan:
+    """The plan of a packed batch (packed_plan): keep it while calls on the batch are in flight."""
+
+    def __init__(self, buf, nseq, total, n_slots, max_seqlen, has_slots):
+        self.buf, self.nseq, self.total, self.n_slots = buf, nseq, total, n_slots
+        self.max_seqlen, self.has_slots, self.device = max_seqlen, has_slots, buf.device
+
+
+def packed_plan(cu_seqlens, total, *, slots=None, resume=None, n_slots=0, max_seqlen=0, buf=None, stream=None):
+    """The plan of a batch of sequences laid end to end: sequence i has rows cu_seqlens[i] .. cu_seqlens[i+1]-1
+    of tensors with `total` rows.  Made on the device, once per batch, and taken by every packed call.
+
+    cu_seqlens [n+1] int32; slots [n] int32 or None (sequence i has slot i), -1 = not kept; resume [n] int32 or
+    None (all): 0 = start from zero; n_slots: slots of the state pools (0 without slots: n); max_seqlen: a
+    bound of the lengths (0: total).  buf: the plan's memory (uint8, lib().ssd_packed_plan_size(n, total)
+    bytes), to make it again in the same place (under a captured graph).
+    """
+    _cuda(cu_seqlens, slots, resume, buf)
+    dev = cu_seqlens.device
+    _same_device(dev, slots, resume, buf)
+    n = cu_seqlens.numel() - 1
+    if n < 0:
+        raise ValueError("cu_seqlens needs at least one entry")
+    _full(cu_seqlens, (n + 1,), torch.int32, "cu_seqlens")
+    _full(slots, (n,), torch.int32, "slots")
+    _full(resume, (n,), torch.int32, "resume")
+    if slots is not None and n_slots <= 0 and n > 0:
+        raise ValueError("n_slots is needed with slots")
+    a = PackedPlanArgs()
+    a.nseq = n; a.total = total
+    a.cu_seqlens = cu_seqlens.data_ptr(); a.slots = _vp_of(slots); a.resume = _vp_of(resume)
+    a.n_slots = n_slots; a.max_seqlen = max_seqlen
+    buf, a.plan, a.plan_bytes = _ws(buf, lib().ssd_packed_plan_size(n, total), dev)
+    _launch(lib().ssd_packed_plan, a, dev, stream)
+    return PackedPlan(buf, n, int(total), n_slots if slots is not None else max(n_slots, n), int(max_seqlen), slots is not None)
+
+
+def _plan_args(a, plan, rows, dev):
+    if rows != plan.total:
+        raise ValueError(f"the plan is for {plan.total} rows, the tensors have {rows}")
+    if plan.device != dev:
+        raise ValueError(f"the plan is on {plan.device}, the tensors on {dev}")
+    a.nseq = plan.nseq; a.total = plan.total; a.plan = plan.buf.data_ptr()
+
+
+def packed_conv_forward(u, w, plan, bias=None, tail_in=None, tail_out=None, v=None, stream=None):
+    """v = silu(causal_conv1d_k4(u)) on each sequence of the plan; returns (v, tail_out).
+
+    u: [total, C_ch] (a view with any row stride of whole 16 bytes); tail_in, tail_out: [n_slots, 3, C_ch] or
+    None, tail_out may be tail_in.  Rows of v that belong to no sequence stay as they were.
+    """
+    _cuda(u, w, bias, tail_in, tail_out, v)
+    dev = u.device
+    _same_device(dev, w, bias, tail_in, tail_out, v)
+    total, cch = u.shape
+    if v is None:
+        v = torch.empty(total, cch, dtype=u.dtype, device=dev)
+    a = PackedConvArgs()
+    a.dtype = _dtype_code(u); a.C_ch = cch
+    _plan_args(a, plan, total, dev)
+    a.u, a.u_row_stride = _rows2(u, cch, u.dtype, "u")
+    _shape(v, (total, cch), "v")
+    a.v, a.v_row_stride = _rows2(v, cch, u.dtype, "v")
+    a.conv_w = _full(w, (cch, 4), torch.float32, "w").data_ptr()
+    a.conv_bias = _vp_of(_full(bias, (cch,), torch.float32, "bias"))
+    a.tail_in = _vp_of(_full(tail_in, (plan.n_slots, 3, cch), u.dtype, "tail_in"))
+    a.tail_out = _vp_of(_full(tail_out, (plan.n_slots, 3, cch), u.dtype, "tail_out"))
+    _launch(lib().ssd_packed_conv_forward, a, dev, stream)
+    return v, tail_out
+
+
+def packed_conv_backward_workspace(plan, cch):
+    """Workspace of packed_conv_backward for this plan and channel count."""
+    return _bytes_on(plan.device, lib().ssd_packed_conv_backward_workspace_size(plan.nseq, plan.total, cch))
+
+
+def packed_conv_backward(u, w, plan, dx, dB, dC, *, bias=None, tail_in=None, dtail_out=None, out=None, workspace=None, stream=None):
+    """Gradients through packed_conv_forward: dict du [total, C_ch], dtail_in [n, 3, C_ch], dconv_w, dconv_bias (float32).
+
+    dx [total, (H, P)], dB, dC [total, (G, N)]: float32 gradients of v's columns, as packed_scan_backward returns
+    them; dtail_out: [n, 3, C_ch] float32 or None, by sequence.  ``out`` may hold outputs under the same keys;
+    rows of no sequence stay as they were in them, and are zero in those allocated here.
+    """
+    _cuda(u, w, dx, dB, dC, bias, tail_in, dtail_out, workspace)
+    dev = u.device
+    _same_device(dev, w, dx, dB, dC, bias, tail_in, dtail_out, workspace)
+    total, cch = u.shape
+    hp, gn = math.prod(dx.shape[1:]), math.prod(dB.shape[1:])
+    if dx.shape[0] != total or dB.shape[0] != total or dC.shape != dB.shape or hp + 2 * gn != cch:
+        raise ValueError(f"dx, dB and dC must be [{total}, ...] with {cch} channels in all")
+    n = plan.nseq
+    o = dict(out or {})
+    for k, shp in (("du", (total, cch)), ("dtail_in", (n, 3, cch)), ("dconv_w", (cch, 4)), ("dconv_bias", (cch,))):
+        if k not in o:
+            o[k] = torch.zeros(shp, dtype=torch.float32, device=dev)
+        _full(o[k], shp, torch.float32, k)
+        _same_device(dev, o[k])
+    a = PackedConvBwdArgs()
+    a.dtype = _dtype_code(u); a.d_inner = hp; a.d_bc = gn
+    _plan_args(a, plan, total, dev)
+    a.u, a.u_row_stride = _rows2(u, cch, u.dtype, "u")
+    a.conv_w = _full(w, (cch, 4), torch.float32, "w").data_ptr()
+    a.conv_bias = _vp_of(_full(bias, (cch,), torch.float32, "bias"))
+    a.tail_in = _vp_of(_full(tail_in, (plan.n_slots, 3, cch), u.dtype, "tail_in"))
+    for t, k in ((dx, "dx"), (dB, "dB"), (dC, "dC")):
+        _f32(t, k)
+    a.dx = dx.data_ptr(); a.dB = dB.data_ptr(); a.dC = dC.data_ptr()
+    a.dtail_out = _vp_of(_full(dtail_out, (n, 3, cch), torch.float32, "dtail_out"))
+    a.du = o["du"].data_ptr(); a.dtail_in = _vp_of(o["dtail_in"]); a.dconv_w = o["dconv_w"].data_ptr()
+    a.dconv_bias = _vp_of(o["dconv_bias"])
+    workspace, a.workspace, a.workspace_bytes = _ws(workspace, lib().ssd_packed_conv_backward_workspace_size(n, total, cch), dev)
+    _launch(lib().ssd_packed_conv_backward, a, dev, stream)
+    return o
+
+
+def packed_scan_workspace(plan, H, P, N, dtype, G=1):
+    """Workspace of packed_scan_forward for this plan, these heads and this I/O dtype."""
+    code = SSD_BF16 if dtype == torch.bfloat16 else SSD_F32
+    with torch.cuda.device(plan.device):
+        n = lib().ssd_packed_scan_workspace_size(plan.nseq, plan.total, plan.max_seqlen, H, P, N, G, code)
+    return _bytes_on(plan.device, n)
+
+
+def _head_dims(x, B, C, H, G):
+    if H <= 0 or G <= 0 or x.dim() != 2 or B.dim() != 2 or x.shape[1] % H or B.shape[1] % G or B.shape != C.shape \
+            or x.shape[0] != B.shape[0]:
+        raise ValueError(f"x must be [total, H*P], B and C [total, G*N] (H={H}, G={G}); got "
+                         f"{tuple(x.shape)}, {tuple(B.shape)}, {tuple(C.shape)}")
+    return x.shape[1] // H, B.shape[1] // G
+
+
+def _rows3(t, H, P, dtype, name):
+    """(pointer, row stride) of rows of H*P elements given as [total, H, P] or [total, H*P]."""
+    if t.dim() == 3:
+        if t.shape[1:] != (H, P) or (P > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != P):
+            raise ValueError(f"{name} must be [total, {H}, {P}] with contiguous rows")
+        t = t.flatten(1)
+    return _rows2(t, H * P, dtype, name)
+
+
+def packed_scan_forward(x, B, C, dt, A, D=None, *, plan, H, G=1, h_in=None, h_out=None, y=None, workspace=None,
+                        stream=None, dt_bias=None, dt_softplus=False, dt_limit=None):
+    """The selective scan on each sequence of the plan; returns (y [total, H, P], h_out).
+
+    x: [total, H*P], B, C: [total, G*N] views (column slices of the conv output), dt: [total, H] float32,
+    A, D: [H] float32.  h_in, h_out: [n_slots, H, P, N] float32 or None; h_out may be h_in (updated in place);
+    slots that the batch does not name stay as they were.  dt_bias / dt_softplus / dt_limit as in scan_forward.
+    Rows of y that belong to no sequence stay as they were.
+    """
+    _cuda(x, B, C, dt, A, D, h_in, h_out, y, workspace, dt_bias)
+    dev = x.device
+    _same_device(dev, B, C, dt, A, D, h_in, h_out, y, dt_bias)
+    P, N = _head_dims(x, B, C, H, G)
+    total = x.shape[0]
+    if y is None:
+        y = torch.empty(total, H, P, dtype=x.dtype, device=dev)
+    a = PackedScanArgs()
+    a.dtype = _dtype_code(x); a.max_seqlen = plan.max_seqlen
+    a.H = H; a.P = P; a.N = N; a.G = G
+    _plan_args(a, plan, total, dev)
+    a.x, a.x_row_stride = _rows2(x, H * P, x.dtype, "x")
+    a.B, a.B_row_stride = _rows2(B, G * N, x.dtype, "B")
+    a.C, a.C_row_stride = _rows2(C, G * N, x.dtype, "C")
+    if y.shape[0] != total:
+        raise ValueError(f"y must have {total} rows")
+    a.y, a.y_row_stride = _rows3(y, H, P, x.dtype, "y")
+    a.dt = _full(dt, (total, H), torch.float32, "dt").data_ptr()
+    a.A = _full(A, (H,), torch.float32, "A").data_ptr()
+    a.D = _vp_of(_full(D, (H,), torch.float32, "D"))
+    _full(dt_bias, (H,), torch.float32, "dt_bias")
+    _set_dt(a, dt_bias, dt_softplus, dt_limit)
+    a.h_in = _vp_of(_full(h_in, (plan.n_slots, H, P, N), torch.float32, "h_in"))
+    a.h_out = _vp_of(_full(h_out, (plan.n_slots, H, P, N), torch.float32, "h_out"))
+    if workspace is None:
+        workspace = packed_scan_workspace(plan, H, P, N, x.dtype, G)
+    workspace, a.workspace, a.workspace_bytes = _ws(workspace, 0, dev)
+    _launch(lib().ssd_packed_scan_forward, a, dev, stream)
+    return y, h_out
+
+
+def packed_scan_backward_workspace(plan, H, P, N):
+    """Workspace of packed_scan_backward for this plan and these heads."""
+    return _bytes_on(plan.device, lib().ssd_packed_scan_backward_workspace_size(plan.nseq, plan.total, H, P, N))
+
+
+def packed_scan_backward(x, B, C, dt, A, D, dy, *, plan, H, G=1, h_in=None, dh_out=None, out=None, workspace=None, stream=None):
+    """Gradients through packed_scan_forward: dict dx [total, H, P], dB, dC [total, G, N], ddt [total, H], dA, dD [H],
+    dh_in [n, H, P, N] (float32).
+
+    x, B, C, dt, A, D, h_in as in the forward (dt the step that the scan used); dy: [total, H*P] or
+    [total, H, P]; dh_out: [n, H, P, N] float32 or None.  dh_out and dh_in go by sequence, h_in by slot.
+    ``out`` may hold outputs under the same keys; rows of no sequence stay as they were in them, and are
+    zero in those allocated here.
+    """
+    _cuda(x, B, C, dt, A, D, dy, h_in, dh_out, workspace)
+    dev = x.device
+    _same_device(dev, B, C, dt, A, D, dy, h_in, dh_out)
+    P, N = _head_dims(x, B, C, H, G)
+    total, n = x.shape[0], plan.nseq
+    o = dict(out or {})
+    for k, shp in (("dx", (total, H, P)), ("dB", (total, G, N)), ("dC", (total, G, N)), ("ddt", (total, H)), ("dA", (H,)),
+                   ("dD", (H,)), ("dh_in", (n, H, P, N))):
+        if k not in o:
+            o[k] = torch.zeros(shp, dtype=torch.float32, device=dev)
+        _full(o[k], shp, torch.float32, k)
+        _same_device(dev, o[k])
+    a = PackedScanBwdArgs()
+    a.dtype = _dtype_code(x); a.H = H; a.P = P; a.N = N; a.G = G
+    _plan_args(a, plan, total, dev)
+    a.x, a.x_row_stride = _rows2(x, H * P, x.dtype, "x")
+    a.B, a.B_row_stride = _rows2(B, G * N, x.dtype, "B")
+    a.C, a.C_row_stride = _rows2(C, G * N, x.dtype, "C")
+    if dy.shape[0] != total:
+        raise ValueError(f"dy must have {total} rows")
+    a.dy, a.dy_row_stride = _rows3(dy, H, P, x.dtype, "dy")
+    a.dt = _full(dt, (total, H), torch.float32, "dt").data_ptr()
+    a.A = _full(A, (H,), torch.float32, "A").data_ptr()
+    a.D = _vp_of(_full(D, (H,), torch.float32, "D"))
+    a.h_in = _vp_of(_full(h_in, (plan.n_slots, H, P, N), torch.float32, "h_in"))
+    a.dh_out = _vp_of(_full(dh_out, (n, H, P, N), torch.float32, "dh_out"))
+    a.dx = o["dx"].data_ptr(); a.dB = o["dB"].data_ptr(); a.dC = o["dC"].data_ptr(); a.ddt = o["ddt"].data_ptr()
+    a.dA = o["dA"].data_ptr(); a.dD = _vp_of(o["dD"]); a.dh_in = _vp_of(o["dh_in"])
+    if workspace is None:
+        workspace = packed_scan_backward_workspace(plan, H, P, N)
+    workspace, a.workspace, a.workspace_bytes = _ws(workspace, 0, dev)
+    _launch(lib().ssd_packed_scan_backward, a, dev, stream)
+    return o
+
+
+def decode_slots(u, conv_w, dt, A, D=None, *, slots, tail_in, h_in, H, P, N, G=1, conv_bias=None, tail_out=None, h_out=None,
+                 y=None, stream=None, dt_bias=None, dt_softplus=False, dt_limit=None):
+    """One token of b streams of a pool: u [b, C_ch], dt [b, H], slots [b] int32 (-1 = an empty row, whose y is
+    zero).  tail_in, tail_out: [n_slots, 3, C_ch], h_in, h_out: [n_slots, H, P, N] float32; without tail_out /
+    h_out they are updated in place.  Returns {"y": [b, H, P], "h_out", "tail_out"}."""
+    if tail_out is None:
+        tail_out = tail_in
+    if h_out is None:
+        h_out = h_in
+    _cuda(u, conv_w, dt, A, D, slots, tail_in, tail_out, h_in, h_out, conv_bias, y, dt_bias)
+    dev = u.device
+    _same_device(dev, conv_w, dt, A, D, slots, tail_in, tail_out, h_in, h_out, conv_bias, y, dt_bias)
+    b, cch = u.shape
+    if cch != H * P + 2 * G * N:
+        raise ValueError(f"u must hold H*P + 2*G*N = {H * P + 2 * G * N} channels, has {cch}")
+    n = h_in.shape[0]
+    if y is None:
+        y = torch.empty(b, H, P, dtype=u.dtype, device=dev)
+    a = DecodeSlotsArgs()
+    a.dtype = _dtype_code(u); a.b = b; a.n_slots = n; a.H = H; a.P = P; a.N = N; a.G = G
+    a.slots = _full(slots, (b,), torch.int32, "slots").data_ptr()
+    a.u, a.u_batch_stride = _rows2(u, cch, u.dtype, "u")
+    if y.shape[0] != b:
+        raise ValueError(f"y must have {b} rows")
+    a.y, a.y_batch_stride = _rows3(y, H, P, u.dtype, "y")
+    a.conv_w = _full(conv_w, (cch, 4), torch.float32, "conv_w").data_ptr()
+    a.conv_bias = _vp_of(_full(conv_bias, (cch,), torch.float32, "conv_bias"))
+    a.tail_in = _full(tail_in, (n, 3, cch), u.dtype, "tail_in").data_ptr()
+    a.tail_out = _full(tail_out, (n, 3, cch), u.dtype, "tail_out").data_ptr()
+    a.h_in = _full(h_in, (n, H, P, N), torch.float32, "h_in").data_ptr()
+    a.h_out = _full(h_out, (n, H, P, N), torch.float32, "h_out").data_ptr()
+    a.dt = _full(dt, (b, H), torch.float32, "dt").data_ptr()
+    a.A = _full(A, (H,), torch.float32, "A").data_ptr()
+    a.D = _vp_of(_full(D, (H,), torch.float32, "D"))
+    _full(dt_bias, (H,), torch.float32, "dt_bias")
+    _set_dt(a, dt_bias, dt_softplus, dt_limit)
+    _launch(lib().ssd_decode_slots, a, dev, stream)
+    return {"y": y, "h_out": h_out, "tail_out": tail_out}
+
+
+def _norm_rows(t, d, name):
+    """(pointer, row stride, rows) of a [..., d] tensor whose leading dimensions step through memory evenly."""
+    if t.shape[-1] != d:
+        raise ValueError(f"{name} must have {d} channels")
+    if t.dim() != 2:
+        t = t.view(-1, d) if t.is_contiguous() else t.flatten(0, -2)
+    p, rs = _rows2(t, d, t.dtype, name)
+    return p, rs, t.shape[0]
+
+
+def gated_rmsnorm_backward_workspace(rows, d, device=None, dtype=torch.bfloat16):
+    """Workspace of gated_rmsnorm_backward for this many rows of d channels."""
+    dev = torch.device(device or "cuda")
+    with torch.cuda.device(dev):
+        n = max(lib().ssd_gated_rmsnorm_backward_workspace_size(rows, d, c) for c in (SSD_F32, SSD_BF16))
+    return _bytes_on(dev, n)
+
+
+def gated_rmsnorm_backward(dout, y, z, weight, eps=1e-5, group_size=0, out=None, workspace=None, stream=None):
+    """Gradients through gated_rmsnorm: dict dy, dz (I/O dtype, shaped like y), dweight [d] float32.
+
+    dout, y, z: [..., d] with the same leading shape, rows of d contiguous channels.  ``out`` may hold outputs
+    under the same keys; dy may be dout or y, dz may be z (a row is read before it is written).
+    """
+    _cuda(dout, y, z, weight, workspace)
+    dev = y.device
+    _same_device(dev, dout, z, weight, workspace)
+    d = y.shape[-1]
+    if dout.shape != y.shape or z.shape != y.shape:
+        raise ValueError("dout, y and z must have the same shape")
+    if dout.dtype != y.dtype or z.dtype != y.dtype:
+        raise TypeError("dout, y and z must share the I/O dtype")
+    o = dict(out or {})
+    for k in ("dy", "dz"):
+        if k not in o:
+            o[k] = torch.empty(y.shape, dtype=y.dtype, device=dev)
+        if o[k].dtype != y.dtype:
+            raise TypeError(f"{k} must have y's dtype")
+        _shape(o[k], y.shape, k)
+    if "dweight" not in o:
+        o["dweight"] = torch.empty(d, dtype=torch.float32, device=dev)
+    _same_device(dev, *(o[k] for k in ("dy", "dz", "dweight")))
+    a = GatedRmsnormBwdArgs()
+    a.dtype = _dtype_code(y); a.d = d; a.group_size = int(group_size); a.eps = float(eps)
+    a.dout, a.dout_row_stride, a.rows = _norm_rows(dout, d, "dout")
+    a.y, a.y_row_stride, _ = _norm_rows(y, d, "y")
+    a.z, a.z_row_stride, _ = _norm_rows(z, d, "z")
+    a.dy, a.dy_row_stride, _ = _norm_rows(o["dy"], d, "dy")
+    a.dz, a.dz_row_stride, _ = _norm_rows(o["dz"], d, "dz")
+    a.weight = _full(weight, (d,), torch.float32, "weight").data_ptr()
+    a.dweight = _full(o["dweight"], (d,), torch.float32, "dweight").data_ptr()
+    if workspace is None:
+        workspace = gated_rmsnorm_backward_workspace(a.rows, d, dev)
+    workspace, a.workspace, a.workspace_bytes = _ws(workspace, 0, dev)
+    _launch(lib().ssd_gated_rmsnorm_backward, a, dev, stream)
+    return o

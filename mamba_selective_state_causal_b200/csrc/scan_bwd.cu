@@ -36,6 +36,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "packed.cuh"
 #include "ssd_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -46,6 +47,30 @@ constexpr int kQb = 64;           // tokens per backward chunk
 constexpr int kBwdThreads = 256;
 constexpr int kGradThreads = 512; // the gradient kernel: 16 warps per SM hide its load latency
 constexpr int kQ1 = kQb + 1;      // padded row of the chunk x chunk matrices
+
+// Chunks in use of a packed batch (0 when the plan is not of the call's sizes: nothing is done)
+__device__ __forceinline__ int bwd_packed_chunks(const BwdParams &p)
+{
+    PackedPlan v{};
+    v.hdr = p.hdr; v.nseq = p.nseq; v.total = p.L; v.max_len = -1;
+    return packed_n64(v, p.status);
+}
+
+// Rows t0 .. t0 + rows - 1 of chunk c; false for a chunk that a packed batch (kPacked) does not use
+template <bool kPacked>
+__device__ __forceinline__ bool bwd_chunk(const BwdParams &p, int c, int64_t &t0, int &rows)
+{
+    if (kPacked) {
+        if (c >= bwd_packed_chunks(p)) return false;
+        const int4 d = p.chunks[c];
+        t0 = d.x;
+        rows = d.y & kChunkRows;
+    } else {
+        t0 = (int64_t)c * kQb;
+        rows = (int)(p.L - t0 < kQb ? p.L - t0 : kQb);
+    }
+    return true;
+}
 
 template <typename T>
 __device__ __forceinline__ void load_rows(float *dst, int dst_rs, const T *src, int64_t src_rs, int rows_valid,
@@ -146,6 +171,7 @@ __device__ __forceinline__ void split8(uint4 v, float w, uint4 &hi, uint4 &lo)
     lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+template <bool kPacked>
 __global__ void __launch_bounds__(kSumTcThreads) bwd_chunk_summary_tc_kernel(BwdParams p)
 {
     extern __shared__ __align__(1024) uint8_t sst_raw[];
@@ -154,8 +180,9 @@ __global__ void __launch_bounds__(kSumTcThreads) bwd_chunk_summary_tc_kernel(Bwd
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int P = 64, N = 128;
     const int g = (int)((int64_t)h * p.G / p.H);
-    const int64_t t0 = (int64_t)c * kQb;
-    const int rows = (int)(p.L - t0 < kQb ? p.L - t0 : kQb);
+    int64_t t0;
+    int rows;
+    if (!bwd_chunk<kPacked>(p, c, t0, rows)) return;
     if (tid == 0) {
         mbar_init(&s.done, 1);
         fence_mbar_init();
@@ -258,15 +285,16 @@ __global__ void __launch_bounds__(kSumTcThreads) bwd_chunk_summary_tc_kernel(Bwd
 }
 
 // One CTA per (chunk, head, batch row): S_c, Gl_c and lam_c (CUDA cores, any shape).
-template <typename T>
+template <typename T, bool kPacked>
 __global__ void __launch_bounds__(kBwdThreads) bwd_chunk_summary_kernel(BwdParams p)
 {
     extern __shared__ float sm[];
     const int c = blockIdx.x, h = blockIdx.y, bi = blockIdx.z;
     const int P = p.P, N = p.N, P1 = P + 1, N1 = N + 1;
     const int g = (int)((int64_t)h * p.G / p.H);
-    const int64_t t0 = (int64_t)c * kQb;
-    const int rows = (int)(p.L - t0 < kQb ? p.L - t0 : kQb);
+    int64_t t0;
+    int rows;
+    if (!bwd_chunk<kPacked>(p, c, t0, rows)) return;
     float *xs = sm;                 // [Qb][P1]  dt_j e^{lam-cs_j} x_j
     float *gs = xs + kQb * P1;      // [Qb][P1]  e^{cs_t} dy_t
     float *bs = gs + kQb * P1;      // [Qb][N1]
@@ -336,6 +364,7 @@ constexpr int kChainPrefetch = 32; // CTAs ahead whose summaries the state chain
 // h = e^{lam_c} h + S_c (the slot held S_c).  Grid: (slices * cells, H, b);
 // a thread carries 4 consecutive state elements.
 // (three CTAs per SM: at one, set by its registers, too few loads were in flight)
+template <bool kPacked>
 __global__ void __launch_bounds__(kBwdThreads, 3) bwd_state_chain_kernel(BwdParams p)
 {
     const int64_t PN = (int64_t)p.P * p.N;
@@ -343,6 +372,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) bwd_state_chain_kernel(BwdPara
     const int sl = blockIdx.x % slices;
     const int64_t k = blockIdx.x / slices;
     const int h = blockIdx.y, bi = blockIdx.z;
+    if (kPacked && bwd_packed_chunks(p) == 0) return;
     if (threadIdx.x < kChainAhead) {
         // the chunk summaries of the CTA kChainPrefetch further on (one contiguous slice of up to
         // 4 KB per chunk), started into L2 with one bulk prefetch per chunk: CTAs run in order, so
@@ -351,8 +381,9 @@ __global__ void __launch_bounds__(kBwdThreads, 3) bwd_state_chain_kernel(BwdPara
         if (ahead < (int64_t)gridDim.x * p.H * p.b) {
             const int64_t xa = ahead % gridDim.x, hua = ahead / gridDim.x;
             const int64_t e0 = (xa % slices) * 4 * kBwdThreads, ka = xa / slices;
-            const int64_t ca = ka * p.cell_chunks + threadIdx.x;
-            const int64_t ce = p.nch < (ka + 1) * p.cell_chunks ? p.nch : (ka + 1) * p.cell_chunks;
+            const int64_t ca = (kPacked ? p.seqs[ka].c64 : ka * p.cell_chunks) + threadIdx.x;
+            const int64_t ce = kPacked ? p.seqs[ka].c64 + p.seqs[ka].n64
+                                        : (p.nch < (ka + 1) * p.cell_chunks ? p.nch : (ka + 1) * p.cell_chunks);
             if (ca < ce) {
                 const int64_t n = PN - e0 < 4 * kBwdThreads ? PN - e0 : 4 * kBwdThreads;
                 const float *src = p.ws_h + (hua * p.nch + ca) * PN + e0;
@@ -364,13 +395,17 @@ __global__ void __launch_bounds__(kBwdThreads, 3) bwd_state_chain_kernel(BwdPara
     if (e >= PN) return;
     const int64_t hu = (int64_t)bi * p.H + h;
     float4 hv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (k == 0) {
+    if (kPacked) {
+        const PackedSeq q = p.seqs[k];
+        if (p.h0 && q.resume && q.slot >= 0)
+            hv = *reinterpret_cast<const float4 *>(p.h0 + ((int64_t)q.slot * p.H + h) * PN + e);
+    } else if (k == 0) {
         if (p.h0) hv = *reinterpret_cast<const float4 *>(p.h0 + hu * PN + e);
     } else {
         hv = *reinterpret_cast<const float4 *>(p.h_ckpt + (((int64_t)bi * p.n_ckpt + (k - 1)) * p.H + h) * PN + e);
     }
-    const int64_t c0 = k * p.cell_chunks;
-    const int64_t c1 = p.nch < c0 + p.cell_chunks ? p.nch : c0 + p.cell_chunks;
+    const int64_t c0 = kPacked ? p.seqs[k].c64 : k * p.cell_chunks;
+    const int64_t c1 = kPacked ? c0 + p.seqs[k].n64 : (p.nch < c0 + p.cell_chunks ? p.nch : c0 + p.cell_chunks);
     float *base = p.ws_h + hu * p.nch * PN + e;
     const float *lam = p.ws_lam + hu * p.nch;
     for (int64_t cb = c0; cb < c1; cb += kChainAhead) {
@@ -395,15 +430,24 @@ __global__ void __launch_bounds__(kBwdThreads, 3) bwd_state_chain_kernel(BwdPara
 // Adjoint arriving at the last token of every chunk, over the whole
 // sequence, last chunk first: G = dh_final; for c = nch-1 .. 0: slot c := G,
 // then G = e^{lam_c} G + Gl_c (the slot held Gl_c).  dh0 = G at the end.
-// Grid: (slices, H, b).
+// Grid: (slices, H, b), or (slices * sequences, H, 1) of a packed batch.
+template <bool kPacked>
 __global__ void __launch_bounds__(kBwdThreads) bwd_adjoint_chain_kernel(BwdParams p)
 {
     const int64_t PN = (int64_t)p.P * p.N;
-    const int sl = blockIdx.x, h = blockIdx.y, bi = blockIdx.z;
+    const int slices = (int)((PN + 4 * kBwdThreads - 1) / (4 * kBwdThreads));
+    const int sl = kPacked ? blockIdx.x % slices : blockIdx.x, h = blockIdx.y, bi = blockIdx.z;
     const int64_t e = (int64_t)sl * 4 * kBwdThreads + 4 * threadIdx.x;
+    if (kPacked && bwd_packed_chunks(p) == 0) return;
     if (e >= PN) return;
     const int64_t hu = (int64_t)bi * p.H + h;
-    float4 gv = p.dh_final ? *reinterpret_cast<const float4 *>(p.dh_final + hu * PN + e)
+    // the chunks lo .. hi - 1 of the whole sequence, or of packed sequence k, whose states go by sequence
+    const int64_t k = blockIdx.x / slices;
+    const int64_t lo = kPacked ? p.seqs[k].c64 : 0;
+    const int64_t hi = kPacked ? lo + p.seqs[k].n64 : p.nch;
+    if (kPacked && hi == lo) return;      // a refused sequence
+    const int64_t su = kPacked ? k * p.H + h : hu;
+    float4 gv = p.dh_final ? *reinterpret_cast<const float4 *>(p.dh_final + su * PN + e)
                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float *base = p.ws_g + hu * p.nch * PN + e;
     const float *lam = p.ws_lam + hu * p.nch;
@@ -415,7 +459,7 @@ __global__ void __launch_bounds__(kBwdThreads) bwd_adjoint_chain_kernel(BwdParam
     auto load = [&](int64_t c, float4 (&sv)[kHalf], float (&lv)[kHalf]) {
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) {
-            const bool in = c - i >= 0;
+            const bool in = c - i >= lo;
             sv[i] = in ? *reinterpret_cast<const float4 *>(base + (c - i) * PN) : make_float4(0.f, 0.f, 0.f, 0.f);
             lv[i] = in ? lam[c - i] : 0.0f;
         }
@@ -423,33 +467,36 @@ __global__ void __launch_bounds__(kBwdThreads) bwd_adjoint_chain_kernel(BwdParam
     auto steps = [&](int64_t c, const float4 (&sv)[kHalf], const float (&lv)[kHalf]) {
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) {
-            if (c - i >= 0) {
+            if (c - i >= lo) {
                 *reinterpret_cast<float4 *>(base + (c - i) * PN) = gv;
                 gv = f4_fma(expf(lv[i]), gv, sv[i]);
             }
         }
     };
-    load(p.nch - 1, sa, la);
-    for (int64_t cb = p.nch - 1; cb >= 0; cb -= 2 * kHalf) {
+    load(hi - 1, sa, la);
+    for (int64_t cb = hi - 1; cb >= lo; cb -= 2 * kHalf) {
         load(cb - kHalf, sb, lb);
         steps(cb, sa, la);
         load(cb - 2 * kHalf, sa, la);
         steps(cb - kHalf, sb, lb);
     }
-    if (p.dh0) *reinterpret_cast<float4 *>(p.dh0 + hu * PN + e) = gv;
+    // a packed sequence that does not resume has no state to pass it on to
+    if (kPacked && !(p.h0 && p.seqs[k].resume)) gv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (p.dh0) *reinterpret_cast<float4 *>(p.dh0 + su * PN + e) = gv;
 }
 
 // ---------------------------------------------------------------- gradients
 // One CTA per (chunk, head, batch row).
-template <typename T>
+template <typename T, bool kPacked>
 __global__ void __launch_bounds__(kGradThreads) bwd_chunk_grad_kernel(BwdParams p)
 {
     extern __shared__ float sm[];
     const int c = blockIdx.x, h = blockIdx.y, bi = blockIdx.z;
     const int P = p.P, N = p.N, P1 = P + 1, N1 = N + 1;
     const int g = (int)((int64_t)h * p.G / p.H);
-    const int64_t t0 = (int64_t)c * kQb;
-    const int rows = (int)(p.L - t0 < kQb ? p.L - t0 : kQb);
+    int64_t t0;
+    int rows;
+    if (!bwd_chunk<kPacked>(p, c, t0, rows)) return;
     const int tid = threadIdx.x;
     float *xs = sm;                  // [Qb][P1]
     float *gs = xs + kQb * P1;       // [Qb][P1] dy
@@ -844,6 +891,7 @@ __device__ __forceinline__ void store_pieces3(uint8_t (&dst)[3][2 * kSumBox], co
 // launch at 32 and 48, 0.509 at 74, 0.512 at 110, no gain at a whole wave (296), 0.535 without
 constexpr int kGradAhead = 32;
 
+template <bool kPacked>
 __global__ void __launch_bounds__(kGradTcThreads, 2) bwd_chunk_grad_tc_kernel(BwdParams p)
 {
     extern __shared__ __align__(1024) uint8_t sgt_raw[];
@@ -852,8 +900,9 @@ __global__ void __launch_bounds__(kGradTcThreads, 2) bwd_chunk_grad_tc_kernel(Bw
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int P = 64, N = 128;
     const int g = (int)((int64_t)h * p.G / p.H);
-    const int64_t t0 = (int64_t)c * kQb;
-    const int rows = (int)(p.L - t0 < kQb ? p.L - t0 : kQb);
+    int64_t t0;
+    int rows;
+    if (!bwd_chunk<kPacked>(p, c, t0, rows)) return;
     const int64_t unit = ((int64_t)bi * p.H + h) * p.nch + c;
     const float Ah = p.A[h];
     const float Dh = p.D ? p.D[h] : 0.0f;
@@ -1312,13 +1361,39 @@ __global__ void bwd_group_sum_kernel(BwdParams p)
     }
 }
 
+// the same for a packed batch, chunk by chunk (rows of no sequence stay as they were)
+__global__ void __launch_bounds__(256) bwd_packed_group_sum_kernel(BwdParams p)
+{
+    int64_t t0;
+    int rows;
+    if (!bwd_chunk<true>(p, blockIdx.x, t0, rows)) return;
+    const int hpg = p.H / p.G, nq = p.N >> 2;
+    for (int i = threadIdx.x + blockDim.x * blockIdx.y; i < rows * p.G * nq; i += blockDim.x * gridDim.y) {
+        const int q = i % nq, g = i / nq % p.G;
+        const int64_t t = t0 + i / (nq * p.G);
+        const float4 *sb = reinterpret_cast<const float4 *>(p.ws_dBh + (t * p.H + (int64_t)g * hpg) * p.N) + q;
+        const float4 *sc = reinterpret_cast<const float4 *>(p.ws_dCh + (t * p.H + (int64_t)g * hpg) * p.N) + q;
+        float4 ab = make_float4(0.f, 0.f, 0.f, 0.f), ac = ab;
+#pragma unroll 4
+        for (int k = 0; k < hpg; ++k) {
+            const float4 b = sb[(int64_t)k * nq], c = sc[(int64_t)k * nq];
+            ab.x += b.x; ab.y += b.y; ab.z += b.z; ab.w += b.w;
+            ac.x += c.x; ac.y += c.y; ac.z += c.z; ac.w += c.w;
+        }
+        reinterpret_cast<float4 *>(p.dB + (t * p.G + g) * p.N)[q] = ab;
+        reinterpret_cast<float4 *>(p.dC + (t * p.G + g) * p.N)[q] = ac;
+    }
+}
+
 // dA[h], dD[h]: sums of the per-(batch row, chunk) partials, in a fixed order.
+template <bool kPacked>
 __global__ void __launch_bounds__(kBwdThreads) bwd_param_sum_kernel(BwdParams p)
 {
     __shared__ float sa[kBwdThreads], sd[kBwdThreads];
     const int h = blockIdx.x;
     float a = 0.0f, d = 0.0f;
-    for (int64_t i = threadIdx.x; i < (int64_t)p.b * p.nch; i += blockDim.x) {
+    const int64_t count = kPacked ? bwd_packed_chunks(p) : (int64_t)p.b * p.nch;
+    for (int64_t i = threadIdx.x; i < count; i += blockDim.x) {
         const int64_t bi = i / p.nch, c = i % p.nch;
         const int64_t unit = (bi * p.H + h) * p.nch + c;
         a += p.ws_pA[unit];
@@ -1357,50 +1432,51 @@ int smem_optin()
     return v;
 }
 
-template <typename T>
+template <typename T, bool kPacked>
 int launch_bwd_t(BwdParams p, cudaStream_t st)
 {
     const size_t s1 = summary_smem(p.P, p.N);
     p.stage_adjoint = grad_smem(p.P, p.N, true) <= (size_t)smem_optin() ? 1 : 0;
     const size_t s2 = grad_smem(p.P, p.N, p.stage_adjoint != 0);
-    if (cudaFuncSetAttribute(bwd_chunk_summary_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1) !=
+    if (cudaFuncSetAttribute(bwd_chunk_summary_kernel<T, kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1) !=
             cudaSuccess ||
-        cudaFuncSetAttribute(bwd_chunk_grad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2) !=
+        cudaFuncSetAttribute(bwd_chunk_grad_kernel<T, kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2) !=
             cudaSuccess)
         return 7;
     const dim3 grid((unsigned)p.nch, (unsigned)p.H, (unsigned)p.b);
     // bf16 inputs at P = 64, N = 128: the summaries and the gradients on the tensor cores
     const bool tc_summary = std::is_same<T, __nv_bfloat16>::value && p.P == 64 && p.N == 128;
     const size_t s_tc = sizeof(SmemSumTc) + 1024, s_gt = sizeof(SmemGradTc) + 1024;
-    if (tc_summary && (cudaFuncSetAttribute(bwd_chunk_summary_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (tc_summary && (cudaFuncSetAttribute(bwd_chunk_summary_tc_kernel<kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             (int)s_tc) != cudaSuccess ||
-                       cudaFuncSetAttribute(bwd_chunk_grad_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       cudaFuncSetAttribute(bwd_chunk_grad_tc_kernel<kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             (int)s_gt) != cudaSuccess ||
-                       cudaFuncSetAttribute(bwd_chunk_grad_tc_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                       cudaFuncSetAttribute(bwd_chunk_grad_tc_kernel<kPacked>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                             (int)cudaSharedmemCarveoutMaxShared) != cudaSuccess))
         return 7;
     prof_begin(st, kKBwdSummary);
-    if (tc_summary) bwd_chunk_summary_tc_kernel<<<grid, kSumTcThreads, s_tc, st>>>(p);
-    else bwd_chunk_summary_kernel<T><<<grid, kBwdThreads, s1, st>>>(p);
+    if (tc_summary) bwd_chunk_summary_tc_kernel<kPacked><<<grid, kSumTcThreads, s_tc, st>>>(p);
+    else bwd_chunk_summary_kernel<T, kPacked><<<grid, kBwdThreads, s1, st>>>(p);
     prof_end(st, kKBwdSummary);
     const int64_t PN = (int64_t)p.P * p.N;
     const unsigned slices = (unsigned)((PN + 4 * kBwdThreads - 1) / (4 * kBwdThreads));
-    const int64_t cells = (p.nch + p.cell_chunks - 1) / p.cell_chunks;
+    const int64_t cells = kPacked ? p.nseq : (p.nch + p.cell_chunks - 1) / p.cell_chunks;
     prof_begin(st, kKBwdChain);
-    bwd_state_chain_kernel<<<dim3(slices * (unsigned)cells, (unsigned)p.H, (unsigned)p.b), kBwdThreads, 0, st>>>(p);
+    bwd_state_chain_kernel<kPacked><<<dim3(slices * (unsigned)cells, (unsigned)p.H, (unsigned)p.b), kBwdThreads, 0, st>>>(p);
     prof_end(st, kKBwdChain);
     prof_begin(st, kKBwdAdjoint);
-    bwd_adjoint_chain_kernel<<<dim3(slices, (unsigned)p.H, (unsigned)p.b), kBwdThreads, 0, st>>>(p);
+    bwd_adjoint_chain_kernel<kPacked><<<dim3(slices * (unsigned)(kPacked ? p.nseq : 1), (unsigned)p.H, (unsigned)p.b), kBwdThreads, 0, st>>>(p);
     prof_end(st, kKBwdAdjoint);
     prof_begin(st, kKBwdGrad);
-    if (tc_summary) bwd_chunk_grad_tc_kernel<<<grid, kGradTcThreads, s_gt, st>>>(p);
-    else bwd_chunk_grad_kernel<T><<<grid, kGradThreads, s2, st>>>(p);
+    if (tc_summary) bwd_chunk_grad_tc_kernel<kPacked><<<grid, kGradTcThreads, s_gt, st>>>(p);
+    else bwd_chunk_grad_kernel<T, kPacked><<<grid, kGradThreads, s2, st>>>(p);
     prof_end(st, kKBwdGrad);
     prof_begin(st, kKBwdReduce);
     const int64_t total = (int64_t)p.b * p.L * p.G * p.N;
     const unsigned blocks = (unsigned)std::min<int64_t>((total + 255) / 256, 148 * 16);
-    bwd_group_sum_kernel<<<blocks, 256, 0, st>>>(p);
-    bwd_param_sum_kernel<<<(unsigned)p.H, kBwdThreads, 0, st>>>(p);
+    if (kPacked) bwd_packed_group_sum_kernel<<<dim3((unsigned)p.nch, 4), 256, 0, st>>>(p);
+    else bwd_group_sum_kernel<<<blocks, 256, 0, st>>>(p);
+    bwd_param_sum_kernel<kPacked><<<(unsigned)p.H, kBwdThreads, 0, st>>>(p);
     prof_end(st, kKBwdReduce);
     return cudaGetLastError() == cudaSuccess ? 0 : 7;
 }
@@ -1411,7 +1487,8 @@ size_t bwd_grad_smem_bytes(int P, int N) { return grad_smem(P, N, false); }
 
 int launch_scan_backward(const BwdParams &p, int dtype, cudaStream_t st)
 {
-    return dtype == 1 ? launch_bwd_t<__nv_bfloat16>(p, st) : launch_bwd_t<float>(p, st);
+    if (p.chunks) return dtype == 1 ? launch_bwd_t<__nv_bfloat16, true>(p, st) : launch_bwd_t<float, true>(p, st);
+    return dtype == 1 ? launch_bwd_t<__nv_bfloat16, false>(p, st) : launch_bwd_t<float, false>(p, st);
 }
 
 }  // namespace ssd

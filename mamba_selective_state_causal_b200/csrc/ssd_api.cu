@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "../../include/ssd.h"
+#include "api_util.cuh"
 #include "ssd_common.cuh"
 
 namespace {
@@ -82,6 +83,13 @@ const EnvHooks &env_hooks()
         return e;
     }();
     return h;
+}
+
+int64_t take_drop_unit()
+{
+    static std::atomic<bool> used{false};
+    const EnvHooks &hooks = env_hooks();
+    return (hooks.test_drop_unit >= 0 && !used.exchange(true)) ? hooks.test_drop_unit : -1;
 }
 
 size_t elem_size(int dtype) { return dtype == SSD_BF16 ? 2 : 4; }
@@ -260,8 +268,7 @@ int scan_impl(const ssd_scan_args *a, cudaStream_t st, const FusedConv *fc = nul
     }
     const EnvHooks &hooks = env_hooks();
     p.wait_limit_ns = hooks.wait_limit_ns;
-    static std::atomic<bool> drop_used{false};
-    p.test_drop_unit = (hooks.test_drop_unit >= 0 && !drop_used.exchange(true)) ? hooks.test_drop_unit : -1;
+    p.test_drop_unit = take_drop_unit();
     // SSD_SCAN_PATH=generic forces the CUDA-core kernels (used to cross-check the paths)
     const bool force_generic = hooks.force_generic;
     rc = 6;
@@ -519,7 +526,9 @@ int conv_impl(const void *u, int64_t ubs, int64_t urs, const float *w, const flo
 const char *const kKernelNames[ssd::kKCount] = {
     "conv1d_silu", "conv_tail", "stripe_state_tc", "stripe_chain", "chunk_output_tc",
     "stripe_state_generic", "chunk_output_generic", "decode_step", "bwd_chunk_summary", "bwd_state_chain",
-    "bwd_chunk_grad", "bwd_reduce", "gated_rmsnorm", "conv_cells", "conv_ckpt", "conv_bwd", "bwd_adjoint_chain"};
+    "bwd_chunk_grad", "bwd_reduce", "gated_rmsnorm", "conv_cells", "conv_ckpt", "conv_bwd", "bwd_adjoint_chain",
+    "packed_plan", "packed_conv", "packed_conv_bwd", "packed_state", "packed_chain", "packed_output", "decode_slots",
+    "gated_rmsnorm_bwd"};
 
 struct ProfRecord {
     int id;
@@ -565,6 +574,22 @@ void prof_end(cudaStream_t st, int id)
     g_prof.recs.push_back({id, g_prof.pending, e});
     g_prof.pending = nullptr;
 }
+
+int api_fail(int code, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return fail(code, "%s", buf);
+}
+int api_ok() { return ok(); }
+unsigned int *api_status_ptr() { return status_ptr(); }
+int api_sm_count() { return sm_count(); }
+uint64_t api_wait_limit_ns() { return env_hooks().wait_limit_ns; }
+bool api_force_generic() { return env_hooks().force_generic; }
+int64_t api_take_drop_unit() { return take_drop_unit(); }
 }  // namespace ssd
 
 namespace {
@@ -861,13 +886,17 @@ int ssd_sync_status(ssd_stream_t stream)
     if (v != 0) {
         const unsigned int zero = 0;
         cudaMemcpy(sp, &zero, sizeof zero, cudaMemcpyHostToDevice);
-        return fail((int)v, "device status %u (a bounded wait gave up)", v);
+        const unsigned int code = v & ~(unsigned int)ssd::kDevIndex;
+        if (code == 0)
+            return fail(SSD_ERR_INDEX, "a packed call was given a sequence offset or a slot out of range, a slot twice, "
+                        "or a plan of other sizes: what it named was left out");
+        return fail((int)code, "device status %u (a bounded wait gave up)", code);
     }
     return ok();
 }
 
 const char *ssd_last_error_string(void) { return g_last_error.c_str(); }
 
-int ssd_version(void) { return 300; }   // 0.3.0: layer backward, conv buffers at the checkpoints
+int ssd_version(void) { return 400; }   // 0.4.0: packed sequences, slot decode, the gated norm's gradient
 
 }  // extern "C"

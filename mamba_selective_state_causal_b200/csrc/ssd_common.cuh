@@ -8,7 +8,8 @@
 namespace ssd {
 
 // Device status codes latched by kernels (mirrors ssd_status in include/ssd.h).
-enum : unsigned int { kDevOk = 0u, kDevUnsupported = 6u, kDevTimeout = 8u };
+enum : unsigned int { kDevOk = 0u, kDevUnsupported = 6u, kDevTimeout = 8u,
+                     kDevIndex = 64u /* an offset or slot was refused; a bit of its own beside the codes */ };
 
 // Everything a scan kernel needs, passed by value.
 struct ScanParams {
@@ -97,6 +98,9 @@ struct DecodeParams {
     float dt_min, dt_max;
 };
 
+struct PackedHeader;
+struct PackedSeq;
+
 // The backward pass of the scan (scan_bwd.cu).
 struct BwdParams {
     int b;
@@ -128,6 +132,13 @@ struct BwdParams {
     int stage_adjoint;      // set by the launcher: copy Gam and h_prev into shared memory
     unsigned int *status;   // device status word (a bounded wait that gave up)
     uint64_t wait_limit_ns; // bound of every device-side wait
+    // packed sequences (packed.cuh), or NULL: b = 1, L = the rows, nch = room for chunks; chunk c is
+    // chunks[c], the sequences take the place of the cells, h0 is a pool of slots, dh_final and dh0
+    // go by sequence
+    const int4 *chunks;
+    const PackedSeq *seqs;
+    const PackedHeader *hdr;
+    int nseq;
 };
 
 // The conv part of the layer's backward pass (conv1d_silu.cu, layer_bwd.cu): the
@@ -208,7 +219,8 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 enum KernelId : int {
     kKConv = 0, kKConvTail, kKStateTc, kKChain, kKOutputTc, kKStateGeneric, kKOutputGeneric, kKDecode,
     kKBwdSummary, kKBwdChain, kKBwdGrad, kKBwdReduce, kKGatedNorm, kKConvCells, kKConvCkpt, kKConvBwd,
-    kKBwdAdjoint, kKCount
+    kKBwdAdjoint, kKPackedPlan, kKPackedConv, kKPackedConvBwd, kKPackedState, kKPackedChain, kKPackedOutput, kKSlotDecode,
+    kKGatedNormBwd, kKCount
 };
 void prof_begin(cudaStream_t st, int id);
 void prof_end(cudaStream_t st, int id);
