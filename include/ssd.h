@@ -687,7 +687,7 @@ typedef struct ssd_gated_rmsnorm_bwd_args {
 } ssd_gated_rmsnorm_bwd_args;
 
 SSD_API int ssd_gated_rmsnorm_backward(const ssd_gated_rmsnorm_bwd_args *args, ssd_stream_t stream);
-SSD_API size_t ssd_gated_rmsnorm_backward_workspace_size(int64_t rows, int d, int dtype);
+SSD_API size_t ssd_gated_rmsnorm_backward_workspace_size(int64_t rows, int d);
 
 /*
  * ssd_scan_forward_static_scratch -- ssd_scan_forward for callers that cannot

@@ -210,7 +210,7 @@ def lib():
                            ("ssd_packed_conv_backward_workspace_size", [ctypes.c_int, _i64, ctypes.c_int]),
                            ("ssd_packed_scan_workspace_size", [ctypes.c_int, _i64, _i64] + [ctypes.c_int] * 5),
                            ("ssd_packed_scan_backward_workspace_size", [ctypes.c_int, _i64] + [ctypes.c_int] * 3),
-                           ("ssd_gated_rmsnorm_backward_workspace_size", [_i64, ctypes.c_int, ctypes.c_int])):
+                           ("ssd_gated_rmsnorm_backward_workspace_size", [_i64, ctypes.c_int])):
             getattr(L, name).argtypes = args
             getattr(L, name).restype = ctypes.c_size_t
         L.ssd_sync_status.argtypes = [_vp]
@@ -579,59 +579,92 @@ def gated_rmsnorm(y, z, weight, eps=1e-5, group_size=0, out=None, stream=None):
 
 
 # ---------------------------------------------------------------- packed sequences and slots
-def _same_device(dev, *ts):
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+# The checks below run on every call of a decoding loop: each tensor is looked at once.
+def _device(t):
+    """The CUDA device that a call's first tensor, and hence all of them, must be on."""
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("all tensors must be CUDA tensors")
+    return dev
 
 
-def _shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
+def _ptr_of(t, shape, dtype, dev, name):
+    """The data pointer of a contiguous tensor of this shape and type on `dev` (None for None)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        _refuse(t, shape, dtype, dev, name)
+    return t.data_ptr()
+
+
+def _refuse(t, shape, dtype, dev, name):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    if t.device != dev:
+        raise ValueError(f"all tensors must be on {dev}, {name} is on {t.device}")
+    raise TypeError(f"{name} must be a contiguous {dtype} tensor")
 
 
-def _full(t, shape, dtype, name):
-    """Check for a contiguous tensor of this shape and type (or None)."""
-    if t is not None:
-        _shape(t, shape, name)
-        if t.dtype != dtype or not t.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous {dtype} tensor")
-    return t
-
-
-def _rows2(t, width, dtype, name):
-    """Rows of `width` elements side by side in memory: (data pointer, row stride) of a [rows, width] view."""
-    if t.dim() != 2 or t.shape[1] != width:
-        raise ValueError(f"{name} must be [rows, {width}], got {tuple(t.shape)}")
-    if t.dtype != dtype:
+def _rows2(t, rows, width, dtype, dev, name):
+    """(data pointer, row stride) of a [rows, width] view whose rows are contiguous."""
+    if t.shape != (rows, width):
+        raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if width > 1 and t.stride(1) != 1:
+    if t.device != dev:
+        raise ValueError(f"all tensors must be on {dev}, {name} is on {t.device}")
+    rs, cs = t.stride()
+    if cs != 1 and width > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     # a tensor of one row (or none) may carry any stride
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+    return t.data_ptr(), rs if rows > 1 else width
+
+
+def _rows3(t, rows, H, P, dtype, dev, name):
+    """(pointer, row stride) of rows of H*P elements given as [rows, H, P] or [rows, H*P]."""
+    if t.dim() != 3:
+        return _rows2(t, rows, H * P, dtype, dev, name)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"all tensors must be on {dev}, {name} is on {t.device}")
+    rs, hs, ps = t.stride()
+    if t.shape != (rows, H, P) or (P > 1 and ps != 1) or (H > 1 and hs != P):
+        raise ValueError(f"{name} must be [{rows}, {H}, {P}] with contiguous rows, got {tuple(t.shape)}")
+    return t.data_ptr(), rs if rows > 1 else H * P
+
+
+# the current stream's handle without making a Stream object of it (2 us of a decoding step's 14 on the host)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _launch(fn, a, dev, stream):
     """Call a C entry point with `dev` current, on `stream` or the device's current stream."""
     if dev.index is not None and dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            s = stream or torch.cuda.current_stream(dev)
-            _check(fn(ctypes.byref(a), s.cuda_stream))
-        return
-    s = stream or torch.cuda.current_stream(dev)
-    _check(fn(ctypes.byref(a), s.cuda_stream))
+            return _launch(fn, a, dev, stream)
+    _check(fn(ctypes.byref(a), stream.cuda_stream if stream is not None else _raw_stream(dev.index or 0)))
 
 
 def _bytes_on(dev, n):
     return torch.empty(max(int(n), 1), dtype=torch.uint8, device=dev)
 
 
-def _ws(workspace, need, dev):
-    if workspace is None:
-        workspace = _bytes_on(dev, need)
-    _same_device(dev, workspace)
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+def _set_ws(a, workspace, dev):
+    if workspace.device != dev:
+        raise ValueError(f"all tensors must be on {dev}, workspace is on {workspace.device}")
+    a.workspace = workspace.data_ptr()
+    a.workspace_bytes = workspace.nbytes
+
+
+def _outputs(out, shapes, dev):
+    """The float32 outputs of these shapes: those given in `out`, the others allocated (zero); with their pointers."""
+    o, ptr = dict(out or {}), {}
+    for k, shp in shapes:
+        if k not in o:
+            o[k] = torch.zeros(shp, dtype=torch.float32, device=dev)
+        ptr[k] = _ptr_of(o[k], shp, torch.float32, dev, k)
+    return o, ptr
 
 
 class PackedPlan:
@@ -651,22 +684,22 @@ def packed_plan(cu_seqlens, total, *, slots=None, resume=None, n_slots=0, max_se
     bound of the lengths (0: total).  buf: the plan's memory (uint8, lib().ssd_packed_plan_size(n, total)
     bytes), to make it again in the same place (under a captured graph).
     """
-    _cuda(cu_seqlens, slots, resume, buf)
-    dev = cu_seqlens.device
-    _same_device(dev, slots, resume, buf)
+    dev = _device(cu_seqlens)
     n = cu_seqlens.numel() - 1
     if n < 0:
         raise ValueError("cu_seqlens needs at least one entry")
-    _full(cu_seqlens, (n + 1,), torch.int32, "cu_seqlens")
-    _full(slots, (n,), torch.int32, "slots")
-    _full(resume, (n,), torch.int32, "resume")
     if slots is not None and n_slots <= 0 and n > 0:
         raise ValueError("n_slots is needed with slots")
     a = PackedPlanArgs()
-    a.nseq = n; a.total = total
-    a.cu_seqlens = cu_seqlens.data_ptr(); a.slots = _vp_of(slots); a.resume = _vp_of(resume)
-    a.n_slots = n_slots; a.max_seqlen = max_seqlen
-    buf, a.plan, a.plan_bytes = _ws(buf, lib().ssd_packed_plan_size(n, total), dev)
+    a.nseq = n; a.total = total; a.n_slots = n_slots; a.max_seqlen = max_seqlen
+    a.cu_seqlens = _ptr_of(cu_seqlens, (n + 1,), torch.int32, dev, "cu_seqlens")
+    a.slots = _ptr_of(slots, (n,), torch.int32, dev, "slots")
+    a.resume = _ptr_of(resume, (n,), torch.int32, dev, "resume")
+    if buf is None:
+        buf = _bytes_on(dev, lib().ssd_packed_plan_size(n, total))
+    if buf.device != dev:
+        raise ValueError(f"all tensors must be on {dev}, buf is on {buf.device}")
+    a.plan = buf.data_ptr(); a.plan_bytes = buf.nbytes
     _launch(lib().ssd_packed_plan, a, dev, stream)
     return PackedPlan(buf, n, int(total), n_slots if slots is not None else max(n_slots, n), int(max_seqlen), slots is not None)
 
@@ -676,7 +709,7 @@ def _plan_args(a, plan, rows, dev):
         raise ValueError(f"the plan is for {plan.total} rows, the tensors have {rows}")
     if plan.device != dev:
         raise ValueError(f"the plan is on {plan.device}, the tensors on {dev}")
-    a.nseq = plan.nseq; a.total = plan.total; a.plan = plan.buf.data_ptr()
+    a.nseq = plan.nseq; a.total = rows; a.plan = plan.buf.data_ptr()
 
 
 def packed_conv_forward(u, w, plan, bias=None, tail_in=None, tail_out=None, v=None, stream=None):
@@ -685,22 +718,20 @@ def packed_conv_forward(u, w, plan, bias=None, tail_in=None, tail_out=None, v=No
     u: [total, C_ch] (a view with any row stride of whole 16 bytes); tail_in, tail_out: [n_slots, 3, C_ch] or
     None, tail_out may be tail_in.  Rows of v that belong to no sequence stay as they were.
     """
-    _cuda(u, w, bias, tail_in, tail_out, v)
-    dev = u.device
-    _same_device(dev, w, bias, tail_in, tail_out, v)
+    dev = _device(u)
     total, cch = u.shape
+    dt = u.dtype
     if v is None:
-        v = torch.empty(total, cch, dtype=u.dtype, device=dev)
+        v = torch.empty(total, cch, dtype=dt, device=dev)
     a = PackedConvArgs()
     a.dtype = _dtype_code(u); a.C_ch = cch
     _plan_args(a, plan, total, dev)
-    a.u, a.u_row_stride = _rows2(u, cch, u.dtype, "u")
-    _shape(v, (total, cch), "v")
-    a.v, a.v_row_stride = _rows2(v, cch, u.dtype, "v")
-    a.conv_w = _full(w, (cch, 4), torch.float32, "w").data_ptr()
-    a.conv_bias = _vp_of(_full(bias, (cch,), torch.float32, "bias"))
-    a.tail_in = _vp_of(_full(tail_in, (plan.n_slots, 3, cch), u.dtype, "tail_in"))
-    a.tail_out = _vp_of(_full(tail_out, (plan.n_slots, 3, cch), u.dtype, "tail_out"))
+    a.u, a.u_row_stride = _rows2(u, total, cch, dt, dev, "u")
+    a.v, a.v_row_stride = _rows2(v, total, cch, dt, dev, "v")
+    a.conv_w = _ptr_of(w, (cch, 4), torch.float32, dev, "w")
+    a.conv_bias = _ptr_of(bias, (cch,), torch.float32, dev, "bias")
+    a.tail_in = _ptr_of(tail_in, (plan.n_slots, 3, cch), dt, dev, "tail_in")
+    a.tail_out = _ptr_of(tail_out, (plan.n_slots, 3, cch), dt, dev, "tail_out")
     _launch(lib().ssd_packed_conv_forward, a, dev, stream)
     return v, tail_out
 
@@ -717,34 +748,26 @@ def packed_conv_backward(u, w, plan, dx, dB, dC, *, bias=None, tail_in=None, dta
     them; dtail_out: [n, 3, C_ch] float32 or None, by sequence.  ``out`` may hold outputs under the same keys;
     rows of no sequence stay as they were in them, and are zero in those allocated here.
     """
-    _cuda(u, w, dx, dB, dC, bias, tail_in, dtail_out, workspace)
-    dev = u.device
-    _same_device(dev, w, dx, dB, dC, bias, tail_in, dtail_out, workspace)
+    dev = _device(u)
     total, cch = u.shape
     hp, gn = math.prod(dx.shape[1:]), math.prod(dB.shape[1:])
     if dx.shape[0] != total or dB.shape[0] != total or dC.shape != dB.shape or hp + 2 * gn != cch:
         raise ValueError(f"dx, dB and dC must be [{total}, ...] with {cch} channels in all")
     n = plan.nseq
-    o = dict(out or {})
-    for k, shp in (("du", (total, cch)), ("dtail_in", (n, 3, cch)), ("dconv_w", (cch, 4)), ("dconv_bias", (cch,))):
-        if k not in o:
-            o[k] = torch.zeros(shp, dtype=torch.float32, device=dev)
-        _full(o[k], shp, torch.float32, k)
-        _same_device(dev, o[k])
+    o, ptr = _outputs(out, (("du", (total, cch)), ("dtail_in", (n, 3, cch)), ("dconv_w", (cch, 4)), ("dconv_bias", (cch,))), dev)
     a = PackedConvBwdArgs()
     a.dtype = _dtype_code(u); a.d_inner = hp; a.d_bc = gn
     _plan_args(a, plan, total, dev)
-    a.u, a.u_row_stride = _rows2(u, cch, u.dtype, "u")
-    a.conv_w = _full(w, (cch, 4), torch.float32, "w").data_ptr()
-    a.conv_bias = _vp_of(_full(bias, (cch,), torch.float32, "bias"))
-    a.tail_in = _vp_of(_full(tail_in, (plan.n_slots, 3, cch), u.dtype, "tail_in"))
-    for t, k in ((dx, "dx"), (dB, "dB"), (dC, "dC")):
-        _f32(t, k)
-    a.dx = dx.data_ptr(); a.dB = dB.data_ptr(); a.dC = dC.data_ptr()
-    a.dtail_out = _vp_of(_full(dtail_out, (n, 3, cch), torch.float32, "dtail_out"))
-    a.du = o["du"].data_ptr(); a.dtail_in = _vp_of(o["dtail_in"]); a.dconv_w = o["dconv_w"].data_ptr()
-    a.dconv_bias = _vp_of(o["dconv_bias"])
-    workspace, a.workspace, a.workspace_bytes = _ws(workspace, lib().ssd_packed_conv_backward_workspace_size(n, total, cch), dev)
+    a.u, a.u_row_stride = _rows2(u, total, cch, u.dtype, dev, "u")
+    a.conv_w = _ptr_of(w, (cch, 4), torch.float32, dev, "w")
+    a.conv_bias = _ptr_of(bias, (cch,), torch.float32, dev, "bias")
+    a.tail_in = _ptr_of(tail_in, (plan.n_slots, 3, cch), u.dtype, dev, "tail_in")
+    a.dx = _ptr_of(dx, dx.shape, torch.float32, dev, "dx")
+    a.dB = _ptr_of(dB, dB.shape, torch.float32, dev, "dB")
+    a.dC = _ptr_of(dC, dC.shape, torch.float32, dev, "dC")
+    a.dtail_out = _ptr_of(dtail_out, (n, 3, cch), torch.float32, dev, "dtail_out")
+    a.du = ptr["du"]; a.dtail_in = ptr["dtail_in"]; a.dconv_w = ptr["dconv_w"]; a.dconv_bias = ptr["dconv_bias"]
+    _set_ws(a, workspace if workspace is not None else packed_conv_backward_workspace(plan, cch), dev)
     _launch(lib().ssd_packed_conv_backward, a, dev, stream)
     return o
 
@@ -757,21 +780,33 @@ def packed_scan_workspace(plan, H, P, N, dtype, G=1):
     return _bytes_on(plan.device, n)
 
 
-def _head_dims(x, B, C, H, G):
-    if H <= 0 or G <= 0 or x.dim() != 2 or B.dim() != 2 or x.shape[1] % H or B.shape[1] % G or B.shape != C.shape \
-            or x.shape[0] != B.shape[0]:
-        raise ValueError(f"x must be [total, H*P], B and C [total, G*N] (H={H}, G={G}); got "
-                         f"{tuple(x.shape)}, {tuple(B.shape)}, {tuple(C.shape)}")
+def _head_dims(x, B, H, G):
+    if H <= 0 or G <= 0 or x.dim() != 2 or B.dim() != 2 or x.shape[1] % H or B.shape[1] % G:
+        raise ValueError(f"x must be [total, H*P], B and C [total, G*N] (H={H}, G={G}); got {tuple(x.shape)}, {tuple(B.shape)}")
     return x.shape[1] // H, B.shape[1] // G
 
 
-def _rows3(t, H, P, dtype, name):
-    """(pointer, row stride) of rows of H*P elements given as [total, H, P] or [total, H*P]."""
-    if t.dim() == 3:
-        if t.shape[1:] != (H, P) or (P > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != P):
-            raise ValueError(f"{name} must be [total, {H}, {P}] with contiguous rows")
-        t = t.flatten(1)
-    return _rows2(t, H * P, dtype, name)
+def _scan_inputs(a, x, B, C, dt, A, D, h_in, plan, H, G, dev):
+    """The arguments that the scan and its gradient share; returns (total, P, N)."""
+    P, N = _head_dims(x, B, H, G)
+    total, io = x.shape[0], x.dtype
+    a.dtype = _dtype_code(x); a.H = H; a.P = P; a.N = N; a.G = G
+    _plan_args(a, plan, total, dev)
+    a.x, a.x_row_stride = _rows2(x, total, H * P, io, dev, "x")
+    a.B, a.B_row_stride = _rows2(B, total, G * N, io, dev, "B")
+    a.C, a.C_row_stride = _rows2(C, total, G * N, io, dev, "C")
+    a.dt = _ptr_of(dt, (total, H), torch.float32, dev, "dt")
+    a.A = _ptr_of(A, (H,), torch.float32, dev, "A")
+    a.D = _ptr_of(D, (H,), torch.float32, dev, "D")
+    a.h_in = _ptr_of(h_in, (plan.n_slots, H, P, N), torch.float32, dev, "h_in")
+    return total, P, N
+
+
+def _dt_args(a, dt_bias, dt_softplus, dt_limit, H, dev):
+    a.dt_bias = _ptr_of(dt_bias, (H,), torch.float32, dev, "dt_bias")
+    a.dt_softplus = 1 if dt_softplus else 0
+    if dt_limit is not None:
+        a.dt_min, a.dt_max = dt_limit
 
 
 def packed_scan_forward(x, B, C, dt, A, D=None, *, plan, H, G=1, h_in=None, h_out=None, y=None, workspace=None,
@@ -783,33 +818,16 @@ def packed_scan_forward(x, B, C, dt, A, D=None, *, plan, H, G=1, h_in=None, h_ou
     slots that the batch does not name stay as they were.  dt_bias / dt_softplus / dt_limit as in scan_forward.
     Rows of y that belong to no sequence stay as they were.
     """
-    _cuda(x, B, C, dt, A, D, h_in, h_out, y, workspace, dt_bias)
-    dev = x.device
-    _same_device(dev, B, C, dt, A, D, h_in, h_out, y, dt_bias)
-    P, N = _head_dims(x, B, C, H, G)
-    total = x.shape[0]
+    dev = _device(x)
+    a = PackedScanArgs()
+    total, P, N = _scan_inputs(a, x, B, C, dt, A, D, h_in, plan, H, G, dev)
     if y is None:
         y = torch.empty(total, H, P, dtype=x.dtype, device=dev)
-    a = PackedScanArgs()
-    a.dtype = _dtype_code(x); a.max_seqlen = plan.max_seqlen
-    a.H = H; a.P = P; a.N = N; a.G = G
-    _plan_args(a, plan, total, dev)
-    a.x, a.x_row_stride = _rows2(x, H * P, x.dtype, "x")
-    a.B, a.B_row_stride = _rows2(B, G * N, x.dtype, "B")
-    a.C, a.C_row_stride = _rows2(C, G * N, x.dtype, "C")
-    if y.shape[0] != total:
-        raise ValueError(f"y must have {total} rows")
-    a.y, a.y_row_stride = _rows3(y, H, P, x.dtype, "y")
-    a.dt = _full(dt, (total, H), torch.float32, "dt").data_ptr()
-    a.A = _full(A, (H,), torch.float32, "A").data_ptr()
-    a.D = _vp_of(_full(D, (H,), torch.float32, "D"))
-    _full(dt_bias, (H,), torch.float32, "dt_bias")
-    _set_dt(a, dt_bias, dt_softplus, dt_limit)
-    a.h_in = _vp_of(_full(h_in, (plan.n_slots, H, P, N), torch.float32, "h_in"))
-    a.h_out = _vp_of(_full(h_out, (plan.n_slots, H, P, N), torch.float32, "h_out"))
-    if workspace is None:
-        workspace = packed_scan_workspace(plan, H, P, N, x.dtype, G)
-    workspace, a.workspace, a.workspace_bytes = _ws(workspace, 0, dev)
+    a.max_seqlen = plan.max_seqlen
+    a.y, a.y_row_stride = _rows3(y, total, H, P, x.dtype, dev, "y")
+    _dt_args(a, dt_bias, dt_softplus, dt_limit, H, dev)
+    a.h_out = _ptr_of(h_out, (plan.n_slots, H, P, N), torch.float32, dev, "h_out")
+    _set_ws(a, workspace if workspace is not None else packed_scan_workspace(plan, H, P, N, x.dtype, G), dev)
     _launch(lib().ssd_packed_scan_forward, a, dev, stream)
     return y, h_out
 
@@ -828,37 +846,17 @@ def packed_scan_backward(x, B, C, dt, A, D, dy, *, plan, H, G=1, h_in=None, dh_o
     ``out`` may hold outputs under the same keys; rows of no sequence stay as they were in them, and are
     zero in those allocated here.
     """
-    _cuda(x, B, C, dt, A, D, dy, h_in, dh_out, workspace)
-    dev = x.device
-    _same_device(dev, B, C, dt, A, D, dy, h_in, dh_out)
-    P, N = _head_dims(x, B, C, H, G)
-    total, n = x.shape[0], plan.nseq
-    o = dict(out or {})
-    for k, shp in (("dx", (total, H, P)), ("dB", (total, G, N)), ("dC", (total, G, N)), ("ddt", (total, H)), ("dA", (H,)),
-                   ("dD", (H,)), ("dh_in", (n, H, P, N))):
-        if k not in o:
-            o[k] = torch.zeros(shp, dtype=torch.float32, device=dev)
-        _full(o[k], shp, torch.float32, k)
-        _same_device(dev, o[k])
+    dev = _device(x)
     a = PackedScanBwdArgs()
-    a.dtype = _dtype_code(x); a.H = H; a.P = P; a.N = N; a.G = G
-    _plan_args(a, plan, total, dev)
-    a.x, a.x_row_stride = _rows2(x, H * P, x.dtype, "x")
-    a.B, a.B_row_stride = _rows2(B, G * N, x.dtype, "B")
-    a.C, a.C_row_stride = _rows2(C, G * N, x.dtype, "C")
-    if dy.shape[0] != total:
-        raise ValueError(f"dy must have {total} rows")
-    a.dy, a.dy_row_stride = _rows3(dy, H, P, x.dtype, "dy")
-    a.dt = _full(dt, (total, H), torch.float32, "dt").data_ptr()
-    a.A = _full(A, (H,), torch.float32, "A").data_ptr()
-    a.D = _vp_of(_full(D, (H,), torch.float32, "D"))
-    a.h_in = _vp_of(_full(h_in, (plan.n_slots, H, P, N), torch.float32, "h_in"))
-    a.dh_out = _vp_of(_full(dh_out, (n, H, P, N), torch.float32, "dh_out"))
-    a.dx = o["dx"].data_ptr(); a.dB = o["dB"].data_ptr(); a.dC = o["dC"].data_ptr(); a.ddt = o["ddt"].data_ptr()
-    a.dA = o["dA"].data_ptr(); a.dD = _vp_of(o["dD"]); a.dh_in = _vp_of(o["dh_in"])
-    if workspace is None:
-        workspace = packed_scan_backward_workspace(plan, H, P, N)
-    workspace, a.workspace, a.workspace_bytes = _ws(workspace, 0, dev)
+    total, P, N = _scan_inputs(a, x, B, C, dt, A, D, h_in, plan, H, G, dev)
+    n = plan.nseq
+    o, ptr = _outputs(out, (("dx", (total, H, P)), ("dB", (total, G, N)), ("dC", (total, G, N)), ("ddt", (total, H)), ("dA", (H,)),
+                            ("dD", (H,)), ("dh_in", (n, H, P, N))), dev)
+    a.dy, a.dy_row_stride = _rows3(dy, total, H, P, x.dtype, dev, "dy")
+    a.dh_out = _ptr_of(dh_out, (n, H, P, N), torch.float32, dev, "dh_out")
+    a.dx = ptr["dx"]; a.dB = ptr["dB"]; a.dC = ptr["dC"]; a.ddt = ptr["ddt"]
+    a.dA = ptr["dA"]; a.dD = ptr["dD"]; a.dh_in = ptr["dh_in"]
+    _set_ws(a, workspace if workspace is not None else packed_scan_backward_workspace(plan, H, P, N), dev)
     _launch(lib().ssd_packed_scan_backward, a, dev, stream)
     return o
 
@@ -868,57 +866,53 @@ def decode_slots(u, conv_w, dt, A, D=None, *, slots, tail_in, h_in, H, P, N, G=1
     """One token of b streams of a pool: u [b, C_ch], dt [b, H], slots [b] int32 (-1 = an empty row, whose y is
     zero).  tail_in, tail_out: [n_slots, 3, C_ch], h_in, h_out: [n_slots, H, P, N] float32; without tail_out /
     h_out they are updated in place.  Returns {"y": [b, H, P], "h_out", "tail_out"}."""
+    dev = _device(u)
+    b, cch = u.shape
+    io, f32 = u.dtype, torch.float32
+    if cch != H * P + 2 * G * N:
+        raise ValueError(f"u must hold H*P + 2*G*N = {H * P + 2 * G * N} channels, has {cch}")
     if tail_out is None:
         tail_out = tail_in
     if h_out is None:
         h_out = h_in
-    _cuda(u, conv_w, dt, A, D, slots, tail_in, tail_out, h_in, h_out, conv_bias, y, dt_bias)
-    dev = u.device
-    _same_device(dev, conv_w, dt, A, D, slots, tail_in, tail_out, h_in, h_out, conv_bias, y, dt_bias)
-    b, cch = u.shape
-    if cch != H * P + 2 * G * N:
-        raise ValueError(f"u must hold H*P + 2*G*N = {H * P + 2 * G * N} channels, has {cch}")
-    n = h_in.shape[0]
     if y is None:
-        y = torch.empty(b, H, P, dtype=u.dtype, device=dev)
+        y = torch.empty(b, H, P, dtype=io, device=dev)
+    n = h_in.shape[0]
     a = DecodeSlotsArgs()
     a.dtype = _dtype_code(u); a.b = b; a.n_slots = n; a.H = H; a.P = P; a.N = N; a.G = G
-    a.slots = _full(slots, (b,), torch.int32, "slots").data_ptr()
-    a.u, a.u_batch_stride = _rows2(u, cch, u.dtype, "u")
-    if y.shape[0] != b:
-        raise ValueError(f"y must have {b} rows")
-    a.y, a.y_batch_stride = _rows3(y, H, P, u.dtype, "y")
-    a.conv_w = _full(conv_w, (cch, 4), torch.float32, "conv_w").data_ptr()
-    a.conv_bias = _vp_of(_full(conv_bias, (cch,), torch.float32, "conv_bias"))
-    a.tail_in = _full(tail_in, (n, 3, cch), u.dtype, "tail_in").data_ptr()
-    a.tail_out = _full(tail_out, (n, 3, cch), u.dtype, "tail_out").data_ptr()
-    a.h_in = _full(h_in, (n, H, P, N), torch.float32, "h_in").data_ptr()
-    a.h_out = _full(h_out, (n, H, P, N), torch.float32, "h_out").data_ptr()
-    a.dt = _full(dt, (b, H), torch.float32, "dt").data_ptr()
-    a.A = _full(A, (H,), torch.float32, "A").data_ptr()
-    a.D = _vp_of(_full(D, (H,), torch.float32, "D"))
-    _full(dt_bias, (H,), torch.float32, "dt_bias")
-    _set_dt(a, dt_bias, dt_softplus, dt_limit)
+    a.slots = _ptr_of(slots, (b,), torch.int32, dev, "slots")
+    a.u, a.u_batch_stride = _rows2(u, b, cch, io, dev, "u")
+    a.y, a.y_batch_stride = _rows3(y, b, H, P, io, dev, "y")
+    a.conv_w = _ptr_of(conv_w, (cch, 4), f32, dev, "conv_w")
+    a.conv_bias = _ptr_of(conv_bias, (cch,), f32, dev, "conv_bias")
+    pool = (n, H, P, N)
+    a.h_in = _ptr_of(h_in, pool, f32, dev, "h_in")
+    a.h_out = a.h_in if h_out is h_in else _ptr_of(h_out, pool, f32, dev, "h_out")
+    pool = (n, 3, cch)
+    a.tail_in = _ptr_of(tail_in, pool, io, dev, "tail_in")
+    a.tail_out = a.tail_in if tail_out is tail_in else _ptr_of(tail_out, pool, io, dev, "tail_out")
+    a.dt = _ptr_of(dt, (b, H), f32, dev, "dt")
+    a.A = _ptr_of(A, (H,), f32, dev, "A")
+    a.D = _ptr_of(D, (H,), f32, dev, "D")
+    _dt_args(a, dt_bias, dt_softplus, dt_limit, H, dev)
     _launch(lib().ssd_decode_slots, a, dev, stream)
     return {"y": y, "h_out": h_out, "tail_out": tail_out}
 
 
-def _norm_rows(t, d, name):
-    """(pointer, row stride, rows) of a [..., d] tensor whose leading dimensions step through memory evenly."""
-    if t.shape[-1] != d:
-        raise ValueError(f"{name} must have {d} channels")
+def _norm_rows(t, shape, dtype, dev, name):
+    """(pointer, row stride) of a [..., d] tensor whose leading dimensions step through memory evenly."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dim() != 2:
-        t = t.view(-1, d) if t.is_contiguous() else t.flatten(0, -2)
-    p, rs = _rows2(t, d, t.dtype, name)
-    return p, rs, t.shape[0]
+        t = t.view(-1, shape[-1])
+    return _rows2(t, t.shape[0], shape[-1], dtype, dev, name)
 
 
-def gated_rmsnorm_backward_workspace(rows, d, device=None, dtype=torch.bfloat16):
+def gated_rmsnorm_backward_workspace(rows, d, device=None):
     """Workspace of gated_rmsnorm_backward for this many rows of d channels."""
     dev = torch.device(device or "cuda")
     with torch.cuda.device(dev):
-        n = max(lib().ssd_gated_rmsnorm_backward_workspace_size(rows, d, c) for c in (SSD_F32, SSD_BF16))
-    return _bytes_on(dev, n)
+        return _bytes_on("cuda", lib().ssd_gated_rmsnorm_backward_workspace_size(rows, d))
 
 
 def gated_rmsnorm_backward(dout, y, z, weight, eps=1e-5, group_size=0, out=None, workspace=None, stream=None):
@@ -927,35 +921,24 @@ def gated_rmsnorm_backward(dout, y, z, weight, eps=1e-5, group_size=0, out=None,
     dout, y, z: [..., d] with the same leading shape, rows of d contiguous channels.  ``out`` may hold outputs
     under the same keys; dy may be dout or y, dz may be z (a row is read before it is written).
     """
-    _cuda(dout, y, z, weight, workspace)
-    dev = y.device
-    _same_device(dev, dout, z, weight, workspace)
-    d = y.shape[-1]
-    if dout.shape != y.shape or z.shape != y.shape:
-        raise ValueError("dout, y and z must have the same shape")
-    if dout.dtype != y.dtype or z.dtype != y.dtype:
-        raise TypeError("dout, y and z must share the I/O dtype")
+    dev = _device(y)
+    shape, io = y.shape, y.dtype
+    d = shape[-1]
     o = dict(out or {})
     for k in ("dy", "dz"):
         if k not in o:
-            o[k] = torch.empty(y.shape, dtype=y.dtype, device=dev)
-        if o[k].dtype != y.dtype:
-            raise TypeError(f"{k} must have y's dtype")
-        _shape(o[k], y.shape, k)
+            o[k] = torch.empty(shape, dtype=io, device=dev)
     if "dweight" not in o:
         o["dweight"] = torch.empty(d, dtype=torch.float32, device=dev)
-    _same_device(dev, *(o[k] for k in ("dy", "dz", "dweight")))
     a = GatedRmsnormBwdArgs()
-    a.dtype = _dtype_code(y); a.d = d; a.group_size = int(group_size); a.eps = float(eps)
-    a.dout, a.dout_row_stride, a.rows = _norm_rows(dout, d, "dout")
-    a.y, a.y_row_stride, _ = _norm_rows(y, d, "y")
-    a.z, a.z_row_stride, _ = _norm_rows(z, d, "z")
-    a.dy, a.dy_row_stride, _ = _norm_rows(o["dy"], d, "dy")
-    a.dz, a.dz_row_stride, _ = _norm_rows(o["dz"], d, "dz")
-    a.weight = _full(weight, (d,), torch.float32, "weight").data_ptr()
-    a.dweight = _full(o["dweight"], (d,), torch.float32, "dweight").data_ptr()
-    if workspace is None:
-        workspace = gated_rmsnorm_backward_workspace(a.rows, d, dev)
-    workspace, a.workspace, a.workspace_bytes = _ws(workspace, 0, dev)
+    a.dtype = _dtype_code(y); a.d = d; a.rows = y.numel() // d; a.group_size = int(group_size); a.eps = eps
+    a.dout, a.dout_row_stride = _norm_rows(dout, shape, io, dev, "dout")
+    a.y, a.y_row_stride = _norm_rows(y, shape, io, dev, "y")
+    a.z, a.z_row_stride = _norm_rows(z, shape, io, dev, "z")
+    a.dy, a.dy_row_stride = _norm_rows(o["dy"], shape, io, dev, "dy")
+    a.dz, a.dz_row_stride = _norm_rows(o["dz"], shape, io, dev, "dz")
+    a.weight = _ptr_of(weight, (d,), torch.float32, dev, "weight")
+    a.dweight = _ptr_of(o["dweight"], (d,), torch.float32, dev, "dweight")
+    _set_ws(a, workspace if workspace is not None else gated_rmsnorm_backward_workspace(a.rows, d, dev), dev)
     _launch(lib().ssd_gated_rmsnorm_backward, a, dev, stream)
     return o

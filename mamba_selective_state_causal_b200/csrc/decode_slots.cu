@@ -9,8 +9,13 @@
 // state in place in shared memory and sends each back with one bulk copy.  The cluster is what lets
 // the new conv buffer be written in the same launch, over the old one: B's and C's channels are read
 // by all CTAs of the stream, and the barrier that every CTA arrives at after reading them (and waits
-// for only before it writes) comes long after.  v is not rounded to the I/O type here: it stays in
+// for only before it writes) comes long after.  A state moves in two halves of P / 2 rows (16 KB at P = 64,
+// N = 128), four in flight per CTA and three CTAs per SM (all of them, up to 16, where the batch is so small
+// that a CTA has its SM to itself); a buffer is refilled one piece after its
+// copy out was started, so that nobody waits for that copy to have read it.  v is not rounded to the I/O type here: it stays in
 // registers and shared memory, where the layer's packed convolution stores it.
+#include <algorithm>
+
 #include <cooperative_groups.h>
 
 #include "packed.cuh"
@@ -23,7 +28,7 @@ namespace {
 using namespace tc;
 
 constexpr int kSlotThreads = 256;
-constexpr int kStages = 2;
+constexpr int kMaxStages = 16;
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
 {
@@ -36,79 +41,98 @@ __device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t 
                  ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
 }
 
-template <typename T>
+// nq = N / 4: lanes of a state row
+template <typename T, int nq>
 __global__ void __launch_bounds__(kSlotThreads) decode_slots_kernel(SlotDecodeParams p)
 {
     extern __shared__ __align__(128) uint8_t raw[];
-    __shared__ uint64_t full[kStages];
+    __shared__ uint64_t full[kMaxStages];
+    const int kStages = p.stages;
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     const int ncta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int bi = blockIdx.x / ncta, tid = threadIdx.x;
-    const int P = p.P, N = p.N, PN = P * N;
+    const int P = p.P, PN = P * 4 * nq;
+    constexpr int N = 4 * nq;
+    const int R = P / 2, piece = R * N;                           // a state goes in two pieces of R rows
     const int h0 = rank * p.heads_per_cta, h1 = min(p.H, h0 + p.heads_per_cta);
     const int din = p.H * P, C_ch = din + 2 * p.G * N;
-    const uint32_t bytes = (uint32_t)PN * 4u;
+    const uint32_t bytes = (uint32_t)piece * 4u;
+    const int np = 2 * (h1 - h0);                                 // pieces of this CTA's heads, one after the other
 
-    float *state = reinterpret_cast<float *>(raw);               // [kStages][P N]
-    float *xs = state + kStages * PN;                             // [heads_per_cta][P]
-    float *bc = xs + p.heads_per_cta * P;                         // [groups][2 N]
+    float *state = reinterpret_cast<float *>(raw);               // [kStages][R N]
+    float *xs = state + kStages * piece;                           // [heads_per_cta][P]
+    float *hv = xs + p.heads_per_cta * P;                         // [heads_per_cta][4]: e^{dt A}, dt, D
+    float *bc = hv + p.heads_per_cta * 4;                         // [groups][2 N]
 
-    // a slot out of range, or one that an earlier row of the batch has, leaves the row empty
-    const int slot = p.slots[bi];
-    bool twice = false;
-    if (slot >= 0)
-        for (int j = tid; j < bi; j += kSlotThreads) twice |= p.slots[j] == slot;
-    if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
-        fence_mbar_init();
-    }
-    const bool refused = __syncthreads_or(twice ? 1 : 0) != 0 || slot < -1 || slot >= p.n_slots;
-    if (refused && tid == 0 && rank == 0) atomicOr(p.status, kDevIndex);
     T *y = reinterpret_cast<T *>(p.y) + (int64_t)bi * p.ybs;
-    if (slot < 0 || refused) {                                    // the same for every CTA of the cluster
+    const int slot = p.slots[bi];
+    const bool inside = slot >= 0 && slot < p.n_slots;            // the same for every CTA of the cluster
+    if (!inside) {
+        if (slot != -1 && tid == 0 && rank == 0) atomicOr(p.status, kDevIndex);
         for (int i = h0 * P + tid; i < h1 * P; i += kSlotThreads) y[i] = from_f32<T>(0.0f);
         return;
     }
-    const float *hin = p.h_in + (int64_t)slot * p.H * PN;
-    float *hout = p.h_out + (int64_t)slot * p.H * PN;
-    if (tid == 0)
-        for (int i = 0; i < kStages && h0 + i < h1; ++i) {
+    const float *hin = p.h_in + ((int64_t)slot * p.H + h0) * PN;
+    float *hout = p.h_out + ((int64_t)slot * p.H + h0) * PN;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+        for (int i = 0; i < kStages && i < np; ++i) {
             mbar_arrive_expect_tx(&full[i], bytes);
-            bulk_load(state + i * PN, hin + (int64_t)(h0 + i) * PN, bytes, &full[i]);
+            bulk_load(state + i * piece, hin + (int64_t)i * piece, bytes, &full[i]);
         }
+    }
 
-    // conv + SiLU of the heads' x, then of B and C of the groups they use
+    // conv + SiLU of the heads' x, then of B and C of the groups they use; two channels per thread and turn,
+    // all of their loads in flight together
     const T *u = reinterpret_cast<const T *>(p.u) + (int64_t)bi * p.ubs;
     const T *tin = reinterpret_cast<const T *>(p.tail_in) + (int64_t)slot * 3 * C_ch;
     T *tout = reinterpret_cast<T *>(p.tail_out) + (int64_t)slot * 3 * C_ch;
-    auto conv = [&](int c, T &r1, T &r2, T &r3) {
-        const float4 w = __ldg(reinterpret_cast<const float4 *>(p.w) + c);
-        const T r0 = tin[c];
-        r1 = tin[C_ch + c]; r2 = tin[2 * C_ch + c]; r3 = u[c];
-        float z = p.bias ? __ldg(p.bias + c) : 0.0f;
-        z = fmaf(w.x, to_f32(r0), z);
-        z = fmaf(w.y, to_f32(r1), z);
-        z = fmaf(w.z, to_f32(r2), z);
-        z = fmaf(w.w, to_f32(r3), z);
-        return z / (1.0f + expf(-z));
-    };
-    auto put = [&](int c, T r1, T r2, T r3) { tout[c] = r1; tout[C_ch + c] = r2; tout[2 * C_ch + c] = r3; };
-    for (int i = tid; i < (h1 - h0) * P; i += kSlotThreads) {
-        T r1, r2, r3;
-        const int c = h0 * P + i;                                 // no other CTA reads or writes this channel
-        xs[i] = conv(c, r1, r2, r3);
-        put(c, r1, r2, r3);
-    }
     const int g0 = h0 < h1 ? (int)((int64_t)h0 * p.G / p.H) : 0;
     const int g1 = h0 < h1 ? (int)((int64_t)(h1 - 1) * p.G / p.H) + 1 : 0;
-    for (int i = tid; i < (g1 - g0) * 2 * N; i += kSlotThreads) {
-        const int g = i / (2 * N), n = i % (2 * N);
-        T r1, r2, r3;
-        bc[i] = conv(n < N ? din + (g0 + g) * N + n : din + (p.G + g0 + g) * N + n - N, r1, r2, r3);
+    const int nx = h0 < h1 ? (h1 - h0) * P : 0, nch = nx + (g1 - g0) * 2 * N;
+    auto channel = [&](int i) {
+        if (i < nx) return h0 * P + i;
+        const int g = (i - nx) / (2 * N), n = (i - nx) % (2 * N);
+        return n < N ? din + (g0 + g) * N + n : din + (p.G + g0 + g) * N + n - N;
+    };
+    bool twice = false;                                           // an earlier row of the batch has this slot
+    for (int j = tid; j < bi; j += kSlotThreads) twice |= p.slots[j] == slot;
+    for (int i0 = tid; i0 < nch; i0 += 2 * kSlotThreads) {
+        T r[2][4];
+        float4 w[2];
+        float b[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = i0 + k * kSlotThreads;
+            if (i < nch) {
+                const int c = channel(i);
+                r[k][0] = tin[c]; r[k][1] = tin[C_ch + c]; r[k][2] = tin[2 * C_ch + c]; r[k][3] = u[c];
+                w[k] = __ldg(reinterpret_cast<const float4 *>(p.w) + c);
+                b[k] = p.bias ? __ldg(p.bias + c) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = i0 + k * kSlotThreads;
+            if (i < nch) {
+                float z = b[k];
+                z = fmaf(w[k].x, to_f32(r[k][0]), z);
+                z = fmaf(w[k].y, to_f32(r[k][1]), z);
+                z = fmaf(w[k].z, to_f32(r[k][2]), z);
+                z = fmaf(w[k].w, to_f32(r[k][3]), z);
+                (i < nx ? xs[i] : bc[i - nx]) = z / (1.0f + expf(-z));
+            }
+        }
     }
-    // this CTA has read the old buffer's B and C rows; it writes its share of the new ones below.
-    // The new rows' values are read before the barrier, since any of them may change after it
+    for (int i = tid; i < h1 - h0; i += kSlotThreads) {
+        const int h = h0 + i;
+        const float dt = dt_effective(p.dt[(int64_t)bi * p.H + h], p.dt_bias, h, p.dt_softplus, p.dt_min, p.dt_max);
+        reinterpret_cast<float4 *>(hv)[i] = make_float4(expf(dt * p.A[h]), dt, p.D ? p.D[h] : 0.0f, 0.0f);
+    }
+    // this CTA has read the old buffer's B and C rows; it writes its share of the new ones at the end.
+    // Their values are read before the barrier, since any of them may change after it
     const int bcn = 2 * p.G * N, share = (bcn + ncta - 1) / ncta;
     constexpr int kKeep = 4;                                      // share <= kKeep * kSlotThreads (checked by the launcher)
     T k1[kKeep], k2[kKeep], k3[kKeep];
@@ -117,70 +141,100 @@ __global__ void __launch_bounds__(kSlotThreads) decode_slots_kernel(SlotDecodePa
         const int i = tid + k * kSlotThreads, c = din + rank * share + i;
         if (i < share && rank * share + i < bcn) { k1[k] = tin[C_ch + c]; k2[k] = tin[2 * C_ch + c]; k3[k] = u[c]; }
     }
-    __syncthreads();
+    if (__syncthreads_or(twice ? 1 : 0)) {                        // the same for every CTA of the cluster
+        if (tid == 0) {
+            if (rank == 0) atomicOr(p.status, kDevIndex);
+            for (int i = 0; i < kStages && i < np; ++i) mbar_wait(&full[i], 0, nullptr, p.wait_limit_ns);
+        }
+        for (int i = h0 * P + tid; i < h1 * P; i += kSlotThreads) y[i] = from_f32<T>(0.0f);
+        return;
+    }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
     const int warp = tid >> 5, lane = tid & 31;
-    const int nq = N >> 2, sub = lane / nq, col = lane % nq, per = 32 / nq;
-    int st = 0;
-    uint32_t ph = 0;
-    for (int h = h0; h < h1; ++h) {
-        float *sm = state + st * PN;
-        const float dt = dt_effective(p.dt[(int64_t)bi * p.H + h], p.dt_bias, h, p.dt_softplus, p.dt_min, p.dt_max);
-        const float a = expf(dt * p.A[h]);
-        const float Dh = p.D ? p.D[h] : 0.0f;
+    constexpr int per = 32 / nq, kRows = 4, kStep = (kSlotThreads / 32) * per;   // rows a warp, a thread, a turn of the CTA takes
+    const int sub = lane / nq, col = lane % nq;
+    const bool up = (lane & (nq / 2)) != 0, up2 = (lane & (nq / 4)) != 0;
+    for (int k = 0; k < np; ++k) {
+        const int st = k % kStages, h = h0 + (k >> 1), r0 = (k & 1) * R;
+        float *sm = state + st * piece;
+        const float4 he = reinterpret_cast<const float4 *>(hv)[h - h0];
+        const float a = he.x, dt = he.y, Dh = he.z;
         const float *bg = bc + ((int)((int64_t)h * p.G / p.H) - g0) * 2 * N;
         const float4 Bv = reinterpret_cast<const float4 *>(bg)[col], Cv = reinterpret_cast<const float4 *>(bg + N)[col];
-        const float *xh = xs + (h - h0) * P;
-        const bool landed = mbar_wait(&full[st], ph, nullptr, p.wait_limit_ns);
-        for (int r = warp * per + sub; r < P; r += (kSlotThreads / 32) * per) {
-            float4 *cell = reinterpret_cast<float4 *>(sm + r * N) + col;
-            float4 v = *cell;
-            const float dx = dt * xh[r];
-            v.x = fmaf(a, v.x, dx * Bv.x);
-            v.y = fmaf(a, v.y, dx * Bv.y);
-            v.z = fmaf(a, v.z, dx * Bv.z);
-            v.w = fmaf(a, v.w, dx * Bv.w);
-            *cell = v;
-            float part = fmaf(Cv.x, v.x, fmaf(Cv.y, v.y, fmaf(Cv.z, v.z, Cv.w * v.w)));
-            for (int o = 1; o < nq; o <<= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-            if (col == 0) y[h * P + r] = from_f32<T>(fmaf(Dh, xh[r], part));
+        const float *xh = xs + (h - h0) * P + r0;
+        const bool landed = mbar_wait(&full[st], (uint32_t)(k / kStages) & 1, nullptr, p.wait_limit_ns);
+        for (int rb = warp * per + sub; rb - sub < R; rb += kRows * kStep) {
+            float4 v[kRows];
+            float part[kRows];
+#pragma unroll
+            for (int e = 0; e < kRows; ++e)
+                if (rb + e * kStep < R) v[e] = reinterpret_cast<const float4 *>(sm + (rb + e * kStep) * N)[col];
+#pragma unroll
+            for (int e = 0; e < kRows; ++e) {
+                part[e] = 0.0f;
+                if (rb + e * kStep < R) {
+                    const float dx = dt * xh[rb + e * kStep];
+                    v[e].x = fmaf(a, v[e].x, dx * Bv.x);
+                    v[e].y = fmaf(a, v[e].y, dx * Bv.y);
+                    v[e].z = fmaf(a, v[e].z, dx * Bv.z);
+                    v[e].w = fmaf(a, v[e].w, dx * Bv.w);
+                    reinterpret_cast<float4 *>(sm + (rb + e * kStep) * N)[col] = v[e];
+                    part[e] = fmaf(Cv.x, v[e].x, fmaf(Cv.y, v[e].y, fmaf(Cv.z, v[e].z, Cv.w * v[e].w)));
+                }
+            }
+            // the four rows' sums over their nq lanes in 3 + log2(nq / 4) exchanges: halves of the lanes take two rows
+            // each, quarters one
+            float k0 = up ? part[2] : part[0], k1 = up ? part[3] : part[1];
+            k0 += __shfl_xor_sync(0xffffffffu, up ? part[0] : part[2], nq / 2);
+            k1 += __shfl_xor_sync(0xffffffffu, up ? part[1] : part[3], nq / 2);
+            float sum = up2 ? k1 : k0;
+            sum += __shfl_xor_sync(0xffffffffu, up2 ? k0 : k1, nq / 4);
+#pragma unroll
+            for (int o = nq / 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const int r = rb + ((up ? 2 : 0) + (up2 ? 1 : 0)) * kStep;
+            if ((col & (nq / 4 - 1)) == 0 && r < R) y[h * P + r0 + r] = from_f32<T>(fmaf(Dh, xh[r], sum));
         }
         fence_proxy_async_smem();
         if (!__syncthreads_and(landed)) {
             // a copy never came: nothing more is written, and what is on its way is waited for
             if (tid == 0) {
                 atomicOr(p.status, kDevTimeout);
-                for (int k = 0; k < kStages && h + k < h1; ++k)
-                    mbar_wait(&full[(st + k) % kStages], st + k < kStages ? ph : ph ^ 1, nullptr, 100000000ull);
+                for (int q = k; q < np && q < k + kStages - (k > 0 ? 1 : 0); ++q)
+                    mbar_wait(&full[q % kStages], (uint32_t)(q / kStages) & 1, nullptr, 100000000ull);
             }
             break;
         }
         if (tid == 0) {
-            bulk_store(hout + (int64_t)h * PN, sm, bytes);
+            bulk_store(hout + (int64_t)k * piece, sm, bytes);
             tma_store_commit();
-            if (h + kStages < h1) {
-                tma_store_wait_read<0>();                         // the copy out has read this stage
-                mbar_arrive_expect_tx(&full[st], bytes);
-                bulk_load(sm, hin + (int64_t)(h + kStages) * PN, bytes, &full[st]);
+            if (k >= 1 && k - 1 + kStages < np) {
+                const int q = k - 1 + kStages;                    // into the buffer of piece k - 1
+                tma_store_wait_read<1>();                         // whose copy out has read it
+                mbar_arrive_expect_tx(&full[q % kStages], bytes);
+                bulk_load(state + (q % kStages) * piece, hin + (int64_t)q * piece, bytes, &full[q % kStages]);
             }
         }
-        if (++st == kStages) { st = 0; ph ^= 1; }
     }
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 #pragma unroll
     for (int k = 0; k < kKeep; ++k) {
         const int i = tid + k * kSlotThreads, c = din + rank * share + i;
-        if (i < share && rank * share + i < bcn) put(c, k1[k], k2[k], k3[k]);
+        if (i < share && rank * share + i < bcn) { tout[c] = k1[k]; tout[C_ch + c] = k2[k]; tout[2 * C_ch + c] = k3[k]; }
+    }
+    for (int i = tid; i < nx; i += kSlotThreads) {                // x's channels: no other CTA reads or writes them
+        const int c = h0 * P + i;
+        const T a = tin[C_ch + c], b = tin[2 * C_ch + c], n = u[c];
+        tout[c] = a; tout[C_ch + c] = b; tout[2 * C_ch + c] = n;
     }
     if (tid == 0) tma_store_wait<0>();
 }
 
-template <typename T>
-int launch_slots_t(const SlotDecodeParams &p, int cluster, size_t smem, cudaStream_t st)
+template <typename T, int nq>
+int launch_slots_n(const SlotDecodeParams &p, int cluster, size_t smem, cudaStream_t st)
 {
-    if (cudaFuncSetAttribute(decode_slots_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return 7;
+    static std::atomic<int> done[64];
+    if (!allow_smem(decode_slots_kernel<T, nq>, (int)smem, done)) return 7;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)p.b * (unsigned)cluster);
     cfg.blockDim = dim3(kSlotThreads);
@@ -194,14 +248,25 @@ int launch_slots_t(const SlotDecodeParams &p, int cluster, size_t smem, cudaStre
     cfg.attrs = at;
     cfg.numAttrs = 1;
     prof_begin(st, kKSlotDecode);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_slots_kernel<T>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_slots_kernel<T, nq>, p);
     prof_end(st, kKSlotDecode);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 0 : 7;
 }
 
+template <typename T>
+int launch_slots_t(const SlotDecodeParams &p, int cluster, size_t smem, cudaStream_t st)
+{
+    switch (p.N) {
+    case 16: return launch_slots_n<T, 4>(p, cluster, smem, st);
+    case 32: return launch_slots_n<T, 8>(p, cluster, smem, st);
+    case 64: return launch_slots_n<T, 16>(p, cluster, smem, st);
+    default: return launch_slots_n<T, 32>(p, cluster, smem, st);
+    }
+}
+
 }  // namespace
 
-int launch_slot_decode(SlotDecodeParams p, int dtype, cudaStream_t st)
+int launch_slot_decode(SlotDecodeParams p, int dtype, int sms, cudaStream_t st)
 {
     int cluster = 8;
     while (cluster > 1 && cluster > p.H) cluster /= 2;
@@ -209,8 +274,13 @@ int launch_slot_decode(SlotDecodeParams p, int dtype, cudaStream_t st)
     // groups that a run of heads can touch
     const int hpg = p.H / p.G;
     const int groups = p.heads_per_cta / hpg + 2 < p.G ? p.heads_per_cta / hpg + 2 : p.G;
-    const size_t smem = sizeof(float) * ((size_t)kStages * p.P * p.N + (size_t)p.heads_per_cta * p.P + (size_t)groups * 2 * p.N);
-    if (smem > 220 * 1024) return 6;
+    const size_t small = sizeof(float) * ((size_t)p.heads_per_cta * (p.P + 4) + (size_t)groups * 2 * p.N);
+    const size_t piece = sizeof(float) * (size_t)(p.P / 2) * p.N;
+    const size_t room = 200 * 1024;
+    if (small + 4 * piece > room) return 6;
+    const int np = 2 * p.heads_per_cta;
+    p.stages = p.b * cluster <= sms ? (int)std::min<size_t>(std::min(np, kMaxStages), (room - small) / piece) : std::min(np, 4);
+    const size_t smem = p.stages * piece + small;
     if ((2 * p.G * p.N + cluster - 1) / cluster > 4 * kSlotThreads) return 6;
     if ((int64_t)p.b * cluster > 0x7fffffffLL) return 6;
     return dtype == 1 ? launch_slots_t<__nv_bfloat16>(p, cluster, smem, st) : launch_slots_t<float>(p, cluster, smem, st);

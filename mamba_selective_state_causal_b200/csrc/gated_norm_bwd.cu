@@ -3,10 +3,11 @@
 //   dv = r (g - v r^2 mean(g v)),   dy = dv silu(z),   dz = dv y silu'(z),   dw = sum over rows of dout v r,
 //   silu(z) = z sg,  silu'(z) = sg (1 + z (1 - sg)),  sg = 1 / (1 + e^-z).
 // A row is read once (y, z, dout) and written once (dy, dz): 5 d elements, the memory's rate is the
-// bound.  A thread owns 8 channels and keeps kRows rows of them in registers (three 16-byte loads per
-// row in bf16) between the two sums over the group (of v^2 and of g v, both at once, in a fixed order)
-// and the outputs; the next rows' loads come from the other CTAs of the SM.  Its share of dw stays in
-// 8 registers over all the rows that its CTA walks, is written once per CTA, and is added over the
+// bound.  A thread owns 8 channels; its pieces of the next kDepth rows stream by cp.async through its own
+// slots of shared memory (48 KB per CTA, four CTAs per SM), where they stay between the two sums over
+// the group (of v^2 and of g v, both at once, in a fixed order) and the outputs, so that loads never
+// wait for a sum and hold no registers.  Its share of dw stays in 8 registers over all the rows that
+// its CTA walks, is written once per CTA, and is added over the
 // CTAs by a second kernel in a fixed order: no atomics, the same result every time.
 // Sums over a group: of 8 m channels, m threads.  m a power of two up to 32: shuffles among those
 // lanes.  m a multiple of 32: shuffles, then the warps' sums through shared memory.  Any other m: every
@@ -15,11 +16,17 @@
 #include <type_traits>
 
 #include "norm_bwd.cuh"
+#include "packed.cuh"
 
 namespace ssd {
 namespace {
 
 constexpr int kV = 8;
+
+__device__ __forceinline__ void cp16(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
 
 __device__ __forceinline__ void unpack8f(const uint4 &a, float (&v)[8])
 {
@@ -27,11 +34,11 @@ __device__ __forceinline__ void unpack8f(const uint4 &a, float (&v)[8])
     v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
 }
 
-// 8 elements as loaded, packed while they wait
-template <typename T> struct Pack8;
-template <> struct Pack8<__nv_bfloat16> {
+// 8 elements in shared memory
+template <typename T> struct Vec8;
+template <> struct Vec8<__nv_bfloat16> {
     uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void fetch(const __nv_bfloat16 *p) { cp16(&a, p); }
     __device__ __forceinline__ void get(float (&v)[8]) const { unpack8f(a, v); }
     __device__ __forceinline__ static void put(__nv_bfloat16 *p, const float (&v)[8])
     {
@@ -39,13 +46,9 @@ template <> struct Pack8<__nv_bfloat16> {
                                                          pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
     }
 };
-template <> struct Pack8<float> {
+template <> struct Vec8<float> {
     float4 a, b;
-    __device__ __forceinline__ void load(const float *p)
-    {
-        a = __ldcs(reinterpret_cast<const float4 *>(p));
-        b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    }
+    __device__ __forceinline__ void fetch(const float *p) { cp16(&a, p); cp16(&b, p + 4); }
     __device__ __forceinline__ void get(float (&v)[8]) const
     {
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -56,122 +59,132 @@ template <> struct Pack8<float> {
         __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
     }
 };
+template <typename T> constexpr int kDepth = 96 / (3 * (int)sizeof(Vec8<T>)) * 2;   // 4 rows of bf16, 2 of fp32: 192 bytes per thread
 
-// sigma(z) with the hardware exponential (bf16) or the library's (fp32); -z is clamped so that the
-// divisor stays finite (sigma is below 2e-35 there either way)
-template <typename T> __device__ __forceinline__ float sigma(float z)
+// sigma(z) through the hardware's exponential and reciprocal (2 units in the last place each); e^-z beyond the
+// range of fp32 is infinite, and sigma 0
+__device__ __forceinline__ float sigma(float z)
 {
-    return std::is_same<T, float>::value ? 1.0f / (1.0f + expf(fminf(-z, 80.0f)))
-                                         : __fdividef(1.0f, 1.0f + __expf(fminf(-z, 80.0f)));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
 }
 
-// One CTA: `teams` rows side by side, d / 8 threads each, kRows rows of each in registers at once.
+// One CTA: `teams` rows side by side, d / 8 threads each; it walks the rows blockIdx.x * teams + team, a grid apart.
 // kMode: 0 groups of a power of two up to 32 threads, 1 of a multiple of 32, 2 any.
-// kMost bounds the threads (rows wider than 4096 channels need up to 1024 and take one row at a time).
-template <typename T, int kRows, int kMode, int kMost>
-__global__ void __launch_bounds__(kMost) gated_norm_bwd_kernel(NormBwdParams p, int teams)
+// kMost bounds the threads (rows wider than 2048 channels need up to 1024).
+template <typename T, int kMode, int kMost>
+__global__ void __launch_bounds__(kMost, 1024 / kMost) gated_norm_bwd_kernel(NormBwdParams p, int teams)
 {
-    extern __shared__ float2 part[];             // mode 1: [2][kRows][warps]; mode 2: [2][kRows][threads]
+    extern __shared__ __align__(16) uint8_t raw[];
+    constexpr int D = kDepth<T>;
+    Vec8<T> *ring = reinterpret_cast<Vec8<T> *>(raw) + threadIdx.x;               // [D][3][threads]
+    float2 *part = reinterpret_cast<float2 *>(raw + sizeof(Vec8<T>) * 3 * D * blockDim.x);   // mode 1: [2][warps]; mode 2: [2][threads]
     const int per = p.d / kV;                    // threads of a row
     const int team = threadIdx.x / per, i = threadIdx.x % per;
     const bool live = team < teams;
     const int m = p.group / kV;                  // threads of a group
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const float inv = 1.0f / (float)p.group;
-    float wv[8], dw[8] = {};
+    float2 wv[4] = {}, dw[4] = {};
     if (live) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) wv[k] = __ldg(p.w + kV * i + k);
+        for (int k = 0; k < 4; ++k) wv[k] = __ldg(reinterpret_cast<const float2 *>(p.w + kV * i) + k);
     }
-    const T *yb = reinterpret_cast<const T *>(p.y) + kV * i, *zb = reinterpret_cast<const T *>(p.z) + kV * i;
-    const T *ob = reinterpret_cast<const T *>(p.dout) + kV * i;
-    const int64_t step = (int64_t)gridDim.x * teams * kRows;
-    int buf = 0;
-    for (int64_t base = (int64_t)blockIdx.x * teams * kRows; base < p.rows; base += step, buf ^= 1) {
-        const int64_t r0 = base + (int64_t)team * kRows;
-        Pack8<T> py[kRows], pz[kRows], po[kRows];
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            if (live && r0 + r < p.rows) {
-                py[r].load(yb + (r0 + r) * p.yrs);
-                pz[r].load(zb + (r0 + r) * p.zrs);
-                po[r].load(ob + (r0 + r) * p.dors);
-            } else {
-                py[r] = {}; pz[r] = {}; po[r] = {};
-            }
+    const int64_t step = (int64_t)gridDim.x * teams;
+    const int64_t r0 = (int64_t)blockIdx.x * teams + team;
+    // the rows of every team in step: the CTA's first row decides the number of turns
+    const int64_t first = (int64_t)blockIdx.x * teams;
+    const int64_t turns = first < p.rows ? (p.rows - first + step - 1) / step : 0;
+    auto fetch = [&](int64_t k) {
+        const int64_t r = r0 + k * step;
+        if (live && k < turns && r < p.rows) {
+            Vec8<T> *q = ring + (int)(k % D) * 3 * blockDim.x;
+            q[0].fetch(reinterpret_cast<const T *>(p.y) + r * p.yrs + kV * i);
+            q[blockDim.x].fetch(reinterpret_cast<const T *>(p.z) + r * p.zrs + kV * i);
+            q[2 * blockDim.x].fetch(reinterpret_cast<const T *>(p.dout) + r * p.dors + kV * i);
         }
-        float2 s[kRows];                         // sums of v^2 and g v
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
+    for (int k = 0; k < D; ++k) fetch(k);
+    for (int64_t k = 0; k < turns; ++k) {
+        const int64_t r = r0 + k * step;
+        const bool on = live && r < p.rows;
+        const Vec8<T> *q = ring + (int)(k % D) * 3 * blockDim.x;
+        asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");    // row k's group is the oldest
+        float2 s = make_float2(0.f, 0.f);        // sums of v^2 and g v
+        float2 sg[4], si[4];                     // sigma(z) and silu(z) of 4 pairs of channels, until the outputs
+        if (on) {
             float y[8], z[8], o[8];
-            py[r].get(y); pz[r].get(z); po[r].get(o);
-            s[r] = make_float2(0.f, 0.f);
+            q[0].get(y); q[blockDim.x].get(z); q[2 * blockDim.x].get(o);
+            float2 vv = make_float2(0.f, 0.f), gv = vv;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float v = y[k] * (z[k] * sigma<T>(z[k]));
-                s[r].x = fmaf(v, v, s[r].x);
-                s[r].y = fmaf(o[k] * wv[k], v, s[r].y);
+            for (int e = 0; e < 4; ++e) {
+                sg[e] = make_float2(sigma(z[2 * e]), sigma(z[2 * e + 1]));
+                si[e] = __fmul2_rn(make_float2(z[2 * e], z[2 * e + 1]), sg[e]);
+                const float2 v = __fmul2_rn(make_float2(y[2 * e], y[2 * e + 1]), si[e]);
+                vv = __ffma2_rn(v, v, vv);
+                gv = __ffma2_rn(__fmul2_rn(make_float2(o[2 * e], o[2 * e + 1]), wv[e]), v, gv);
             }
+            s = make_float2(vv.x + vv.y, gv.x + gv.y);
         }
         if (kMode <= 1) {
             const int span = kMode == 0 ? m : 32;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r)
-                for (int o = 1; o < span; o <<= 1) {
-                    s[r].x += __shfl_xor_sync(0xffffffffu, s[r].x, o);
-                    s[r].y += __shfl_xor_sync(0xffffffffu, s[r].y, o);
-                }
+            for (int o = 1; o < span; o <<= 1) {
+                s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+                s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+            }
         }
         if (kMode == 1) {
-            float2 *q = part + buf * kRows * warps;
-            if (lane == 0) {
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) q[r * warps + warp] = s[r];
-            }
-            __syncthreads();                     // one per step: the buffers alternate
-            const int mw = m / 32, first = warp / mw * mw;
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                s[r] = make_float2(0.f, 0.f);
-                for (int k = 0; k < mw; ++k) { const float2 t = q[r * warps + first + k]; s[r].x += t.x; s[r].y += t.y; }
-            }
+            float2 *b = part + (k & 1) * warps;  // two in turn: one barrier per row
+            if (lane == 0) b[warp] = s;
+            __syncthreads();
+            const int mw = m / 32, w0 = warp / mw * mw;
+            s = make_float2(0.f, 0.f);
+            for (int e = 0; e < mw; ++e) { const float2 t = b[w0 + e]; s.x += t.x; s.y += t.y; }
         }
         if (kMode == 2) {
-            float2 *q = part + buf * kRows * blockDim.x;
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) q[r * blockDim.x + threadIdx.x] = s[r];
+            float2 *b = part + (k & 1) * blockDim.x;
+            b[threadIdx.x] = s;
             __syncthreads();
-            const int first = live ? team * per + i / m * m : 0;
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                s[r] = make_float2(0.f, 0.f);
-                if (live)
-                    for (int k = 0; k < m; ++k) { const float2 t = q[r * blockDim.x + first + k]; s[r].x += t.x; s[r].y += t.y; }
+            if (live) {
+                const int t0 = team * per + i / m * m;
+                s = make_float2(0.f, 0.f);
+                for (int e = 0; e < m; ++e) { const float2 t = b[t0 + e]; s.x += t.x; s.y += t.y; }
             }
         }
+        if (on) {
+            float y[8], o[8], a[8], b[8];
+            q[0].get(y); q[2 * blockDim.x].get(o);
+            const float rs = 1.0f / sqrtf(fmaf(s.x, inv, p.eps));
+            const float c = -rs * rs * (s.y * inv);
+            const float2 rs2 = make_float2(rs, rs), c2 = make_float2(c, c);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            if (!live || r0 + r >= p.rows) continue;
-            float y[8], z[8], o[8], a[8], b[8];
-            py[r].get(y); pz[r].get(z); po[r].get(o);
-            const float rs = 1.0f / sqrtf(fmaf(s[r].x, inv, p.eps));
-            const float c = rs * rs * (s[r].y * inv);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float sg = sigma<T>(z[k]), si = z[k] * sg, v = y[k] * si;
-                const float dv = rs * fmaf(-v, c, o[k] * wv[k]);
-                a[k] = dv * si;
-                b[k] = dv * y[k] * (sg * fmaf(z[k], 1.0f - sg, 1.0f));
-                dw[k] = fmaf(o[k] * rs, v, dw[k]);
+            for (int e = 0; e < 4; ++e) {
+                const float2 y2 = make_float2(y[2 * e], y[2 * e + 1]), o2 = make_float2(o[2 * e], o[2 * e + 1]);
+                const float2 v = __fmul2_rn(y2, si[e]);
+                const float2 dv = __fmul2_rn(rs2, __ffma2_rn(v, c2, __fmul2_rn(o2, wv[e])));
+                const float2 da = __fmul2_rn(dv, si[e]);
+                // silu'(z) = sg + si (1 - sg)
+                const float2 one = make_float2(1.0f - sg[e].x, 1.0f - sg[e].y);
+                const float2 db = __fmul2_rn(__fmul2_rn(dv, y2), __ffma2_rn(si[e], one, sg[e]));
+                a[2 * e] = da.x; a[2 * e + 1] = da.y;
+                b[2 * e] = db.x; b[2 * e + 1] = db.y;
+                dw[e] = __ffma2_rn(__fmul2_rn(o2, rs2), v, dw[e]);
             }
-            Pack8<T>::put(reinterpret_cast<T *>(p.dy) + (r0 + r) * p.dyrs + kV * i, a);
-            Pack8<T>::put(reinterpret_cast<T *>(p.dz) + (r0 + r) * p.dzrs + kV * i, b);
+            Vec8<T>::put(reinterpret_cast<T *>(p.dy) + r * p.dyrs + kV * i, a);
+            Vec8<T>::put(reinterpret_cast<T *>(p.dz) + r * p.dzrs + kV * i, b);
         }
+        fetch(k + D);                            // into the slots just read, which are this thread's own
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (live) {
         float4 *q = reinterpret_cast<float4 *>(p.ws + ((int64_t)blockIdx.x * teams + team) * p.d + kV * i);
-        q[0] = make_float4(dw[0], dw[1], dw[2], dw[3]);
-        q[1] = make_float4(dw[4], dw[5], dw[6], dw[7]);
+        q[0] = make_float4(dw[0].x, dw[0].y, dw[1].x, dw[1].y);
+        q[1] = make_float4(dw[2].x, dw[2].y, dw[3].x, dw[3].y);
     }
 }
 
@@ -203,49 +216,51 @@ __global__ void __launch_bounds__(32 * kSumWarps) gated_norm_dw_kernel(NormBwdPa
     }
 }
 
-template <typename T, int kRows, int kMode, int kMost>
+template <typename T, int kMode, int kMost>
 int launch_mode(const NormBwdParams &p, const NormBwdPlan &pl, cudaStream_t st)
 {
-    const size_t smem = sizeof(float2) * 2 * kRows * (kMode == 0 ? 0 : kMode == 1 ? pl.threads / 32 : pl.threads);
+    const size_t smem = sizeof(Vec8<T>) * 3 * kDepth<T> * pl.threads +
+                        sizeof(float2) * 2 * (kMode == 0 ? 0 : kMode == 1 ? pl.threads / 32 : pl.threads);
+    static std::atomic<int> done[64];
+    if (!allow_smem(gated_norm_bwd_kernel<T, kMode, kMost>, (int)smem, done)) return 7;
     prof_begin(st, kKGatedNormBwd);
-    gated_norm_bwd_kernel<T, kRows, kMode, kMost><<<(unsigned)pl.grid, pl.threads, smem, st>>>(p, pl.teams);
+    gated_norm_bwd_kernel<T, kMode, kMost><<<(unsigned)pl.grid, pl.threads, smem, st>>>(p, pl.teams);
     gated_norm_dw_kernel<<<(unsigned)((p.d + 31) / 32), 32 * kSumWarps, 0, st>>>(p, pl.grid * pl.teams);
     prof_end(st, kKGatedNormBwd);
     return cudaGetLastError() == cudaSuccess ? 0 : 7;
 }
 
-template <typename T, int kRows, int kMost>
+template <typename T, int kMost>
 int launch_t(const NormBwdParams &p, const NormBwdPlan &pl, cudaStream_t st)
 {
     const int m = p.group / kV;
     // rows start at multiples of 32 threads, or their groups do not straddle warps
     const bool whole = (p.d / kV) % 32 == 0;
-    if (m <= 32 && (m & (m - 1)) == 0) return launch_mode<T, kRows, 0, kMost>(p, pl, st);
-    if (m % 32 == 0 && whole) return launch_mode<T, kRows, 1, kMost>(p, pl, st);
-    return launch_mode<T, kRows, 2, kMost>(p, pl, st);
+    if (m <= 32 && (m & (m - 1)) == 0) return launch_mode<T, 0, kMost>(p, pl, st);
+    if (m % 32 == 0 && whole) return launch_mode<T, 1, kMost>(p, pl, st);
+    return launch_mode<T, 2, kMost>(p, pl, st);
 }
 
 }  // namespace
 
 // Threads: whole rows side by side up to 256 threads (wider rows: their own d / 8), rounded up to
-// warps.  Grid: what fits two CTAs' worth of 512 threads on each of the SMs, and no more than there are rows.
-NormBwdPlan norm_bwd_plan(int64_t rows, int d, int dtype, int sms)
+// warps.  Grid: the 1024 threads that fit an SM, on each of them, and no more than there are rows.
+NormBwdPlan norm_bwd_plan(int64_t rows, int d, int sms)
 {
     NormBwdPlan pl;
     const int per = d / kV;
-    pl.rows = per > 512 ? 1 : (dtype == 1 ? 4 : 2);
     pl.teams = std::max(1, 256 / per);
     pl.threads = (pl.teams * per + 31) / 32 * 32;
-    const int64_t need = (rows + pl.teams * pl.rows - 1) / (pl.teams * pl.rows);
+    const int64_t need = (rows + pl.teams - 1) / pl.teams;
     pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(need, (int64_t)sms * std::max(1, 1024 / pl.threads)));
     return pl;
 }
 
 int launch_gated_norm_backward(const NormBwdParams &p, int dtype, int sms, cudaStream_t st)
 {
-    const NormBwdPlan pl = norm_bwd_plan(p.rows, p.d, dtype, sms);
-    if (pl.rows == 1) return dtype == 1 ? launch_t<__nv_bfloat16, 1, 1024>(p, pl, st) : launch_t<float, 1, 1024>(p, pl, st);
-    return dtype == 1 ? launch_t<__nv_bfloat16, 4, 512>(p, pl, st) : launch_t<float, 2, 512>(p, pl, st);
+    const NormBwdPlan pl = norm_bwd_plan(p.rows, p.d, sms);
+    if (pl.threads > 256) return dtype == 1 ? launch_t<__nv_bfloat16, 1024>(p, pl, st) : launch_t<float, 1024>(p, pl, st);
+    return dtype == 1 ? launch_t<__nv_bfloat16, 256>(p, pl, st) : launch_t<float, 256>(p, pl, st);
 }
 
 }  // namespace ssd

@@ -20,9 +20,9 @@ struct NormBwdParams {
 };
 
 struct NormBwdPlan {
-    int rows, teams, threads, grid;
+    int teams, threads, grid;
 };
-NormBwdPlan norm_bwd_plan(int64_t rows, int d, int dtype, int sms);
+NormBwdPlan norm_bwd_plan(int64_t rows, int d, int sms);
 int launch_gated_norm_backward(const NormBwdParams &p, int dtype, int sms, cudaStream_t st);
 
 }  // namespace ssd

@@ -9,6 +9,8 @@
 // no rows (its state still moves from h_in to h_out); one whose offsets are refused has none.
 #pragma once
 
+#include <atomic>
+
 #include "ssd_common.cuh"
 
 namespace ssd {
@@ -92,6 +94,15 @@ __device__ __forceinline__ int packed_n64(const PackedPlan &p, unsigned int *sta
 __device__ __forceinline__ int packed_n128(const PackedPlan &p, unsigned int *status)
 {
     return packed_ok(p, status) ? p.hdr->n128 : 0;
+}
+
+// Descriptor of 64-row chunk k (k < m64), false past the chunks in use; the header's load and the
+// descriptor's are in flight together
+__device__ __forceinline__ bool packed_chunk64(const PackedPlan &p, int64_t k, unsigned int *status, int4 &d)
+{
+    if (k >= p.m64) return false;
+    d = __ldg(p.chunk64 + k);
+    return k < packed_n64(p, status);
 }
 
 struct PackedPlanParams {
@@ -196,6 +207,18 @@ __device__ __forceinline__ const float *window_start(const PackedScanParams &p, 
         if ((k64 ? s.c64 + s.n64 : s.c128 + s.n128) > c1) return p.ws_start + ((int64_t)window * p.H + h) * PN;
     }
     return p.h_in + ((int64_t)d.w * p.H + h) * PN;
+}
+
+// Let a kernel take up to `bytes` of dynamic shared memory, once per device (`done` is the kernel's own)
+template <typename F>
+inline bool allow_smem(F *kernel, int bytes, std::atomic<int> (&done)[64])
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (done[dev].load(std::memory_order_relaxed) >= bytes) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done[dev].store(bytes, std::memory_order_relaxed);
+    return true;
 }
 
 int launch_packed_plan(const PackedPlanParams &p, cudaStream_t st);

@@ -372,15 +372,15 @@ int ssd_decode_slots(const ssd_decode_slots_args *a, ssd_stream_t stream)
     p.h_in = a->h_in; p.h_out = a->h_out; p.y = a->y; p.ybs = a->y_batch_stride;
     p.dt_bias = a->dt_bias; p.dt_softplus = a->dt_softplus; p.dt_min = a->dt_min; p.dt_max = a->dt_max;
     p.wait_limit_ns = api_wait_limit_ns();
-    rc = launch_slot_decode(p, a->dtype, (cudaStream_t)stream);
+    rc = launch_slot_decode(p, a->dtype, api_sm_count(), (cudaStream_t)stream);
     if (rc == 6) return api_fail(SSD_ERR_UNSUPPORTED, "no GPU kernel for this shape (b=%d H=%d P=%d N=%d G=%d)", a->b, a->H, a->P, a->N, a->G);
     return rc ? cuda_fail("slot decode") : api_ok();
 }
 
-size_t ssd_gated_rmsnorm_backward_workspace_size(int64_t rows, int d, int dtype)
+size_t ssd_gated_rmsnorm_backward_workspace_size(int64_t rows, int d)
 {
     if (rows <= 0 || d <= 0 || d % 8 != 0 || d > 8192) return 0;
-    const NormBwdPlan pl = norm_bwd_plan(rows, d, dtype, api_sm_count());
+    const NormBwdPlan pl = norm_bwd_plan(rows, d, api_sm_count());
     return api_round256(sizeof(float) * (size_t)pl.grid * pl.teams * d);
 }
 
@@ -408,7 +408,7 @@ int ssd_gated_rmsnorm_backward(const ssd_gated_rmsnorm_bwd_args *a, ssd_stream_t
         return rc;
     if (!a->weight) return api_fail(SSD_ERR_NULL, "weight is NULL");
     if (!api_aligned(a->weight)) return api_fail(SSD_ERR_ALIGN, "weight must be 16-byte aligned");
-    const size_t need = ssd_gated_rmsnorm_backward_workspace_size(a->rows, d, a->dtype);
+    const size_t need = ssd_gated_rmsnorm_backward_workspace_size(a->rows, d);
     if ((rc = check_workspace(a->workspace, a->workspace_bytes, need))) return rc;
     NormBwdParams p{};
     p.y = a->y; p.yrs = a->y_row_stride; p.z = a->z; p.zrs = a->z_row_stride; p.dout = a->dout; p.dors = a->dout_row_stride;

@@ -4,9 +4,9 @@
 // where the rows before a sequence's first come from the 3-row buffer of its slot (zeros when it
 // does not resume), never from the sequence that lies before it in the tensor.
 //
-// Forward.  A thread owns one 16-byte vector of channels over kTok consecutive rows of a 64-row
-// chunk; its rows are loaded kAhead at a time into registers before any is used, which keeps 128 to
-// 256 KB of loads in flight per SM.  Every row is read once, plus three rows of halo per thread, and
+// Forward.  A thread owns one 16-byte vector of channels over the rows of a 64-row chunk; they stream
+// through its own kRing slots of shared memory by cp.async, which keeps 128 KB of loads in flight per SM
+// without holding registers.  Every row is read once, plus three rows of halo per thread, and
 // written once: the bound is the memory's rate.  The arithmetic and its order are the layer's
 // convolution's, so that a packed sequence gets the same v bit for bit.  The thread of a sequence's
 // first rows also writes its buffer: nobody else reads the slot's old one, so that tail_out may be
@@ -72,30 +72,45 @@ template <> struct ConvVec<float> {
     __device__ __forceinline__ static float silu(float z) { return z / (1.0f + expf(-z)); }
 };
 
-constexpr int kPackedConvThreads = 128;
-constexpr int kAhead = 8;
+constexpr int kPackedConvThreads = 256;
+constexpr int kRing = 16;          // rows in flight per thread
 
-template <typename T, int kTok>
-__global__ void __launch_bounds__(kPackedConvThreads) packed_conv_kernel(PackedConvParams p)
+__device__ __forceinline__ void cp_row(void *smem, const void *gmem)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <typename T>
+__global__ void __launch_bounds__(kPackedConvThreads, 2) packed_conv_kernel(PackedConvParams p)
 {
     using IO = ConvVec<T>;
     constexpr int V = IO::kN;
+    extern __shared__ Vec16p ring[];                        // [kRing][threads]
     const int ncv = p.C_ch / V;
     const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int c0 = (int)(gid % ncv) * V;
-    const int64_t part = gid / ncv;
-    const int64_t chunk = part / (64 / kTok);
-    const int r0 = (int)(part % (64 / kTok)) * kTok;
-    if (chunk >= packed_n64(p.plan, p.status)) return;
-    const int4 d = p.plan.chunk64[chunk];
-    const int n = min(kTok, (d.y & kChunkRows) - r0);
-    const bool head = (d.y & kChunkFirst) && r0 == 0;       // the first rows of a sequence (there may be none)
-    if (n <= 0 && !head) return;
+    const int64_t chunk = gid / ncv;
+    int4 d;
+    if (!packed_chunk64(p.plan, chunk, p.status, d)) return;
+    const int n = d.y & kChunkRows;
+    const bool head = (d.y & kChunkFirst) != 0;
     const T *u = reinterpret_cast<const T *>(p.u) + c0;
+    const int64_t t0 = d.x;
+    const T *up = u + t0 * p.urs;
+    Vec16p *slot = ring + threadIdx.x;
+    // one commit group per row (empty ones past the end keep the count uniform)
+#pragma unroll
+    for (int j = 0; j < kRing; ++j) {
+        if (j < n) cp_row(slot + j * kPackedConvThreads, up + j * p.urs);
+        cp_commit();
+    }
     const bool kept = d.w >= 0;
     const int64_t tail = kept ? (int64_t)d.w * 3 * p.C_ch + c0 : 0;
     const T *tin = (p.tail_in && kept && (d.y & kChunkResume)) ? reinterpret_cast<const T *>(p.tail_in) + tail : nullptr;
-    const int64_t t0 = (int64_t)d.x + r0;
     Vec16p m[3];                                            // rows t0 - 3 .. t0 - 1
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
@@ -103,26 +118,6 @@ __global__ void __launch_bounds__(kPackedConvThreads) packed_conv_kernel(PackedC
         else if (tin) m[k] = *reinterpret_cast<const Vec16p *>(tin + k * p.C_ch);
         else m[k] = Vec16p{{0u, 0u, 0u, 0u}};
     }
-    if (head && kept && p.tail_out) {
-        // the last three rows of the sequence, or of its old buffer and it when it is shorter
-        const PackedSeq s = p.plan.seqs[d.z];
-        T *to = reinterpret_cast<T *>(p.tail_out) + tail;
-        Vec16p o[3];
-#pragma unroll
-        for (int r = 0; r < 3; ++r) {
-            const int pos = s.len - 3 + r;                  // < 0: row 3 + pos of the old buffer
-            if (pos >= 0) o[r] = ld_rows(u + ((int64_t)s.row0 + pos) * p.urs);
-            else o[r] = pos == -3 ? m[0] : (pos == -2 ? m[1] : m[2]);
-        }
-#pragma unroll
-        for (int r = 0; r < 3; ++r) *reinterpret_cast<Vec16p *>(to + r * p.C_ch) = o[r];
-    }
-    if (n <= 0) return;
-    const T *up = u + t0 * p.urs;
-    Vec16p nx[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-        if (j < n) nx[j] = ld_rows(up + j * p.urs);
     float w0[V], w1[V], w2[V], w3[V], bs[V];
     const float4 *wp = reinterpret_cast<const float4 *>(p.w + (int64_t)c0 * 4);
 #pragma unroll
@@ -135,14 +130,35 @@ __global__ void __launch_bounds__(kPackedConvThreads) packed_conv_kernel(PackedC
     IO::unpack(m[0], m3);
     IO::unpack(m[1], m2);
     IO::unpack(m[2], m1);
-    T *vp = reinterpret_cast<T *>(p.v) + t0 * p.vrs + c0;
-    for (int i0 = 0; i0 < n; i0 += kAhead) {
+    if (head && kept && p.tail_out) {
+        // the last three rows of the sequence, or of its old buffer and it when it is shorter
+        const PackedSeq s = p.plan.seqs[d.z];
+        T *to = reinterpret_cast<T *>(p.tail_out) + tail;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
+        for (int r = 0; r < 3; ++r) {
+            const int pos = s.len - 3 + r;                  // < 0: row 3 + pos of the old buffer
+            Vec16p o;
+            if (pos >= 0) {
+                o = ld_rows(u + ((int64_t)s.row0 + pos) * p.urs);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o.w[e] = pos == -3 ? m[0].w[e] : (pos == -2 ? m[1].w[e] : m[2].w[e]);
+            }
+            *reinterpret_cast<Vec16p *>(to + r * p.C_ch) = o;
+        }
+    }
+    T *vp = reinterpret_cast<T *>(p.v) + t0 * p.vrs + c0;
+    up += kRing * p.urs;
+    for (int i0 = 0; i0 < n; i0 += kRing) {
+#pragma unroll
+        for (int j = 0; j < kRing; ++j) {
             if (i0 + j < n) {
+                cp_wait<kRing - 1>();                       // row i0 + j has landed (its group is the oldest)
                 float cur[V], out[V];
-                IO::unpack(nx[j], cur);
-                if (i0 + j + kAhead < n) nx[j] = ld_rows(up + (int64_t)(i0 + j + kAhead) * p.urs);
+                IO::unpack(slot[j * kPackedConvThreads], cur);
+                if (i0 + j + kRing < n) cp_row(slot + j * kPackedConvThreads, up);
+                cp_commit();
+                up += p.urs;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float z = bs[i];
@@ -158,16 +174,20 @@ __global__ void __launch_bounds__(kPackedConvThreads) packed_conv_kernel(PackedC
             }
         }
     }
+    cp_wait<0>();
 }
 
-template <typename T, int kTok>
-int launch_conv_tok(const PackedConvParams &p, cudaStream_t st)
+template <typename T>
+int launch_conv_t(const PackedConvParams &p, cudaStream_t st)
 {
-    const int64_t threads = p.plan.m64 * (64 / kTok) * (p.C_ch / ConvVec<T>::kN);
+    const int64_t threads = p.plan.m64 * (p.C_ch / ConvVec<T>::kN);
     const int64_t blocks = (threads + kPackedConvThreads - 1) / kPackedConvThreads;
     if (blocks > 0x7fffffffLL) return 2;
+    constexpr int smem = kRing * kPackedConvThreads * (int)sizeof(Vec16p);
+    static std::atomic<int> done[64];
+    if (!allow_smem(packed_conv_kernel<T>, smem, done)) return 7;
     prof_begin(st, kKPackedConv);
-    packed_conv_kernel<T, kTok><<<(unsigned)blocks, kPackedConvThreads, 0, st>>>(p);
+    packed_conv_kernel<T><<<(unsigned)blocks, kPackedConvThreads, smem, st>>>(p);
     prof_end(st, kKPackedConv);
     return cudaGetLastError() == cudaSuccess ? 0 : 7;
 }
@@ -179,10 +199,10 @@ int launch_conv_tok(const PackedConvParams &p, cudaStream_t st)
 // q < 0) reaches the rows t <= q + 3 through tap q - t + 3.
 // A thread owns 4 channels over a 64-row chunk and walks it forward with the window of u and of dz
 // in registers: du[t-3] is complete once dz[t] is, so it runs three rows past the chunk (recomputing
-// their dz) instead of handing dz between threads.  kBack rows of u (8 bytes) and dv (16 bytes) are
-// in registers before they are used.  dw and dbias are summed over the thread's rows in fp32, written
+// their dz) instead of handing dz between threads.  The next kBack rows of u and dv are on their
+// way while kBack rows are worked on.  dw and dbias are summed over the thread's rows in fp32, written
 // per chunk, and added over the chunks in a fixed order by a second kernel.
-constexpr int kBack = 8;
+constexpr int kBack = 4;
 constexpr int kConvBwdT = 128;
 
 __device__ __forceinline__ float4 ld4(const float *q) { return __ldg(reinterpret_cast<const float4 *>(q)); }
@@ -191,6 +211,18 @@ __device__ __forceinline__ float4 ld4(const __nv_bfloat16 *q)
     const uint2 v = __ldg(reinterpret_cast<const uint2 *>(q));
     return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
 }
+// 4 elements as loaded
+template <typename T> struct Raw4;
+template <> struct Raw4<float> {
+    float4 v;
+    __device__ __forceinline__ void load(const float *q) { v = __ldcs(reinterpret_cast<const float4 *>(q)); }
+    __device__ __forceinline__ float4 get() const { return v; }
+};
+template <> struct Raw4<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *q) { v = __ldg(reinterpret_cast<const uint2 *>(q)); }
+    __device__ __forceinline__ float4 get() const { return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)); }
+};
 
 __device__ __forceinline__ float dz1(float dv, float w0, float w1, float w2, float w3, float b, float a3, float a2,
                                      float a1, float a0)
@@ -207,29 +239,48 @@ __device__ __forceinline__ float dz1(float dv, float w0, float w1, float w2, flo
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kConvBwdT) packed_conv_bwd_kernel(PackedConvBwdParams p)
+__global__ void __launch_bounds__(kConvBwdT, 3) packed_conv_bwd_kernel(PackedConvBwdParams p)
 {
     const int np = p.C_ch >> 2;
     const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int c = 4 * (int)(gid % np);
     const int64_t chunk = gid / np;
-    if (chunk >= packed_n64(p.plan, p.status)) return;
-    const int4 d = p.plan.chunk64[chunk];
+    int4 d;
+    if (!packed_chunk64(p.plan, chunk, p.status, d)) return;
     const PackedSeq s = p.plan.seqs[d.z];
     const bool head = (d.y & kChunkFirst) != 0;
-    const int64_t t0 = d.x, t1 = t0 + (d.y & kChunkRows), se = (int64_t)s.row0 + s.len;
-    const T *u = reinterpret_cast<const T *>(p.u) + c;
+    const int64_t t0 = d.x, se = (int64_t)s.row0 + s.len;
+    const int n = d.y & kChunkRows;
+    const int nt = n > 0 ? n + 3 : 0;
+    const int nin = (int)min((int64_t)nt, se - t0);  // rows past the sequence's end have dz = 0
+    const T *u = reinterpret_cast<const T *>(p.u) + c + t0 * p.urs;
     // dv of 4 channels, all in one of x, B and C
     const float *dv;
     int64_t dvs;
     if (c < p.HP) { dv = p.dx + c; dvs = p.HP; }
     else if (c < p.HP + p.GN) { dv = p.dB + (c - p.HP); dvs = p.GN; }
     else { dv = p.dC + (c - p.HP - p.GN); dvs = p.GN; }
+    dv += t0 * dvs;
+    Raw4<T> un[kBack];
+    Raw4<float> dn[kBack];
+    auto fetch = [&](int b0) {
+#pragma unroll
+        for (int j = 0; j < kBack; ++j) {
+            if (b0 + j < nin) {
+                un[j].load(u + (int64_t)(b0 + j) * p.urs);
+                dn[j].load(dv + (int64_t)(b0 + j) * dvs);
+            } else {
+                un[j] = {};
+                dn[j] = {};
+            }
+        }
+    };
+    fetch(0);
     const bool resumed = p.tail_in && s.slot >= 0 && s.resume;
     const T *tin = resumed ? reinterpret_cast<const T *>(p.tail_in) + (int64_t)s.slot * 3 * p.C_ch + c : nullptr;
     const float4 z4 = make_float4(0.f, 0.f, 0.f, 0.f);
     float4 a3, a2, a1;                      // u[t-3], u[t-2], u[t-1]
-    if (!head) { a3 = ld4(u + (t0 - 3) * p.urs); a2 = ld4(u + (t0 - 2) * p.urs); a1 = ld4(u + (t0 - 1) * p.urs); }
+    if (!head) { a3 = ld4(u - 3 * p.urs); a2 = ld4(u - 2 * p.urs); a1 = ld4(u - p.urs); }
     else if (tin) { a3 = ld4(tin); a2 = ld4(tin + p.C_ch); a1 = ld4(tin + 2 * p.C_ch); }
     else { a3 = z4; a2 = z4; a1 = z4; }
     float wk[4][4];                         // [tap][channel]
@@ -243,66 +294,16 @@ __global__ void __launch_bounds__(kConvBwdT) packed_conv_bwd_kernel(PackedConvBw
     for (int i = 0; i < 4; ++i) bs[i] = p.bias ? __ldg(p.bias + c + i) : 0.0f;
     float gw[4][4] = {}, gb[4] = {};
     float e3[4] = {}, e2[4] = {}, e1[4] = {};       // dz[t-3], dz[t-2], dz[t-1] (zero before t0: those rows' du is another thread's)
-    float f0[4] = {}, f1[4] = {}, f2[4] = {};       // dz of the sequence's first three rows, for its buffer
-    const int n = (int)(t1 - t0);
-    const int nt = n > 0 ? n + 3 : 0;
-    const int nin = (int)min((int64_t)nt, se - t0);  // rows past the sequence's end have dz = 0
-    for (int b0 = 0; b0 < nt; b0 += kBack) {
-        float4 uu[kBack], dd[kBack];
-#pragma unroll
-        for (int j = 0; j < kBack; ++j) {
-            const bool in = b0 + j < nin;
-            uu[j] = in ? ld4(u + (t0 + b0 + j) * p.urs) : z4;
-            dd[j] = in ? ld4(dv + (t0 + b0 + j) * dvs) : z4;
-        }
-#pragma unroll
-        for (int j = 0; j < kBack; ++j) {
-            const int r = b0 + j;
-            if (r < nt) {
-                const float x3[4] = {a3.x, a3.y, a3.z, a3.w}, x2[4] = {a2.x, a2.y, a2.z, a2.w};
-                const float x1[4] = {a1.x, a1.y, a1.z, a1.w}, x0[4] = {uu[j].x, uu[j].y, uu[j].z, uu[j].w};
-                const float dvv[4] = {dd[j].x, dd[j].y, dd[j].z, dd[j].w};
-                float e0[4], g[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    e0[i] = r < nin ? dz1(dvv[i], wk[0][i], wk[1][i], wk[2][i], wk[3][i], bs[i], x3[i], x2[i], x1[i], x0[i]) : 0.0f;
-                    g[i] = fmaf(wk[0][i], e0[i], fmaf(wk[1][i], e1[i], fmaf(wk[2][i], e2[i], wk[3][i] * e3[i])));
-                    if (r < n) {
-                        gb[i] += e0[i];
-                        gw[0][i] = fmaf(e0[i], x3[i], gw[0][i]);
-                        gw[1][i] = fmaf(e0[i], x2[i], gw[1][i]);
-                        gw[2][i] = fmaf(e0[i], x1[i], gw[2][i]);
-                        gw[3][i] = fmaf(e0[i], x0[i], gw[3][i]);
-                    }
-                    if (r == 0) f0[i] = e0[i];
-                    if (r == 1) f1[i] = e0[i];
-                    if (r == 2) f2[i] = e0[i];
-                    e3[i] = e2[i]; e2[i] = e1[i]; e1[i] = e0[i];
-                }
-                if (r >= 3) {
-                    const int64_t t = t0 + r - 3;
-                    if (p.dtail_out && t >= se - 3) {
-                        const float4 q = ld4(p.dtail_out + ((int64_t)d.z * 3 + (t - (se - 3))) * p.C_ch + c);
-                        g[0] += q.x; g[1] += q.y; g[2] += q.z; g[3] += q.w;
-                    }
-                    *reinterpret_cast<float4 *>(p.du + t * p.C_ch + c) = make_float4(g[0], g[1], g[2], g[3]);
-                }
-                a3 = a2; a2 = a1; a1 = uu[j];
-            }
-        }
-    }
-    float4 *pw = reinterpret_cast<float4 *>(p.ws_dw) + chunk * p.C_ch + c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pw[i] = make_float4(gw[0][i], gw[1][i], gw[2][i], gw[3][i]);
-    *reinterpret_cast<float4 *>(p.ws_db + chunk * p.C_ch + c) = make_float4(gb[0], gb[1], gb[2], gb[3]);
-    if (head && p.dtail_in) {
+    float *du = p.du + t0 * p.C_ch + c;
+    // the gradient of the buffer that the sequence starts from, with dz of its first three rows in e1, e2, e3
+    auto put_tail = [&]() {
         float g[3][4] = {};
         if (resumed) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                g[0][i] = wk[0][i] * f0[i];
-                g[1][i] = fmaf(wk[1][i], f0[i], wk[0][i] * f1[i]);
-                g[2][i] = fmaf(wk[2][i], f0[i], fmaf(wk[1][i], f1[i], wk[0][i] * f2[i]));
+                g[0][i] = wk[0][i] * e3[i];
+                g[1][i] = fmaf(wk[1][i], e3[i], wk[0][i] * e2[i]);
+                g[2][i] = fmaf(wk[2][i], e3[i], fmaf(wk[1][i], e2[i], wk[0][i] * e1[i]));
             }
             if (p.dtail_out) {
                 // a sequence of fewer than three rows hands rows of its old buffer on
@@ -320,7 +321,56 @@ __global__ void __launch_bounds__(kConvBwdT) packed_conv_bwd_kernel(PackedConvBw
         for (int q = 0; q < 3; ++q)
             *reinterpret_cast<float4 *>(p.dtail_in + ((int64_t)d.z * 3 + q) * p.C_ch + c) =
                 make_float4(g[q][0], g[q][1], g[q][2], g[q][3]);
+    };
+    if (n == 0 && head && p.dtail_in) put_tail();
+#pragma unroll 1
+    for (int b0 = 0; b0 < nt; b0 += kBack) {
+        Raw4<T> uc[kBack];
+        Raw4<float> dc[kBack];
+#pragma unroll
+        for (int j = 0; j < kBack; ++j) { uc[j] = un[j]; dc[j] = dn[j]; }
+        if (b0 + kBack < nt) fetch(b0 + kBack);
+#pragma unroll
+        for (int j = 0; j < kBack; ++j) {
+            const int r = b0 + j;
+            if (r < nt) {
+                const float4 uu = uc[j].get(), dd = dc[j].get();
+                const float x3[4] = {a3.x, a3.y, a3.z, a3.w}, x2[4] = {a2.x, a2.y, a2.z, a2.w};
+                const float x1[4] = {a1.x, a1.y, a1.z, a1.w}, x0[4] = {uu.x, uu.y, uu.z, uu.w};
+                const float dvv[4] = {dd.x, dd.y, dd.z, dd.w};
+                float g[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // (a row past the sequence's end has dv = 0, its window may be anything finite: cleared)
+                    float e0 = dz1(dvv[i], wk[0][i], wk[1][i], wk[2][i], wk[3][i], bs[i], x3[i], x2[i], x1[i], x0[i]);
+                    e0 = r < nin ? e0 : 0.0f;
+                    g[i] = fmaf(wk[0][i], e0, fmaf(wk[1][i], e1[i], fmaf(wk[2][i], e2[i], wk[3][i] * e3[i])));
+                    if (r < n) {
+                        gb[i] += e0;
+                        gw[0][i] = fmaf(e0, x3[i], gw[0][i]);
+                        gw[1][i] = fmaf(e0, x2[i], gw[1][i]);
+                        gw[2][i] = fmaf(e0, x1[i], gw[2][i]);
+                        gw[3][i] = fmaf(e0, x0[i], gw[3][i]);
+                    }
+                    e3[i] = e2[i]; e2[i] = e1[i]; e1[i] = e0;
+                }
+                if (r == 2 && head && p.dtail_in) put_tail();
+                if (r >= 3) {
+                    const int64_t back = t0 + r - 3 - (se - 3);     // row of the buffer handed on that du's row is
+                    if (p.dtail_out && back >= 0) {
+                        const float4 q = ld4(p.dtail_out + ((int64_t)d.z * 3 + back) * p.C_ch + c);
+                        g[0] += q.x; g[1] += q.y; g[2] += q.z; g[3] += q.w;
+                    }
+                    __stcs(reinterpret_cast<float4 *>(du + (int64_t)(r - 3) * p.C_ch), make_float4(g[0], g[1], g[2], g[3]));
+                }
+                a3 = a2; a2 = a1; a1 = uu;
+            }
+        }
     }
+    float4 *pw = reinterpret_cast<float4 *>(p.ws_dw) + chunk * p.C_ch + c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pw[i] = make_float4(gw[0][i], gw[1][i], gw[2][i], gw[3][i]);
+    *reinterpret_cast<float4 *>(p.ws_db + chunk * p.C_ch + c) = make_float4(gb[0], gb[1], gb[2], gb[3]);
 }
 
 // dw and dbias: the chunks' sums, added in a fixed order.  A CTA takes 32 channels; each of its 16
@@ -371,7 +421,7 @@ __global__ void __launch_bounds__(32 * kRedWarps) packed_conv_reduce_kernel(Pack
 int launch_packed_conv(const PackedConvParams &p, int dtype, cudaStream_t st)
 {
     if (p.plan.m64 == 0) return 0;
-    return dtype == 1 ? launch_conv_tok<__nv_bfloat16, 64>(p, st) : launch_conv_tok<float, 64>(p, st);
+    return dtype == 1 ? launch_conv_t<__nv_bfloat16>(p, st) : launch_conv_t<float>(p, st);
 }
 
 int launch_packed_conv_backward(const PackedConvBwdParams &p, int dtype, cudaStream_t st)

@@ -184,15 +184,8 @@ int launch_packed_plan(const PackedPlanParams &p, cudaStream_t st)
     int hash = 64;
     if (p.slots) while (hash < 2 * p.nseq) hash *= 2;
     const int smem = p.slots ? hash * (int)sizeof(int) : 0;
-    static std::atomic<bool> attr_set[64];   // set once per device (a repeat is harmless)
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        if (cudaFuncSetAttribute(packed_seq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 2 * kPackedMaxSlotted * (int)sizeof(int)) != cudaSuccess)
-            return 7;
-        attr_set[dev] = true;
-    }
+    static std::atomic<int> done[64];
+    if (!allow_smem(packed_seq_kernel, 2 * kPackedMaxSlotted * (int)sizeof(int), done)) return 7;
     prof_begin(st, kKPackedPlan);
     packed_seq_kernel<<<1, kPlanThreads, smem, st>>>(p, reinterpret_cast<PackedSeq *>(b + l.off_seq), hash);
     if (l.m64 > 0)

@@ -919,15 +919,8 @@ int launch_packed_scan_tc(const PackedScanParams &p, bool carry, cudaStream_t st
         (!encode_bf16(enc, &maps.x, p.x, hp, rows, 1, p.xrs, 0) || !encode_bf16(enc, &maps.B, p.B, gn, rows, 1, p.Brs, 0) ||
          !encode_bf16(enc, &maps.C, p.C, gn, rows, 1, p.Crs, 0) || !encode_bf16(enc, &maps.y, p.y, hp, rows, 1, p.yrs, 0)))
         return 6;
-    static std::atomic<bool> attr_set[64];   // set once per device (a repeat is harmless)
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        if (cudaFuncSetAttribute(packed_state_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemA) != cudaSuccess ||
-            cudaFuncSetAttribute(packed_output_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemC) != cudaSuccess)
-            return 7;
-        attr_set[dev] = true;
-    }
+    static std::atomic<int> done_a[64], done_c[64];
+    if (!allow_smem(packed_state_tc_kernel, (int)kSmemA, done_a) || !allow_smem(packed_output_tc_kernel, (int)kSmemC, done_c)) return 7;
     const unsigned units = (unsigned)p.nw * (unsigned)(p.H / 2);
     if (carry && p.nw > 1) {
         prof_begin(st, kKPackedState);

@@ -22,11 +22,11 @@ struct SlotDecodeParams {
     const float *dt_bias;
     int dt_softplus;
     float dt_min, dt_max;
-    int heads_per_cta;          // set by the launcher
+    int heads_per_cta, stages;  // set by the launcher
     unsigned int *status;
     uint64_t wait_limit_ns;
 };
 
-int launch_slot_decode(SlotDecodeParams p, int dtype, cudaStream_t st);
+int launch_slot_decode(SlotDecodeParams p, int dtype, int sms, cudaStream_t st);
 
 }  // namespace ssd

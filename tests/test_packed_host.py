@@ -145,29 +145,44 @@ def test_nothing_to_do_is_no_error(ssd):
 
 
 def test_binding_refuses_host_tensors_and_wrong_shapes(ssd):
+    cpu, f32 = torch.device("cpu"), torch.float32
     cu = torch.tensor([0, 3], dtype=torch.int32)
     with pytest.raises(ValueError):
         ssd.packed_plan(cu, 3)
     with pytest.raises(ValueError):
         ssd.gated_rmsnorm_backward(torch.zeros(2, 8), torch.zeros(2, 8), torch.zeros(2, 8), torch.ones(8))
     with pytest.raises(ValueError):
-        ssd._rows2(torch.zeros(4, 6), 8, torch.float32, "u")
+        ssd._rows2(torch.zeros(4, 6), 4, 8, f32, cpu, "u")
+    with pytest.raises(ValueError):
+        ssd._rows2(torch.zeros(4, 8), 5, 8, f32, cpu, "u")
     with pytest.raises(TypeError):
-        ssd._rows2(torch.zeros(4, 8), 8, torch.bfloat16, "u")
+        ssd._rows2(torch.zeros(4, 8), 4, 8, torch.bfloat16, cpu, "u")
     with pytest.raises(ValueError):
-        ssd._rows2(torch.zeros(8, 4).t(), 8, torch.float32, "u")
+        ssd._rows2(torch.zeros(8, 4).t(), 4, 8, f32, cpu, "u")
     with pytest.raises(ValueError):
-        ssd._full(torch.zeros(3), (4,), torch.float32, "A")
+        ssd._rows2(torch.zeros(4, 8), 4, 8, f32, torch.device("cuda:0"), "u")
     with pytest.raises(ValueError):
-        ssd._head_dims(torch.zeros(4, 10), torch.zeros(4, 8), torch.zeros(4, 8), 3, 1)
+        ssd._ptr_of(torch.zeros(3), (4,), f32, cpu, "A")
+    with pytest.raises(TypeError):
+        ssd._ptr_of(torch.zeros(4, 2).t(), (2, 4), f32, cpu, "A")
+    with pytest.raises(TypeError):
+        ssd._ptr_of(torch.zeros(4, dtype=torch.float64), (4,), f32, cpu, "A")
+    with pytest.raises(ValueError):
+        ssd._ptr_of(torch.zeros(4), (4,), f32, torch.device("cuda:1"), "A")
+    assert ssd._ptr_of(None, (4,), f32, cpu, "A") is None
+    with pytest.raises(ValueError):
+        ssd._head_dims(torch.zeros(4, 10), torch.zeros(4, 8), 3, 1)
 
 
 def test_rows_of_a_view(ssd):
     """Column slices keep their row stride; one row takes its width, whatever stride it carries."""
+    cpu, f32 = torch.device("cpu"), torch.float32
     t = torch.zeros(4, 32)
-    assert ssd._rows2(t[:, 8:16], 8, torch.float32, "u") == (t.data_ptr() + 32, 32)
-    assert ssd._rows2(t[:1, :8], 8, torch.float32, "u") == (t.data_ptr(), 8)
+    assert ssd._rows2(t[:, 8:16], 4, 8, f32, cpu, "u") == (t.data_ptr() + 32, 32)
+    assert ssd._rows2(t[:1, :8], 1, 8, f32, cpu, "u") == (t.data_ptr(), 8)
     y = torch.zeros(4, 2, 8)
-    assert ssd._rows3(y, 2, 8, torch.float32, "y") == (y.data_ptr(), 16)
+    assert ssd._rows3(y, 4, 2, 8, f32, cpu, "y") == (y.data_ptr(), 16)
+    wide = torch.zeros(4, 5, 8)
+    assert ssd._rows3(wide[:, 1:3], 4, 2, 8, f32, cpu, "y") == (wide.data_ptr() + 32, 40)
     with pytest.raises(ValueError):
-        ssd._rows3(y.transpose(1, 2), 8, 2, torch.float32, "y")
+        ssd._rows3(y.transpose(1, 2), 4, 8, 2, f32, cpu, "y")
