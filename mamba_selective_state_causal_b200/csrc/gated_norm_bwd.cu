@@ -4,9 +4,8 @@
 //   silu(z) = z sg,  silu'(z) = sg (1 + z (1 - sg)),  sg = 1 / (1 + e^-z).
 // A row is read once (y, z, dout) and written once (dy, dz): 5 d elements, the memory's rate is the
 // bound.  A thread owns 8 channels; its pieces of the next kDepth rows stream by cp.async through its own
-// slots of shared memory (48 KB per CTA, four CTAs per SM), where they stay between the two sums over
-// the group (of v^2 and of g v, both at once, in a fixed order) and the outputs, so that loads never
-// wait for a sum and hold no registers.  Its share of dw stays in 8 registers over all the rows that
+// slots of shared memory (48 KB per CTA, two CTAs per SM), so that loads never wait for the two sums
+// over the group (of v^2 and of g v, both at once, in a fixed order).  Its share of dw stays in 8 registers over all the rows that
 // its CTA walks, is written once per CTA, and is added over the
 // CTAs by a second kernel in a fixed order: no atomics, the same result every time.
 // Sums over a group: of 8 m channels, m threads.  m a power of two up to 32: shuffles among those
@@ -73,9 +72,11 @@ __device__ __forceinline__ float sigma(float z)
 
 // One CTA: `teams` rows side by side, d / 8 threads each; it walks the rows blockIdx.x * teams + team, a grid apart.
 // kMode: 0 groups of a power of two up to 32 threads, 1 of a multiple of 32, 2 any.
-// kMost bounds the threads (rows wider than 2048 channels need up to 1024).
+// kMost bounds the threads (rows wider than 2048 channels need up to 1024).  Two CTAs of 256 threads per SM leave
+// the 128 registers that a thread needs: 222 us at 65536 rows of 2048 in bf16 (6.0 TB/s), against 294 with
+// three (80 registers, a few of them spilled) and 335 with four.
 template <typename T, int kMode, int kMost>
-__global__ void __launch_bounds__(kMost, 1024 / kMost) gated_norm_bwd_kernel(NormBwdParams p, int teams)
+__global__ void __launch_bounds__(kMost, kMost == 256 ? 2 : 1) gated_norm_bwd_kernel(NormBwdParams p, int teams)
 {
     extern __shared__ __align__(16) uint8_t raw[];
     constexpr int D = kDepth<T>;
@@ -94,60 +95,80 @@ __global__ void __launch_bounds__(kMost, 1024 / kMost) gated_norm_bwd_kernel(Nor
     }
     const int64_t step = (int64_t)gridDim.x * teams;
     const int64_t r0 = (int64_t)blockIdx.x * teams + team;
-    // the rows of every team in step: the CTA's first row decides the number of turns
+    // the rows of every team in step: the CTA's first row decides the number of turns, its own this thread's
     const int64_t first = (int64_t)blockIdx.x * teams;
-    const int64_t turns = first < p.rows ? (p.rows - first + step - 1) / step : 0;
-    auto fetch = [&](int64_t k) {
-        const int64_t r = r0 + k * step;
-        if (live && k < turns && r < p.rows) {
-            Vec8<T> *q = ring + (int)(k % D) * 3 * blockDim.x;
-            q[0].fetch(reinterpret_cast<const T *>(p.y) + r * p.yrs + kV * i);
-            q[blockDim.x].fetch(reinterpret_cast<const T *>(p.z) + r * p.zrs + kV * i);
-            q[2 * blockDim.x].fetch(reinterpret_cast<const T *>(p.dout) + r * p.dors + kV * i);
+    const int turns = first < p.rows ? (int)((p.rows - first + step - 1) / step) : 0;
+    const int mine = live && r0 < p.rows ? (int)((p.rows - r0 + step - 1) / step) : 0;
+    const T *yp = reinterpret_cast<const T *>(p.y) + r0 * p.yrs + kV * i, *zp = reinterpret_cast<const T *>(p.z) + r0 * p.zrs + kV * i;
+    const T *op = reinterpret_cast<const T *>(p.dout) + r0 * p.dors + kV * i;
+    T *dyp = reinterpret_cast<T *>(p.dy) + r0 * p.dyrs + kV * i, *dzp = reinterpret_cast<T *>(p.dz) + r0 * p.dzrs + kV * i;
+    const int64_t ys = step * p.yrs, zs = step * p.zrs, os = step * p.dors, dys = step * p.dyrs, dzs = step * p.dzrs;
+    const int nt = blockDim.x;
+    auto fetch = [&](int k) {                    // rows are fetched in order: the pointers step along
+        if (k < mine) {
+            Vec8<T> *q = ring + (k % D) * 3 * nt;
+            q[0].fetch(yp);
+            q[nt].fetch(zp);
+            q[2 * nt].fetch(op);
+            yp += ys; zp += zs; op += os;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
     for (int k = 0; k < D; ++k) fetch(k);
-    for (int64_t k = 0; k < turns; ++k) {
-        const int64_t r = r0 + k * step;
-        const bool on = live && r < p.rows;
-        const Vec8<T> *q = ring + (int)(k % D) * 3 * blockDim.x;
+#pragma unroll 1
+    for (int k = 0; k < turns; ++k) {
+        const bool on = k < mine;
+        const Vec8<T> *q = ring + (k % D) * 3 * nt;
         asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");    // row k's group is the oldest
         float2 s = make_float2(0.f, 0.f);        // sums of v^2 and g v
-        float2 sg[4], si[4];                     // sigma(z) and silu(z) of 4 pairs of channels, until the outputs
+        // until the outputs: sigma(z), silu(z), y and g of 4 pairs of channels
+        float2 sg[4], si[4], y2[4], o2[4];
         if (on) {
             float y[8], z[8], o[8];
-            q[0].get(y); q[blockDim.x].get(z); q[2 * blockDim.x].get(o);
+            q[0].get(y); q[nt].get(z); q[2 * nt].get(o);
             float2 vv = make_float2(0.f, 0.f), gv = vv;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
+                y2[e] = make_float2(y[2 * e], y[2 * e + 1]);
+                o2[e] = make_float2(o[2 * e], o[2 * e + 1]);
                 sg[e] = make_float2(sigma(z[2 * e]), sigma(z[2 * e + 1]));
                 si[e] = __fmul2_rn(make_float2(z[2 * e], z[2 * e + 1]), sg[e]);
-                const float2 v = __fmul2_rn(make_float2(y[2 * e], y[2 * e + 1]), si[e]);
+                const float2 v = __fmul2_rn(y2[e], si[e]);
                 vv = __ffma2_rn(v, v, vv);
-                gv = __ffma2_rn(__fmul2_rn(make_float2(o[2 * e], o[2 * e + 1]), wv[e]), v, gv);
+                gv = __ffma2_rn(__fmul2_rn(o2[e], wv[e]), v, gv);
             }
             s = make_float2(vv.x + vv.y, gv.x + gv.y);
         }
-        if (kMode <= 1) {
-            const int span = kMode == 0 ? m : 32;
-#pragma unroll
-            for (int o = 1; o < span; o <<= 1) {
+        fetch(k + D);                            // into the slots just read, which are this thread's own
+        if (kMode == 0) {
+            for (int o = 1; o < m; o <<= 1) {
                 s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
                 s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
             }
         }
         if (kMode == 1) {
-            float2 *b = part + (k & 1) * warps;  // two in turn: one barrier per row
-            if (lane == 0) b[warp] = s;
+            // half of the lanes sum v^2, the other half g v: 5 exchanges for the two sums
+            const bool up = (lane & 16) != 0;
+            float t = up ? s.y : s.x;
+            t += __shfl_xor_sync(0xffffffffu, up ? s.x : s.y, 16);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            float *b = reinterpret_cast<float *>(part + (k & 1) * warps);    // two in turn: one barrier per row
+            if ((lane & 15) == 0) b[2 * warp + (up ? 1 : 0)] = t;
             __syncthreads();
-            const int mw = m / 32, w0 = warp / mw * mw;
-            s = make_float2(0.f, 0.f);
-            for (int e = 0; e < mw; ++e) { const float2 t = b[w0 + e]; s.x += t.x; s.y += t.y; }
+            const int mw = m / 32;
+            const float2 *b2 = part + (k & 1) * warps + warp / mw * mw;
+            s = b2[0];
+            if (mw == 8) {
+#pragma unroll
+                for (int e = 1; e < 8; ++e) s = __fadd2_rn(s, b2[e]);
+            } else {
+                for (int e = 1; e < mw; ++e) s = __fadd2_rn(s, b2[e]);
+            }
         }
         if (kMode == 2) {
-            float2 *b = part + (k & 1) * blockDim.x;
+            float2 *b = part + (k & 1) * nt;
             b[threadIdx.x] = s;
             __syncthreads();
             if (live) {
@@ -157,28 +178,26 @@ __global__ void __launch_bounds__(kMost, 1024 / kMost) gated_norm_bwd_kernel(Nor
             }
         }
         if (on) {
-            float y[8], o[8], a[8], b[8];
-            q[0].get(y); q[2 * blockDim.x].get(o);
-            const float rs = 1.0f / sqrtf(fmaf(s.x, inv, p.eps));
+            float a[8], b[8];
+            const float rs = rsqrtf(fmaf(s.x, inv, p.eps));
             const float c = -rs * rs * (s.y * inv);
             const float2 rs2 = make_float2(rs, rs), c2 = make_float2(c, c);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 y2 = make_float2(y[2 * e], y[2 * e + 1]), o2 = make_float2(o[2 * e], o[2 * e + 1]);
-                const float2 v = __fmul2_rn(y2, si[e]);
-                const float2 dv = __fmul2_rn(rs2, __ffma2_rn(v, c2, __fmul2_rn(o2, wv[e])));
+                const float2 v = __fmul2_rn(y2[e], si[e]);
+                const float2 dv = __fmul2_rn(rs2, __ffma2_rn(v, c2, __fmul2_rn(o2[e], wv[e])));
                 const float2 da = __fmul2_rn(dv, si[e]);
                 // silu'(z) = sg + si (1 - sg)
                 const float2 one = make_float2(1.0f - sg[e].x, 1.0f - sg[e].y);
-                const float2 db = __fmul2_rn(__fmul2_rn(dv, y2), __ffma2_rn(si[e], one, sg[e]));
+                const float2 db = __fmul2_rn(__fmul2_rn(dv, y2[e]), __ffma2_rn(si[e], one, sg[e]));
                 a[2 * e] = da.x; a[2 * e + 1] = da.y;
                 b[2 * e] = db.x; b[2 * e + 1] = db.y;
-                dw[e] = __ffma2_rn(__fmul2_rn(o2, rs2), v, dw[e]);
+                dw[e] = __ffma2_rn(__fmul2_rn(o2[e], rs2), v, dw[e]);
             }
-            Vec8<T>::put(reinterpret_cast<T *>(p.dy) + r * p.dyrs + kV * i, a);
-            Vec8<T>::put(reinterpret_cast<T *>(p.dz) + r * p.dzrs + kV * i, b);
+            Vec8<T>::put(dyp, a);
+            Vec8<T>::put(dzp, b);
+            dyp += dys; dzp += dzs;
         }
-        fetch(k + D);                            // into the slots just read, which are this thread's own
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (live) {
@@ -244,7 +263,7 @@ int launch_t(const NormBwdParams &p, const NormBwdPlan &pl, cudaStream_t st)
 }  // namespace
 
 // Threads: whole rows side by side up to 256 threads (wider rows: their own d / 8), rounded up to
-// warps.  Grid: the 1024 threads that fit an SM, on each of them, and no more than there are rows.
+// warps.  Grid: the 512 threads that fit an SM, on each of them, and no more than there are rows.
 NormBwdPlan norm_bwd_plan(int64_t rows, int d, int sms)
 {
     NormBwdPlan pl;
@@ -252,7 +271,7 @@ NormBwdPlan norm_bwd_plan(int64_t rows, int d, int sms)
     pl.teams = std::max(1, 256 / per);
     pl.threads = (pl.teams * per + 31) / 32 * 32;
     const int64_t need = (rows + pl.teams - 1) / pl.teams;
-    pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(need, (int64_t)sms * std::max(1, 1024 / pl.threads)));
+    pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(need, (int64_t)sms * std::max(1, 512 / pl.threads)));
     return pl;
 }
 
