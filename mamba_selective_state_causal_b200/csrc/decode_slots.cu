@@ -10,7 +10,7 @@
 // the new conv buffer be written in the same launch, over the old one: B's and C's channels are read
 // by all CTAs of the stream, and the barrier that every CTA arrives at after reading them (and waits
 // for only before it writes) comes long after.  A state moves in two halves of P / 2 rows (16 KB at P = 64,
-// N = 128), four in flight per CTA and three CTAs per SM (all of them, up to 16, where the batch is so small
+// N = 128), three in flight per CTA and four CTAs per SM (all of them, up to 16, where the batch is so small
 // that a CTA has its SM to itself); a buffer is refilled one piece after its
 // copy out was started, so that nobody waits for that copy to have read it.  v is not rounded to the I/O type here: it stays in
 // registers and shared memory, where the layer's packed convolution stores it.
@@ -277,9 +277,9 @@ int launch_slot_decode(SlotDecodeParams p, int dtype, int sms, cudaStream_t st)
     const size_t small = sizeof(float) * ((size_t)p.heads_per_cta * (p.P + 4) + (size_t)groups * 2 * p.N);
     const size_t piece = sizeof(float) * (size_t)(p.P / 2) * p.N;
     const size_t room = 200 * 1024;
-    if (small + 4 * piece > room) return 6;
+    if (small + 3 * piece > room) return 6;
     const int np = 2 * p.heads_per_cta;
-    p.stages = p.b * cluster <= sms ? (int)std::min<size_t>(std::min(np, kMaxStages), (room - small) / piece) : std::min(np, 4);
+    p.stages = p.b * cluster <= sms ? (int)std::min<size_t>(std::min(np, kMaxStages), (room - small) / piece) : std::min(np, 3);
     const size_t smem = p.stages * piece + small;
     if ((2 * p.G * p.N + cluster - 1) / cluster > 4 * kSlotThreads) return 6;
     if ((int64_t)p.b * cluster > 0x7fffffffLL) return 6;

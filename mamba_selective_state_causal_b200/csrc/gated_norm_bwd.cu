@@ -60,16 +60,6 @@ template <> struct Vec8<float> {
 };
 template <typename T> constexpr int kDepth = 96 / (3 * (int)sizeof(Vec8<T>)) * 2;   // 4 rows of bf16, 2 of fp32: 192 bytes per thread
 
-// sigma(z) through the hardware's exponential and reciprocal (2 units in the last place each); e^-z beyond the
-// range of fp32 is infinite, and sigma 0
-__device__ __forceinline__ float sigma(float z)
-{
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return r;
-}
-
 // One CTA: `teams` rows side by side, d / 8 threads each; it walks the rows blockIdx.x * teams + team, a grid apart.
 // kMode: 0 groups of a power of two up to 32 threads, 1 of a multiple of 32, 2 any.
 // kMost bounds the threads (rows wider than 2048 channels need up to 1024).  Two CTAs of 256 threads per SM leave
@@ -132,7 +122,7 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 2 : 1) gated_norm_bwd_ke
             for (int e = 0; e < 4; ++e) {
                 y2[e] = make_float2(y[2 * e], y[2 * e + 1]);
                 o2[e] = make_float2(o[2 * e], o[2 * e + 1]);
-                sg[e] = make_float2(sigma(z[2 * e]), sigma(z[2 * e + 1]));
+                sg[e] = make_float2(sigma_fast(z[2 * e]), sigma_fast(z[2 * e + 1]));
                 si[e] = __fmul2_rn(make_float2(z[2 * e], z[2 * e + 1]), sg[e]);
                 const float2 v = __fmul2_rn(y2[e], si[e]);
                 vv = __ffma2_rn(v, v, vv);

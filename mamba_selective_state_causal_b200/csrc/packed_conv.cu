@@ -199,10 +199,10 @@ int launch_conv_t(const PackedConvParams &p, cudaStream_t st)
 // q < 0) reaches the rows t <= q + 3 through tap q - t + 3.
 // A thread owns 4 channels over a 64-row chunk and walks it forward with the window of u and of dz
 // in registers: du[t-3] is complete once dz[t] is, so it runs three rows past the chunk (recomputing
-// their dz) instead of handing dz between threads.  The next kBack rows of u and dv are on their
-// way while kBack rows are worked on.  dw and dbias are summed over the thread's rows in fp32, written
+// their dz) instead of handing dz between threads.  Its rows of u and dv stream through its own kBack
+// slots of shared memory by cp.async (72 KB in flight per SM, no registers held).  dw and dbias are summed over the thread's rows in fp32, written
 // per chunk, and added over the chunks in a fixed order by a second kernel.
-constexpr int kBack = 4;
+constexpr int kBack = 8;
 constexpr int kConvBwdT = 128;
 
 __device__ __forceinline__ float4 ld4(const float *q) { return __ldg(reinterpret_cast<const float4 *>(q)); }
@@ -211,36 +211,47 @@ __device__ __forceinline__ float4 ld4(const __nv_bfloat16 *q)
     const uint2 v = __ldg(reinterpret_cast<const uint2 *>(q));
     return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
 }
-// 4 elements as loaded
+// 4 elements of u in shared memory
 template <typename T> struct Raw4;
 template <> struct Raw4<float> {
     float4 v;
-    __device__ __forceinline__ void load(const float *q) { v = __ldcs(reinterpret_cast<const float4 *>(q)); }
     __device__ __forceinline__ float4 get() const { return v; }
 };
 template <> struct Raw4<__nv_bfloat16> {
     uint2 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *q) { v = __ldg(reinterpret_cast<const uint2 *>(q)); }
     __device__ __forceinline__ float4 get() const { return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)); }
 };
-
-__device__ __forceinline__ float dz1(float dv, float w0, float w1, float w2, float w3, float b, float a3, float a2,
-                                     float a1, float a0)
+template <int kBytes>
+__device__ __forceinline__ void cp_small(void *dst, const void *src)
 {
-    float z = b;
-    z = fmaf(w0, a3, z);
-    z = fmaf(w1, a2, z);
-    z = fmaf(w2, a1, z);
-    z = fmaf(w3, a0, z);
-    // sigma through the hardware exponential (relative error about 2^-21); -z is clamped so that the
-    // divisor stays below 2^126 (sigma is below 2e-35 there either way)
-    const float sg = __fdividef(1.0f, 1.0f + __expf(fminf(-z, 80.0f)));
-    return dv * (sg * fmaf(z, 1.0f - sg, 1.0f));
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "n"(kBytes)
+                 : "memory");
+}
+
+// two channels at a time (packed fp32 instructions: the arithmetic is what bounds this kernel)
+struct F2x2 {
+    float2 a, b;
+};
+__device__ __forceinline__ F2x2 pairs(float4 v) { return F2x2{make_float2(v.x, v.y), make_float2(v.z, v.w)}; }
+
+// dz = dv sg (1 + z (1 - sg)), sg = sigma(z), z from the window x3 .. x0
+__device__ __forceinline__ float2 dz2(float2 dv, const float2 (&w)[4], float2 b, float2 x3, float2 x2, float2 x1, float2 x0)
+{
+    float2 z = __ffma2_rn(w[0], x3, b);
+    z = __ffma2_rn(w[1], x2, z);
+    z = __ffma2_rn(w[2], x1, z);
+    z = __ffma2_rn(w[3], x0, z);
+    const float2 sg = make_float2(sigma_fast(z.x), sigma_fast(z.y));
+    const float2 f = __ffma2_rn(z, make_float2(1.0f - sg.x, 1.0f - sg.y), make_float2(1.0f, 1.0f));
+    return __fmul2_rn(dv, __fmul2_rn(sg, f));
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kConvBwdT, 3) packed_conv_bwd_kernel(PackedConvBwdParams p)
 {
+    extern __shared__ __align__(16) uint8_t cbr[];
+    float4 *rd = reinterpret_cast<float4 *>(cbr) + threadIdx.x;                                  // [kBack][threads] dv
+    Raw4<T> *ru = reinterpret_cast<Raw4<T> *>(cbr + sizeof(float4) * kBack * kConvBwdT) + threadIdx.x;   // [kBack][threads] u
     const int np = p.C_ch >> 2;
     const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int c = 4 * (int)(gid % np);
@@ -249,10 +260,10 @@ __global__ void __launch_bounds__(kConvBwdT, 3) packed_conv_bwd_kernel(PackedCon
     if (!packed_chunk64(p.plan, chunk, p.status, d)) return;
     const PackedSeq s = p.plan.seqs[d.z];
     const bool head = (d.y & kChunkFirst) != 0;
-    const int64_t t0 = d.x, se = (int64_t)s.row0 + s.len;
+    const int64_t t0 = d.x;
     const int n = d.y & kChunkRows;
-    const int nt = n > 0 ? n + 3 : 0;
-    const int nin = (int)min((int64_t)nt, se - t0);  // rows past the sequence's end have dz = 0
+    const int left = (int)((int64_t)s.row0 + s.len - t0);   // rows to the sequence's end
+    const int nin = n > 0 ? min(n + 3, left) : 0;           // rows past the sequence's end have dz = 0
     const T *u = reinterpret_cast<const T *>(p.u) + c + t0 * p.urs;
     // dv of 4 channels, all in one of x, B and C
     const float *dv;
@@ -261,116 +272,127 @@ __global__ void __launch_bounds__(kConvBwdT, 3) packed_conv_bwd_kernel(PackedCon
     else if (c < p.HP + p.GN) { dv = p.dB + (c - p.HP); dvs = p.GN; }
     else { dv = p.dC + (c - p.HP - p.GN); dvs = p.GN; }
     dv += t0 * dvs;
-    Raw4<T> un[kBack];
-    Raw4<float> dn[kBack];
-    auto fetch = [&](int b0) {
-#pragma unroll
-        for (int j = 0; j < kBack; ++j) {
-            if (b0 + j < nin) {
-                un[j].load(u + (int64_t)(b0 + j) * p.urs);
-                dn[j].load(dv + (int64_t)(b0 + j) * dvs);
-            } else {
-                un[j] = {};
-                dn[j] = {};
-            }
+    // row r of u and dv (in order: the pointers step along) into slot r % kBack; one commit group per row
+    const T *uf = u;
+    const float *df = dv;
+    auto fetch = [&](int r, int sl) {
+        if (r < nin) {
+            cp_row(rd + sl * kConvBwdT, df);
+            cp_small<(int)sizeof(Raw4<T>)>(ru + sl * kConvBwdT, uf);
+            df += dvs;
+            uf += p.urs;
         }
+        cp_commit();
     };
-    fetch(0);
+#pragma unroll
+    for (int j = 0; j < kBack; ++j) fetch(j, j);
     const bool resumed = p.tail_in && s.slot >= 0 && s.resume;
     const T *tin = resumed ? reinterpret_cast<const T *>(p.tail_in) + (int64_t)s.slot * 3 * p.C_ch + c : nullptr;
     const float4 z4 = make_float4(0.f, 0.f, 0.f, 0.f);
-    float4 a3, a2, a1;                      // u[t-3], u[t-2], u[t-1]
-    if (!head) { a3 = ld4(u - 3 * p.urs); a2 = ld4(u - 2 * p.urs); a1 = ld4(u - p.urs); }
-    else if (tin) { a3 = ld4(tin); a2 = ld4(tin + p.C_ch); a1 = ld4(tin + 2 * p.C_ch); }
-    else { a3 = z4; a2 = z4; a1 = z4; }
-    float wk[4][4];                         // [tap][channel]
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 q = __ldg(reinterpret_cast<const float4 *>(p.w) + c + i);
-        wk[0][i] = q.x; wk[1][i] = q.y; wk[2][i] = q.z; wk[3][i] = q.w;
+    const float2 z2 = make_float2(0.f, 0.f);
+    F2x2 x3, x2, x1;                        // u[t-3], u[t-2], u[t-1]
+    if (!head) { x3 = pairs(ld4(u - 3 * p.urs)); x2 = pairs(ld4(u - 2 * p.urs)); x1 = pairs(ld4(u - p.urs)); }
+    else if (tin) { x3 = pairs(ld4(tin)); x2 = pairs(ld4(tin + p.C_ch)); x1 = pairs(ld4(tin + 2 * p.C_ch)); }
+    else { x3 = x2 = x1 = F2x2{z2, z2}; }
+    float2 wa[4], wb[4];                    // taps of the two channel pairs
+    {
+        const float4 q0 = __ldg(reinterpret_cast<const float4 *>(p.w) + c), q1 = __ldg(reinterpret_cast<const float4 *>(p.w) + c + 1);
+        const float4 q2 = __ldg(reinterpret_cast<const float4 *>(p.w) + c + 2), q3 = __ldg(reinterpret_cast<const float4 *>(p.w) + c + 3);
+        wa[0] = make_float2(q0.x, q1.x); wa[1] = make_float2(q0.y, q1.y); wa[2] = make_float2(q0.z, q1.z); wa[3] = make_float2(q0.w, q1.w);
+        wb[0] = make_float2(q2.x, q3.x); wb[1] = make_float2(q2.y, q3.y); wb[2] = make_float2(q2.z, q3.z); wb[3] = make_float2(q2.w, q3.w);
     }
-    float bs[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bs[i] = p.bias ? __ldg(p.bias + c + i) : 0.0f;
-    float gw[4][4] = {}, gb[4] = {};
-    float e3[4] = {}, e2[4] = {}, e1[4] = {};       // dz[t-3], dz[t-2], dz[t-1] (zero before t0: those rows' du is another thread's)
+    F2x2 bs{z2, z2};
+    if (p.bias) bs = pairs(make_float4(__ldg(p.bias + c), __ldg(p.bias + c + 1), __ldg(p.bias + c + 2), __ldg(p.bias + c + 3)));
+    float2 gwa[4] = {}, gwb[4] = {}, gba = z2, gbb = z2;
+    F2x2 e3{z2, z2}, e2{z2, z2}, e1{z2, z2};    // dz[t-3], dz[t-2], dz[t-1] (zero before t0: those rows' du is another thread's)
     float *du = p.du + t0 * p.C_ch + c;
-    // the gradient of the buffer that the sequence starts from, with dz of its first three rows in e1, e2, e3
+    const int handed = p.dtail_out ? left : 0x7fffffff;   // du's row r - 3 also feeds row r - left of the buffer handed on, r >= left
+    const float *dto = p.dtail_out ? p.dtail_out + (int64_t)d.z * 3 * p.C_ch + c : nullptr;
+    // the gradient of the buffer that the sequence starts from, with dz of its first three rows in e3, e2, e1
     auto put_tail = [&]() {
-        float g[3][4] = {};
+        F2x2 g[3] = {{z2, z2}, {z2, z2}, {z2, z2}};
         if (resumed) {
+            g[0] = F2x2{__fmul2_rn(wa[0], e3.a), __fmul2_rn(wb[0], e3.b)};
+            g[1] = F2x2{__ffma2_rn(wa[1], e3.a, __fmul2_rn(wa[0], e2.a)), __ffma2_rn(wb[1], e3.b, __fmul2_rn(wb[0], e2.b))};
+            g[2] = F2x2{__ffma2_rn(wa[2], e3.a, __ffma2_rn(wa[1], e2.a, __fmul2_rn(wa[0], e1.a))),
+                        __ffma2_rn(wb[2], e3.b, __ffma2_rn(wb[1], e2.b, __fmul2_rn(wb[0], e1.b)))};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                g[0][i] = wk[0][i] * e3[i];
-                g[1][i] = fmaf(wk[1][i], e3[i], wk[0][i] * e2[i]);
-                g[2][i] = fmaf(wk[2][i], e3[i], fmaf(wk[1][i], e2[i], wk[0][i] * e1[i]));
-            }
-            if (p.dtail_out) {
-                // a sequence of fewer than three rows hands rows of its old buffer on
-#pragma unroll
-                for (int q = 0; q < 3; ++q) {
-                    const int r = q - s.len;            // row of the new buffer that holds old row q
-                    if (r >= 0) {
-                        const float4 x = ld4(p.dtail_out + ((int64_t)d.z * 3 + r) * p.C_ch + c);
-                        g[q][0] += x.x; g[q][1] += x.y; g[q][2] += x.z; g[q][3] += x.w;
-                    }
+            for (int q = 0; q < 3; ++q) {
+                const int r = q - s.len;            // row of the new buffer that holds old row q, where the sequence is so short
+                if (dto && r >= 0) {
+                    const F2x2 x = pairs(ld4(dto + (int64_t)r * p.C_ch));
+                    g[q].a = __fadd2_rn(g[q].a, x.a);
+                    g[q].b = __fadd2_rn(g[q].b, x.b);
                 }
             }
         }
 #pragma unroll
         for (int q = 0; q < 3; ++q)
             *reinterpret_cast<float4 *>(p.dtail_in + ((int64_t)d.z * 3 + q) * p.C_ch + c) =
-                make_float4(g[q][0], g[q][1], g[q][2], g[q][3]);
+                make_float4(g[q].a.x, g[q].a.y, g[q].b.x, g[q].b.y);
+    };
+    // du of row r - 3, once dz of row r (e0) is known
+    auto put_du = [&](int r, const F2x2 &e0) {
+        F2x2 g{__ffma2_rn(wa[0], e0.a, __ffma2_rn(wa[1], e1.a, __ffma2_rn(wa[2], e2.a, __fmul2_rn(wa[3], e3.a)))),
+               __ffma2_rn(wb[0], e0.b, __ffma2_rn(wb[1], e1.b, __ffma2_rn(wb[2], e2.b, __fmul2_rn(wb[3], e3.b))))};
+        if (r >= handed) {
+            const F2x2 x = pairs(ld4(dto + (int64_t)(r - left) * p.C_ch));
+            g.a = __fadd2_rn(g.a, x.a);
+            g.b = __fadd2_rn(g.b, x.b);
+        }
+        __stcs(reinterpret_cast<float4 *>(du), make_float4(g.a.x, g.a.y, g.b.x, g.b.y));
+        du += p.C_ch;
     };
     if (n == 0 && head && p.dtail_in) put_tail();
 #pragma unroll 1
-    for (int b0 = 0; b0 < nt; b0 += kBack) {
-        Raw4<T> uc[kBack];
-        Raw4<float> dc[kBack];
+    for (int b0 = 0; b0 < n; b0 += 4) {             // four rows bring the windows back to the same registers
 #pragma unroll
-        for (int j = 0; j < kBack; ++j) { uc[j] = un[j]; dc[j] = dn[j]; }
-        if (b0 + kBack < nt) fetch(b0 + kBack);
-#pragma unroll
-        for (int j = 0; j < kBack; ++j) {
-            const int r = b0 + j;
-            if (r < nt) {
-                const float4 uu = uc[j].get(), dd = dc[j].get();
-                const float x3[4] = {a3.x, a3.y, a3.z, a3.w}, x2[4] = {a2.x, a2.y, a2.z, a2.w};
-                const float x1[4] = {a1.x, a1.y, a1.z, a1.w}, x0[4] = {uu.x, uu.y, uu.z, uu.w};
-                const float dvv[4] = {dd.x, dd.y, dd.z, dd.w};
-                float g[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // (a row past the sequence's end has dv = 0, its window may be anything finite: cleared)
-                    float e0 = dz1(dvv[i], wk[0][i], wk[1][i], wk[2][i], wk[3][i], bs[i], x3[i], x2[i], x1[i], x0[i]);
-                    e0 = r < nin ? e0 : 0.0f;
-                    g[i] = fmaf(wk[0][i], e0, fmaf(wk[1][i], e1[i], fmaf(wk[2][i], e2[i], wk[3][i] * e3[i])));
-                    if (r < n) {
-                        gb[i] += e0;
-                        gw[0][i] = fmaf(e0, x3[i], gw[0][i]);
-                        gw[1][i] = fmaf(e0, x2[i], gw[1][i]);
-                        gw[2][i] = fmaf(e0, x1[i], gw[2][i]);
-                        gw[3][i] = fmaf(e0, x0[i], gw[3][i]);
-                    }
-                    e3[i] = e2[i]; e2[i] = e1[i]; e1[i] = e0;
-                }
+        for (int j = 0; j < 4; ++j) {
+            const int r = b0 + j, sl = (b0 & (kBack - 1)) + j;
+            if (r < n) {
+                cp_wait<kBack - 1>();               // row r's group is the oldest
+                const F2x2 x0 = pairs(ru[sl * kConvBwdT].get()), dd = pairs(rd[sl * kConvBwdT]);
+                fetch(r + kBack, sl);
+                const F2x2 e0{dz2(dd.a, wa, bs.a, x3.a, x2.a, x1.a, x0.a), dz2(dd.b, wb, bs.b, x3.b, x2.b, x1.b, x0.b)};
+                gba = __fadd2_rn(gba, e0.a);
+                gbb = __fadd2_rn(gbb, e0.b);
+                gwa[0] = __ffma2_rn(e0.a, x3.a, gwa[0]); gwb[0] = __ffma2_rn(e0.b, x3.b, gwb[0]);
+                gwa[1] = __ffma2_rn(e0.a, x2.a, gwa[1]); gwb[1] = __ffma2_rn(e0.b, x2.b, gwb[1]);
+                gwa[2] = __ffma2_rn(e0.a, x1.a, gwa[2]); gwb[2] = __ffma2_rn(e0.b, x1.b, gwb[2]);
+                gwa[3] = __ffma2_rn(e0.a, x0.a, gwa[3]); gwb[3] = __ffma2_rn(e0.b, x0.b, gwb[3]);
+                if (r >= 3) put_du(r, e0);
+                e3 = e2; e2 = e1; e1 = e0;
+                x3 = x2; x2 = x1; x1 = x0;
                 if (r == 2 && head && p.dtail_in) put_tail();
-                if (r >= 3) {
-                    const int64_t back = t0 + r - 3 - (se - 3);     // row of the buffer handed on that du's row is
-                    if (p.dtail_out && back >= 0) {
-                        const float4 q = ld4(p.dtail_out + ((int64_t)d.z * 3 + back) * p.C_ch + c);
-                        g[0] += q.x; g[1] += q.y; g[2] += q.z; g[3] += q.w;
-                    }
-                    __stcs(reinterpret_cast<float4 *>(du + (int64_t)(r - 3) * p.C_ch), make_float4(g[0], g[1], g[2], g[3]));
-                }
-                a3 = a2; a2 = a1; a1 = uu;
             }
         }
     }
-    float4 *pw = reinterpret_cast<float4 *>(p.ws_dw) + chunk * p.C_ch + c;
+    // three rows past the chunk: their dz completes du of its last rows
+    if (n > 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pw[i] = make_float4(gw[0][i], gw[1][i], gw[2][i], gw[3][i]);
-    *reinterpret_cast<float4 *>(p.ws_db + chunk * p.C_ch + c) = make_float4(gb[0], gb[1], gb[2], gb[3]);
+        for (int j = 0; j < 3; ++j) {
+            const int r = n + j;
+            F2x2 e0{z2, z2};
+            cp_wait<kBack - 1>();
+            if (r < nin) {
+                const int sl = r & (kBack - 1);
+                const F2x2 x0 = pairs(ru[sl * kConvBwdT].get()), dd = pairs(rd[sl * kConvBwdT]);
+                e0 = F2x2{dz2(dd.a, wa, bs.a, x3.a, x2.a, x1.a, x0.a), dz2(dd.b, wb, bs.b, x3.b, x2.b, x1.b, x0.b)};
+                x3 = x2; x2 = x1; x1 = x0;
+            }
+            cp_commit();
+            if (r >= 3) put_du(r, e0);
+            e3 = e2; e2 = e1; e1 = e0;
+            if (r == 2 && head && p.dtail_in) put_tail();
+        }
+    }
+    cp_wait<0>();
+    float4 *pw = reinterpret_cast<float4 *>(p.ws_dw) + chunk * p.C_ch + c;
+    pw[0] = make_float4(gwa[0].x, gwa[1].x, gwa[2].x, gwa[3].x);
+    pw[1] = make_float4(gwa[0].y, gwa[1].y, gwa[2].y, gwa[3].y);
+    pw[2] = make_float4(gwb[0].x, gwb[1].x, gwb[2].x, gwb[3].x);
+    pw[3] = make_float4(gwb[0].y, gwb[1].y, gwb[2].y, gwb[3].y);
+    *reinterpret_cast<float4 *>(p.ws_db + chunk * p.C_ch + c) = make_float4(gba.x, gba.y, gbb.x, gbb.y);
 }
 
 // dw and dbias: the chunks' sums, added in a fixed order.  A CTA takes 32 channels; each of its 16
@@ -431,8 +453,12 @@ int launch_packed_conv_backward(const PackedConvBwdParams &p, int dtype, cudaStr
     if (blocks > 0x7fffffffLL) return 2;
     prof_begin(st, kKPackedConvBwd);
     if (blocks > 0) {
-        if (dtype == 1) packed_conv_bwd_kernel<__nv_bfloat16><<<(unsigned)blocks, kConvBwdT, 0, st>>>(p);
-        else packed_conv_bwd_kernel<float><<<(unsigned)blocks, kConvBwdT, 0, st>>>(p);
+        static std::atomic<int> done_b[64], done_f[64];
+        const int smem_b = (16 + 8) * kBack * kConvBwdT, smem_f = (16 + 16) * kBack * kConvBwdT;
+        if (!(dtype == 1 ? allow_smem(packed_conv_bwd_kernel<__nv_bfloat16>, smem_b, done_b) : allow_smem(packed_conv_bwd_kernel<float>, smem_f, done_f)))
+            return 7;
+        if (dtype == 1) packed_conv_bwd_kernel<__nv_bfloat16><<<(unsigned)blocks, kConvBwdT, smem_b, st>>>(p);
+        else packed_conv_bwd_kernel<float><<<(unsigned)blocks, kConvBwdT, smem_f, st>>>(p);
     }
     packed_conv_reduce_kernel<<<(unsigned)((p.C_ch + 31) / 32), 32 * kRedWarps, 0, st>>>(p);
     prof_end(st, kKPackedConvBwd);
