@@ -46,7 +46,8 @@ __device__ __forceinline__ void raise_timeout(const PackedScanParams &p, volatil
     atomicOr(p.status, kDevTimeout);
 }
 
-// w times 8 bf16 values: the bf16 rounding of the products and that of what it leaves
+// w times 8 bf16 values: their bf16 rounding (on the integer pipe, ties away from zero; |w v| stays finite) and the
+// bf16 rounding of what it leaves (on the conversion unit)
 __device__ __forceinline__ void split8(uint4 v, float w, uint4 &hi, uint4 &lo)
 {
     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
@@ -55,7 +56,7 @@ __device__ __forceinline__ void split8(uint4 v, float w, uint4 &hi, uint4 &lo)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 q = mul2(unpack2(in[i]), w2);
-        h[i] = pack_bf16x2(q.x, q.y);
+        h[i] = pack_bf16x2_int(q.x, q.y);
         l[i] = pack_bf16x2(q.x - bf16_lo(h[i]), q.y - bf16_hi(h[i]));
     }
     hi = make_uint4(h[0], h[1], h[2], h[3]);
@@ -302,22 +303,37 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
 }
 
 // =============================================================== pass C
-// One CTA per (window, head pair): 16 compute warps, an issuing warp, a store warp and a B/C warp.
+// A bounded wait whose loop is out of line: the output kernel has some thirty of them, and with the loops in place
+// the warps waited for instructions (298 against 282 us at 65536 rows of 32 heads).
+static __device__ __noinline__ bool wait_loop(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns)
+{
+    return mbar_wait(bar, parity, abort, limit_ns);
+}
+__device__ __forceinline__ bool cwait(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns)
+{
+    const bool ok = mbar_try_wait(bar, parity) || wait_loop(bar, parity, abort, limit_ns);
+    return __all_sync(0xffffffffu, ok);
+}
+
+// One CTA per (window, head pair): 16 compute warps, an issuing warp, a store warp, a B/C warp and a scan warp.
 // The output accumulator T of a chunk first receives Ys = C [h_a | h_b]^T, which the compute warps scale
 // row by row by e^{cs_i}; Y = Pm X then accumulates onto it, so the epilogue only adds D x.  Per chunk c:
 //   issuing warp: Pm written and T scaled -> Y_a, Y_b onto T; w o X ready -> S, both of its parts, onto the
-//       state H; T read and the state of chunk c+1 written -> Ys of chunk c+1
-//   B/C warp: products done -> the B/C slot refilled with chunk c+2; then G of chunk c+2
+//       state H; the state of chunk c+1 written -> Ys of chunk c+1
+//   B/C warp: products done -> the B/C slot refilled with chunk c+2; G of chunk c+2 after Y of chunk c+1
 //   store warp: y staged -> stored (TMA, or row by row for a short chunk), X of chunk c+2 into its slot
 //   compute warp (lane quarter q = warp & 3, column slice cs = warp >> 2 of the 128 (head, p) columns):
-//       T scaled; w o X into the C half of the B/C slot (spent once G and Ys have read C) and its
-//       remainder into hp (spent once Ys has read it); the masked decay of chunk c+1 under S; at the end
-//       the state step of chunk c+1 -- or, where a sequence ends, its state to its slot and the next
-//       one's start in its place -- and y
-// Warp 4 also publishes the running sums and the descriptor of chunk c+1.
+//       T scaled; under Y, w o X into the C half of the B/C slot (spent once G and Ys have read C) and its
+//       remainder into hp (spent once Ys has read it); under S, y; then the state step of chunk c+1 -- or, where a
+//       sequence ends, its state to its slot and the next one's start in its place -- and under Ys the masked
+//       decay of chunk c+1
+//   scan warp: the running sums of chunk c+1, ready in registers, into shared memory as soon as every warp has
+//       used those of chunk c; it also starts the slot's state of a sequence about to begin into L2
+// The decay is kept away from S: both live off TMEM, and together they took 1.9 us where one after the other
+// takes 1.5.  A chunk of fewer than 128 rows takes only the K-steps (of 16 rows) of Y and S that have rows.
 // TMEM (512 columns): R0 = 0..127 G; R1 = 128..255 Pm_a | Pm_b (bf16); T = 256..383; H = 384..511 (rows n).
 constexpr int kComputeWarps = 16;
-constexpr int kThreadsC = 32 * (kComputeWarps + 3);
+constexpr int kThreadsC = 32 * (kComputeWarps + 4);
 
 struct SmemC {
     uint8_t bc[2][4 * kBox];   // ring slot: C box 0, C box 1, B box 0, B box 1; later w o X in the C half
@@ -329,7 +345,7 @@ struct SmemC {
     int4 desc[2];              // descriptors of chunks c and c+1
     uint64_t full_bc[2], full_x[2], g_done, ys_done, ymma_done, mma_done[2];
     uint64_t fin, fin2;
-    uint64_t pmw, pm_ready, xw_ready, ys_go, st0_ready, scan_ready;
+    uint64_t pmw, pm_ready, xw_ready, ys_go, scan_ready;
     uint64_t y_ready[2];
     uint32_t tmem;
     int abort;
@@ -373,7 +389,6 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
         mbar_init(&s.ys_go, kComputeWarps);
         mbar_init(&s.y_ready[0], kComputeWarps);
         mbar_init(&s.y_ready[1], kComputeWarps);
-        mbar_init(&s.st0_ready, kComputeWarps);
         mbar_init(&s.scan_ready, 1);
         s.abort = 0;
         fence_mbar_init();
@@ -398,56 +413,13 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
         const int hh = ha + hd;
         auto fail = [&]() { if (lane == 0) raise_timeout(p, abort); };
 
-        // the state that chunk d starts from: thread (n = r, cs) owns h[p0 .. p0 + 31][n] of head hh
-        auto load_state = [&](int4 d, uint32_t (&hv)[32]) {
-            const float *src = (d.y & kChunkFirst) ? window_start<false>(p, d, k, first + nc, hh)
-                                                   : p.ws_hin + ((int64_t)k * p.H + hh) * kPN;
-#pragma unroll
-            for (int pp = 0; pp < 32; ++pp) hv[pp] = src ? __float_as_uint(src[(p0 + pp) * kN + r]) : 0u;
-        };
+        // thread (n = r, cs) owns h[p0 .. p0 + 31][n] of head hh
         auto store_state = [&](int slot, const uint32_t (&hv)[32]) {
             float *dst = p.h_out + ((int64_t)slot * p.H + hh) * kPN + (int64_t)p0 * kN + r;
 #pragma unroll
             for (int pp = 0; pp < 32; ++pp) dst[pp * kN] = __uint_as_float(hv[pp]);
         };
 
-        // running sums of both heads (warp 4): lane l holds rows 4 l .. 4 l + 3; dt and the descriptor
-        // are read a chunk ahead
-        const bool scan_warp = warp == 4;
-        float2 dtn[4];
-        int4 dn = make_int4(0, 0, 0, 0);
-        auto fetch = [&](int c) {
-            dn = chunks[c];
-            load_dt(p, dn.x, dn.y & kChunkRows, lane, ha, dtn);
-        };
-        auto scan = [&](int c) {
-            use_dt(p, dn.y & kChunkRows, lane, ha, dtn);
-            float ca[4], cb[4];
-            chunk_sums(dtn, p.A[ha] * kLog2e, p.A[ha + 1] * kLog2e, lane, ca, cb);
-            // the sum at the end of this lane's 32-row block (row 32 J + 31 = lane 8 J + 7)
-            const float ea = __shfl_sync(0xffffffffu, ca[3], lane | 7);
-            const float eb = __shfl_sync(0xffffffffu, cb[3], lane | 7);
-            reinterpret_cast<float4 *>(s.cvs[0])[lane] = make_float4(ca[0], ca[1], ca[2], ca[3]);
-            reinterpret_cast<float4 *>(s.cvs[1])[lane] = make_float4(cb[0], cb[1], cb[2], cb[3]);
-            reinterpret_cast<float4 *>(s.dvs[0])[lane] = make_float4(dtn[0].x, dtn[1].x, dtn[2].x, dtn[3].x);
-            reinterpret_cast<float4 *>(s.dvs[1])[lane] = make_float4(dtn[0].y, dtn[1].y, dtn[2].y, dtn[3].y);
-            if (lane < 24) {
-                reinterpret_cast<float4 *>(s.fs[0])[lane] =
-                    make_float4(dtn[0].x * ex2(ea - ca[0]), dtn[1].x * ex2(ea - ca[1]),
-                                dtn[2].x * ex2(ea - ca[2]), dtn[3].x * ex2(ea - ca[3]));
-                reinterpret_cast<float4 *>(s.fs[1])[lane] =
-                    make_float4(dtn[0].y * ex2(eb - cb[0]), dtn[1].y * ex2(eb - cb[1]),
-                                dtn[2].y * ex2(eb - cb[2]), dtn[3].y * ex2(eb - cb[3]));
-            }
-            if (lane == 0) s.desc[c & 1] = dn;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.scan_ready);
-        };
-        if (scan_warp && live) {
-            fetch(0);
-            scan(0);
-            if (nc > 1) fetch(1);
-        }
         const float Dh = p.D ? p.D[hh] : 0.0f;
 
         // hv = the state entering a chunk: its bf16 copy feeds C h^T, then H = e^{cs_last} h, to which S is added
@@ -464,8 +436,20 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
             }
             const float dec = ex2(s.cvs[hd][kQ - 1]);
 #pragma unroll
-            for (int pp = 0; pp < 32; ++pp) hv[pp] = __float_as_uint(dec * __uint_as_float(hv[pp]));
+            for (int pp = 0; pp < 32; pp += 2) {
+                const float2 q2 = mul2(make_float2(__uint_as_float(hv[pp]), __uint_as_float(hv[pp + 1])), make_float2(dec, dec));
+                hv[pp] = __float_as_uint(q2.x); hv[pp + 1] = __float_as_uint(q2.y);
+            }
             tmem_st32(tH + lane_base + 32 * cs, hv);
+        };
+        auto state_zero = [&]() {
+            uint8_t *dst = s.hp + hd * kBox;
+            uint32_t z[32];
+#pragma unroll
+            for (int pp = 0; pp < 32; ++pp) z[pp] = 0u;
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) sts128(dst + swz(r, (p0 >> 3) + c4), make_uint4(0u, 0u, 0u, 0u));
+            tmem_st32(tH + lane_base + 32 * cs, z);
         };
         // y = T + D x for 16 columns -> bf16, in place over x in the X slot (same swizzle as the y map)
         auto y_half = [&](uint8_t *xs, const uint32_t (&tv)[16], int hf) {
@@ -487,11 +471,13 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
 
         // masked decay of the chunk whose sums are published: column blocks J = 2 (cs & 1) + jb of head
         // hd, rows of quarter q
-        auto decay = [&]() {
+        auto decay = [&](int rows) {
+            if (32 * q >= rows) return;         // rows of y that are not stored
             const float csr = s.cvs[hd][r];
-#pragma unroll
+#pragma unroll 1
             for (int jb = 0; jb < 2; ++jb) {
                 const int J = 2 * (cs & 1) + jb;
+                if (32 * J >= rows) break;      // columns that no K-step of Y takes
                 uint32_t pk[16];
                 if (J < q) {
                     // below the diagonal: e^{cs_r - cs_j} = e^{cs_r - m_J} e^{m_J - cs_j}
@@ -548,32 +534,16 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
             }
         };
 
-        bool ok = ewait(&s.scan_ready, 0, abort, lim);
-        if (ok) {
-            uint32_t hv[32];
-            load_state(s.desc[0], hv);
-            state_step(hv);
-            tmem_wait_st();
-            fence_proxy_async_smem();   // hp, read by Ys of chunk 0
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.st0_ready);
-            ok = ewait(&s.g_done, 0, abort, lim);
-            if (ok) {
-                tc_fence_after();
-                decay();
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.pmw);
-            }
-        }
-        if (!ok) fail();
-        for (int c = 0; ok && c < nc; ++c) {
+        // turn c: T, w o X and y of chunk c, then the state step and the masked decay of chunk c+1 (turn -1: those
+        // of chunk 0 only, from the state that enters the window).  One copy of each: what the warps run through per
+        // chunk has to stay in the instruction cache
+#pragma unroll 1
+        for (int c = -1; c < nc; ++c) {
+          if (c >= 0) {
             uint8_t *xs = s.x[c & 1];
 
             // ---- T (= Ys of this chunk) *= e^{cs_r} on this warp's rows and columns
-            if (!ewait(&s.ys_done, c & 1, abort, lim)) { fail(); break; }
+            if (!cwait(&s.ys_done, c & 1, abort, lim)) { fail(); break; }
             tc_fence_after();
             const int rows = s.desc[c & 1].y & kChunkRows;
             {
@@ -581,40 +551,41 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                 uint32_t tv[32];
                 tmem_ld32(tT + lane_base + 32 * cs, tv);
                 tmem_wait_ld(tv);
+                const float2 e2 = make_float2(e_r, e_r);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) tv[i] = __float_as_uint(e_r * __uint_as_float(tv[i]));
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 q2 = mul2(make_float2(__uint_as_float(tv[i]), __uint_as_float(tv[i + 1])), e2);
+                    tv[i] = __float_as_uint(q2.x); tv[i + 1] = __float_as_uint(q2.y);
+                }
                 tmem_st32(tT + lane_base + 32 * cs, tv);
             }
-            if (rows < kQ) {
-                // a short chunk: rows of X and B behind its end are cleared (G has read B: the decay of this
-                // chunk waited for it) before Y and S sum over them
-                if (!(ewait(&s.full_x[c & 1], (c >> 1) & 1, abort, lim) && ewait(&s.full_bc[c & 1], (c >> 1) & 1, abort, lim))) { fail(); break; }
-                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                for (int i = 32 * warp + lane; i < (kQ - rows) * 32; i += 32 * kComputeWarps) {
-                    const int row = rows + (i >> 5), ch = i & 7, box = (i >> 3) & 3;
-                    uint8_t *t = box < 2 ? xs + box * kBox : s.bc[c & 1] + box * kBox;
-                    sts128(t + swz(row, ch), z);
-                }
+            // a short chunk: Y and S take K-steps of 16 rows; the rows of X behind the chunk's end in its last step are
+            // cleared before Y sums over them, those of B before S does (G has read B: the decay waited for it)
+            const int stop = (rows + 15) & ~15;
+            if (rows < stop) {
+                if (!cwait(&s.full_x[c & 1], (c >> 1) & 1, abort, lim)) { fail(); break; }
+                for (int i = 32 * warp + lane; i < (stop - rows) * 16; i += 32 * kComputeWarps)
+                    sts128(xs + ((i >> 3) & 1) * kBox + swz(rows + (i >> 4), i & 7), make_uint4(0u, 0u, 0u, 0u));
                 fence_proxy_async_smem();
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.pm_ready);   // Pm written, T scaled, the tail cleared
+            if (lane == 0) mbar_arrive(&s.pm_ready);   // Pm written, T scaled, X's end cleared
 
             // ---- w o X of head hd: its bf16 rounding into the C half of this chunk's B/C slot (G and Ys have read
             //      C), the remainder into hp (Ys has read it), for S, which runs after Y
-            if (!ewait(&s.full_x[c & 1], (c >> 1) & 1, abort, lim)) { fail(); break; }
+            if (!cwait(&s.full_x[c & 1], (c >> 1) & 1, abort, lim)) { fail(); break; }
             {
                 const int ti = 32 * (warp & 7) + lane;
                 const int j = ti >> 1, ch = 4 * (ti & 1);
                 const float w = s.dvs[hd][j] * ex2(s.cvs[hd][kQ - 1] - s.cvs[hd][j]);
                 const uint8_t *src = xs + hd * kBox;
                 uint8_t *dst = s.bc[c & 1] + hd * kBox, *rem = s.hp + hd * kBox;
-#pragma unroll
+#pragma unroll 1
                 for (int u = 0; u < 4; ++u) {
                     const uint32_t o = swz(j, ch + u);
-                    // (a row behind a short chunk's end may not be cleared yet)
+                    // (a row behind a short chunk's end is zero, whatever X holds there)
                     const uint4 v = j < rows ? lds128(src + o) : make_uint4(0u, 0u, 0u, 0u);
                     uint4 hi, lo;
                     split8(v, w, hi, lo);
@@ -622,69 +593,79 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                     sts128(rem + o, lo);
                 }
             }
+            if (rows < stop) {
+                if (!cwait(&s.full_bc[c & 1], (c >> 1) & 1, abort, lim)) { fail(); break; }
+                for (int i = 32 * warp + lane; i < (stop - rows) * 16; i += 32 * kComputeWarps)
+                    sts128(s.bc[c & 1] + (2 + ((i >> 3) & 1)) * kBox + swz(rows + (i >> 4), i & 7), make_uint4(0u, 0u, 0u, 0u));
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.xw_ready);
 
-            // every warp has read this chunk's sums once all have written w o X: publish the next chunk's
-            if (scan_warp && c + 1 < nc) {
-                if (!ewait(&s.xw_ready, c & 1, abort, lim)) { fail(); break; }
-                scan(c + 1);
-                if (c + 2 < nc) fetch(c + 2);
+            // ---- y of chunk c while S runs: Y is done, and every warp has read X for its w o X
+            if (!(cwait(&s.ymma_done, c & 1, abort, lim) && cwait(&s.xw_ready, c & 1, abort, lim))) { fail(); break; }
+            tc_fence_after();
+            {
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t t0v[16];
+                    tmem_ld16(tT + lane_base + 32 * cs + 16 * hf, t0v);
+                    tmem_wait_ld(t0v);
+                    y_half(xs, t0v, hf);
+                }
             }
+            fence_proxy_async_smem();   // y, read by the TMA store
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.y_ready[c & 1]);
 
-            // ---- the masked decay of chunk c+1 while S of this chunk runs
+            // ---- S is done too
+            if (!cwait(&s.mma_done[c & 1], (c >> 1) & 1, abort, lim)) { fail(); break; }
+          }
+            // ---- the state step of chunk c+1, then its masked decay while its Ys runs
             if (c + 1 < nc) {
-                if (!(ewait(&s.ymma_done, c & 1, abort, lim) && ewait(&s.g_done, (c + 1) & 1, abort, lim) &&
-                      ewait(&s.scan_ready, (c + 1) & 1, abort, lim))) { fail(); break; }
+                if (!cwait(&s.scan_ready, (c + 1) & 1, abort, lim)) { fail(); break; }
                 tc_fence_after();
-                decay();
+                uint32_t hv[32];
+                const int4 dn = s.desc[(c + 1) & 1];
+                int slot = -1;
+                bool ends = true;
+                if (c >= 0) {
+                    tmem_ld32(tH + lane_base + 32 * cs, hv);
+                    tmem_wait_ld(hv);
+                    ends = (s.desc[c & 1].y & kChunkLast) != 0;
+                    if (p.h_out && ends) slot = s.desc[c & 1].w;
+                }
+                // where a sequence ends, its state goes to its slot and the next one's start takes its place; a
+                // start from zero needs no registers, so that the old state can leave after Ys was let go
+                const float *src = nullptr;
+                if (ends)
+                    src = (dn.y & kChunkFirst) ? window_start<false>(p, dn, k, first + nc, hh)
+                                               : p.ws_hin + ((int64_t)k * p.H + hh) * kPN;
+                if (src) {
+                    if (slot >= 0) store_state(slot, hv);
+#pragma unroll
+                    for (int pp = 0; pp < 32; ++pp) hv[pp] = __float_as_uint(src[(p0 + pp) * kN + r]);
+                }
+                if (ends && !src) state_zero();
+                else state_step(hv);
+                tmem_wait_st();
+                fence_proxy_async_smem();   // hp, read by Ys of chunk c+1
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.ys_go);
+                if (slot >= 0 && !src) store_state(slot, hv);
+                if (!cwait(&s.g_done, (c + 1) & 1, abort, lim)) { fail(); break; }
+                tc_fence_after();
+                decay(dn.y & kChunkRows);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.pmw);
             }
-
-            // ---- once every product of the chunk is done: y of chunk c and the state step of chunk c+1
-            if (!ewait(&s.mma_done[c & 1], (c >> 1) & 1, abort, lim)) { fail(); break; }
-            tc_fence_after();
-            if (c + 1 < nc) {
-                uint32_t hv[32], t0v[16], t1v[16];
-                tmem_ld32(tH + lane_base + 32 * cs, hv);
-                tmem_ld16(tT + lane_base + 32 * cs, t0v);
-                tmem_ld16(tT + lane_base + 32 * cs + 16, t1v);
-                tmem_wait_ld(t0v, t1v);
-                tmem_wait_ld(hv);
-                if (s.desc[c & 1].y & kChunkLast) {
-                    // the sequence ends here: its state to its slot, the next one's start in its place
-                    const int slot = s.desc[c & 1].w;
-                    if (p.h_out && slot >= 0) store_state(slot, hv);
-                    load_state(s.desc[(c + 1) & 1], hv);
-                }
-                // with T read and hp written, Ys of chunk c+1 may start while y is formed from the registers
-                state_step(hv);
-                tmem_wait_st();
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.ys_go);
-                y_half(xs, t0v, 0);
-                y_half(xs, t1v, 1);
-            } else {
-                uint32_t t0v[16], t1v[16];
-                tmem_ld16(tT + lane_base + 32 * cs, t0v);
-                tmem_ld16(tT + lane_base + 32 * cs + 16, t1v);
-                tmem_wait_ld(t0v, t1v);
-                y_half(xs, t0v, 0);
-                y_half(xs, t1v, 1);
-            }
-            tmem_wait_st();
-            fence_proxy_async_smem();   // y, read by the TMA store
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.y_ready[c & 1]);
         }
         if (!__any_sync(0xffffffffu, *abort != 0)) {
+            tc_fence_after();
             const int4 d = s.desc[(nc - 1) & 1];
             if ((d.y & kChunkLast) && p.h_out && d.w >= 0) {
                 uint32_t hv[32];
@@ -710,7 +691,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
         auto issue_g = [&](int c) {
             const uint64_t dc = (c & 1) ? dC1 : dC0, db = (c & 1) ? dBk1 : dBk0;
             const uint32_t id_g = idesc_bf16(128, 128, 0, 0);
-#pragma unroll
+#pragma unroll 2
             for (int kk = 0; kk < 8; ++kk) mma_ss(tG, dc + koff(kk), db + koff(kk), id_g, kk > 0);
             mma_commit(&s.g_done);
         };
@@ -720,7 +701,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
             auto issue_ys = [&](int c) {
                 const uint64_t dc = (c & 1) ? dC1 : dC0;
                 const uint32_t id_ys = idesc_bf16(128, 128, 0, 1);    // A = C (K-major), B = hp (MN-major)
-#pragma unroll
+#pragma unroll 2
                 for (int kk = 0; kk < 8; ++kk) mma_ss(tT, dc + koff(kk), dHp + moff(kk), id_ys, kk > 0);
                 mma_commit(&s.ys_done);
             };
@@ -728,12 +709,12 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
             const uint32_t id_s = idesc_bf16(128, 128, 1, 1);     // A = B^T (MN-major), B = w o X (MN-major)
             bool ok = live;
             if (ok) {
-                ok = ewait(&s.full_bc[0], 0, abort, lim);
+                ok = cwait(&s.full_bc[0], 0, abort, lim);
                 if (ok) {
                     tc_fence_after();
                     if (lane == 0) issue_g(0);
                     __syncwarp();
-                    ok = ewait(&s.st0_ready, 0, abort, lim);
+                    ok = cwait(&s.ys_go, 0, abort, lim);
                     if (ok) {
                         tc_fence_after();
                         if (lane == 0) issue_ys(0);
@@ -742,33 +723,50 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                 }
             }
             for (int c = 0; ok && c < nc; ++c) {
-                ok = ewait(&s.pm_ready, c & 1, abort, lim) && ewait(&s.full_x[c & 1], (c >> 1) & 1, abort, lim);
+                ok = cwait(&s.pm_ready, c & 1, abort, lim) && cwait(&s.full_x[c & 1], (c >> 1) & 1, abort, lim);
                 if (!ok) break;
                 tc_fence_after();
+                const int steps = ((s.desc[c & 1].y & kChunkRows) + 15) >> 4;
                 if (lane == 0) {
                     const uint64_t dx = (c & 1) ? dX1 : dX0;
-#pragma unroll
-                    for (int hd2 = 0; hd2 < 2; ++hd2)
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_ts(tT + 64 * hd2, tPm + 64 * hd2 + kk * 8, dx + hd2 * kBoxD + moff(kk), id_pm, true);
+                    if (steps == 8) {
+#pragma unroll 1
+                        for (int hd2 = 0; hd2 < 2; ++hd2)
+#pragma unroll 2
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_ts(tT + 64 * hd2, tPm + 64 * hd2 + kk * 8, dx + hd2 * kBoxD + moff(kk), id_pm, true);
+                    } else {
+#pragma unroll 1
+                        for (int kk = 0; kk < steps; ++kk) {
+                            mma_ts(tT, tPm + kk * 8, dx + moff(kk), id_pm, true);
+                            mma_ts(tT + 64, tPm + 64 + kk * 8, dx + kBoxD + moff(kk), id_pm, true);
+                        }
+                    }
                     mma_commit(&s.ymma_done);
                 }
                 __syncwarp();
-                ok = ewait(&s.xw_ready, c & 1, abort, lim);
+                ok = cwait(&s.xw_ready, c & 1, abort, lim);
                 if (!ok) break;
                 tc_fence_after();
                 if (lane == 0) {
                     const uint64_t dbt = (c & 1) ? dBt1 : dBt0, dxw = (c & 1) ? dXw1 : dXw0;
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) mma_ss(tH, dbt + moff(kk), dxw + moff(kk), id_s, true);
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) mma_ss(tH, dbt + moff(kk), dHp + moff(kk), id_s, true);
+                    if (steps == 8) {
+#pragma unroll 2
+                        for (int kk = 0; kk < 8; ++kk) mma_ss(tH, dbt + moff(kk), dxw + moff(kk), id_s, true);
+#pragma unroll 2
+                        for (int kk = 0; kk < 8; ++kk) mma_ss(tH, dbt + moff(kk), dHp + moff(kk), id_s, true);
+                    } else {
+#pragma unroll 1
+                        for (int kk = 0; kk < steps; ++kk) {
+                            mma_ss(tH, dbt + moff(kk), dxw + moff(kk), id_s, true);
+                            mma_ss(tH, dbt + moff(kk), dHp + moff(kk), id_s, true);
+                        }
+                    }
                     mma_commit(&s.mma_done[c & 1]);
                 }
                 __syncwarp();
                 if (c + 1 < nc) {
-                    ok = ewait(&s.ys_go, c & 1, abort, lim);
+                    ok = cwait(&s.ys_go, (c + 1) & 1, abort, lim);
                     if (!ok) break;
                     tc_fence_after();
                     if (lane == 0) issue_ys(c + 1);
@@ -779,7 +777,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                 if (live && !ok) raise_timeout(p, abort);
                 // every MMA of this warp complete before TMEM is freed
                 mma_commit(&s.fin);
-                mbar_wait(&s.fin, 0, nullptr, 100000000ull);
+                wait_loop(&s.fin, 0, nullptr, 100000000ull);
             }
             __syncwarp();
         } else if (warp == kComputeWarps + 1) {
@@ -804,7 +802,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                 const int rows = d.y & kChunkRows;
                 uint8_t *xs = s.x[c & 1];
                 // y staged: store it; once its slot has been read, X of chunk c+2 is loaded there
-                ok = ewait(&s.y_ready[c & 1], (c >> 1) & 1, abort, lim);
+                ok = cwait(&s.y_ready[c & 1], (c >> 1) & 1, abort, lim);
                 if (!ok) break;
                 if (rows == kQ) {
                     if (lane == 0) {
@@ -830,10 +828,54 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                     // the last load issued into each X slot lands before the CTA's shared memory is
                     // released (an earlier load into the same slot has been waited on by the compute warps)
                     for (int i = x_issued > 2 ? x_issued - 2 : 0; i < x_issued; ++i)
-                        mbar_wait(&s.full_x[i & 1], (i >> 1) & 1, nullptr, 100000000ull);
+                        wait_loop(&s.full_x[i & 1], (i >> 1) & 1, nullptr, 100000000ull);
                 }
                 tma_store_wait<0>();
             }
+            __syncwarp();
+        } else if (warp == kComputeWarps + 3) {
+            // ============================================= scan warp: lane l holds rows 4 l .. 4 l + 3
+            const float A2a = p.A[ha] * kLog2e, A2b = p.A[ha + 1] * kLog2e;
+            bool ok = live;
+            int4 dn = chunks[0];
+            float2 dt[4];
+            load_dt(p, dn.x, dn.y & kChunkRows, lane, ha, dt);
+            for (int c = 0; ok && c < nc; ++c) {
+                const int4 d = dn;
+                if (c + 1 < nc) dn = chunks[c + 1];
+                use_dt(p, d.y & kChunkRows, lane, ha, dt);
+                float ca[4], cb[4];
+                chunk_sums(dt, A2a, A2b, lane, ca, cb);
+                // the sum at the end of this lane's 32-row block (row 32 J + 31 = lane 8 J + 7)
+                const float ea = __shfl_sync(0xffffffffu, ca[3], lane | 7), eb = __shfl_sync(0xffffffffu, cb[3], lane | 7);
+                const float4 fa = make_float4(dt[0].x * ex2(ea - ca[0]), dt[1].x * ex2(ea - ca[1]),
+                                              dt[2].x * ex2(ea - ca[2]), dt[3].x * ex2(ea - ca[3]));
+                const float4 fb = make_float4(dt[0].y * ex2(eb - cb[0]), dt[1].y * ex2(eb - cb[1]),
+                                              dt[2].y * ex2(eb - cb[2]), dt[3].y * ex2(eb - cb[3]));
+                if (lane < 2 && c > 0 && (d.y & kChunkFirst)) {
+                    const float *src = window_start<false>(p, d, k, first + nc, ha + lane);
+                    if (src)
+                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"((uint32_t)(kPN * 4)) : "memory");
+                }
+                // every warp has used the sums of chunk c - 1 once all have written its w o X
+                if (c > 0) {
+                    ok = cwait(&s.xw_ready, (c - 1) & 1, abort, lim);
+                    if (!ok) break;
+                }
+                reinterpret_cast<float4 *>(s.cvs[0])[lane] = make_float4(ca[0], ca[1], ca[2], ca[3]);
+                reinterpret_cast<float4 *>(s.cvs[1])[lane] = make_float4(cb[0], cb[1], cb[2], cb[3]);
+                reinterpret_cast<float4 *>(s.dvs[0])[lane] = make_float4(dt[0].x, dt[1].x, dt[2].x, dt[3].x);
+                reinterpret_cast<float4 *>(s.dvs[1])[lane] = make_float4(dt[0].y, dt[1].y, dt[2].y, dt[3].y);
+                if (lane < 24) {
+                    reinterpret_cast<float4 *>(s.fs[0])[lane] = fa;
+                    reinterpret_cast<float4 *>(s.fs[1])[lane] = fb;
+                }
+                if (lane == 0) s.desc[c & 1] = d;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.scan_ready);
+                if (c + 1 < nc) load_dt(p, dn.x, dn.y & kChunkRows, lane, ha, dt);
+            }
+            if (lane == 0 && live && !ok) raise_timeout(p, abort);
             __syncwarp();
         } else {
             // ============================================= B/C warp: B and C in, G of chunks 1..
@@ -856,7 +898,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                     if (nc > 1) issue_bc(1);
                 }
                 if (nc > 1) {
-                    ok = ewait(&s.pmw, 0, abort, lim) && ewait(&s.full_bc[1], 0, abort, lim);
+                    ok = cwait(&s.pmw, 0, abort, lim) && cwait(&s.full_bc[1], 0, abort, lim);
                     if (ok) {
                         tc_fence_after();
                         if (lane == 0) issue_g(1);
@@ -866,15 +908,15 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
             }
             for (int c = 0; ok && c + 2 < nc; ++c) {
                 // S of chunk c done: its B/C slot (C, B, w o X) is spent -- refill it with chunk c+2
-                ok = ewait(&s.mma_done[c & 1], (c >> 1) & 1, abort, lim);
+                ok = cwait(&s.mma_done[c & 1], (c >> 1) & 1, abort, lim);
                 if (!ok) break;
                 if (lane == 0) issue_bc(c + 2);
                 __syncwarp();
-                // G of chunk c+2 once the warps have read G of chunk c+1, the slot has landed and Ys of
+                // G of chunk c+2 once the warps have read G of chunk c+1, the slot has landed and Y of
                 // chunk c+1 is done (G must not sit in front of it in the tensor pipe)
-                ok = ewait(&s.pmw, (c + 1) & 1, abort, lim) &&
-                     ewait(&s.full_bc[c & 1], ((c + 2) >> 1) & 1, abort, lim) &&
-                     ewait(&s.ys_done, (c + 1) & 1, abort, lim);
+                ok = cwait(&s.pmw, (c + 1) & 1, abort, lim) &&
+                     cwait(&s.full_bc[c & 1], ((c + 2) >> 1) & 1, abort, lim) &&
+                     cwait(&s.ymma_done, (c + 1) & 1, abort, lim);
                 if (!ok) break;
                 tc_fence_after();
                 if (lane == 0) issue_g(c + 2);
@@ -883,10 +925,10 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
             if (lane == 0) {
                 if (live && !ok) raise_timeout(p, abort);
                 mma_commit(&s.fin2);
-                mbar_wait(&s.fin2, 0, nullptr, 100000000ull);
+                wait_loop(&s.fin2, 0, nullptr, 100000000ull);
                 if (*abort) {
                     for (int i = bc_issued > 2 ? bc_issued - 2 : 0; i < bc_issued; ++i)
-                        mbar_wait(&s.full_bc[i & 1], (i >> 1) & 1, nullptr, 100000000ull);
+                        wait_loop(&s.full_bc[i & 1], (i >> 1) & 1, nullptr, 100000000ull);
                 }
             }
             __syncwarp();
