@@ -159,7 +159,8 @@ struct PackedScanParams {
     int64_t yrs;
     int nw;                     // windows
     float *ws_S;                // [nw][H][P][N] what the chunks before a window's end leave of its last sequence
-    float *ws_hin;              // [nw][H][P][N] state entering the window
+    float *ws_hin;              // [nw][H][P][N] state entering the window, from the chain; NULL: few windows, each
+                                // forms it for itself (window_enter)
     float *ws_start;            // [nw][H][P][N] state that a sequence which begins in the window and leaves it
                                 // starts from, when it resumes: its slot may be written (h_out may be h_in) by
                                 // the window where it ends before the one where it begins reads it
@@ -220,6 +221,45 @@ inline bool allow_smem(F *kernel, int bytes, std::atomic<int> (&done)[64])
     done[dev].store(bytes, std::memory_order_relaxed);
     return true;
 }
+
+// The state entering window k, whose first chunk d continues a sequence that began in window b, is
+//   e^{dA_{k-1} + .. + dA_b} start + sum_w e^{dA_{k-1} + .. + dA_{w+1}} S_w,   b <= w < k:
+// n elements of it, `stride` apart, from `at` on, of head h (of the chain's result where there is one).
+template <bool k64, int n, typename F>
+__device__ __forceinline__ void window_enter(const PackedScanParams &p, int4 d, int k, int per, int h, int64_t at, int stride, F put)
+{
+    const int64_t PN = (int64_t)p.P * p.N;
+    if (p.ws_hin) {
+        const float *src = p.ws_hin + ((int64_t)k * p.H + h) * PN + at;
+#pragma unroll
+        for (int e = 0; e < n; ++e) put(e, src[(int64_t)e * stride]);
+        return;
+    }
+    const PackedSeq s = p.plan.seqs[d.z];
+    const int b = (k64 ? s.c64 : s.c128) / per;
+    float acc[n];
+#pragma unroll
+    for (int e = 0; e < n; ++e) acc[e] = 0.0f;
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int w = k - 1; w >= b; --w) {
+        const float f = expf(sum);
+        const float *src = p.ws_S + ((int64_t)w * p.H + h) * PN + at;
+#pragma unroll
+        for (int e = 0; e < n; ++e) acc[e] = fmaf(f, src[(int64_t)e * stride], acc[e]);
+        sum += p.ws_dA[(int64_t)w * p.H + h];
+    }
+    if (p.h_in && s.resume) {
+        const float f = expf(sum);
+        const float *src = p.ws_start + ((int64_t)b * p.H + h) * PN + at;
+#pragma unroll
+        for (int e = 0; e < n; ++e) acc[e] = fmaf(f, src[(int64_t)e * stride], acc[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < n; ++e) put(e, acc[e]);
+}
+
+constexpr int kMaxOwnWindows = 16;         // up to so many windows each forms its entering state for itself
 
 int launch_packed_plan(const PackedPlanParams &p, cudaStream_t st);
 int launch_packed_conv(const PackedConvParams &p, int dtype, cudaStream_t st);

@@ -101,10 +101,12 @@ ScanPlan scan_plan(int nseq, int64_t total, int64_t longest, int H, int P, int N
         if (best < 0 || cost < best) { best = cost; s.nw = (int)nw; }
     }
     if (s.carry) {
+        // S and the starts, the sums of dt A, and with many windows the entering states
         const size_t state = api_round256(sizeof(float) * (size_t)s.nw * H * P * N);
-        s.off_hin = state;
-        s.off_start = 2 * state;
-        s.off_dA = 3 * state;
+        const bool chain = s.nw > kMaxOwnWindows;
+        s.off_start = state;
+        s.off_hin = chain ? 2 * state : 0;
+        s.off_dA = (chain ? 3 : 2) * state;
         s.bytes = s.off_dA + api_round256(sizeof(float) * (size_t)s.nw * H);
     }
     return s;
@@ -278,7 +280,7 @@ int ssd_packed_scan_forward(const ssd_packed_scan_args *a, ssd_stream_t stream)
     if (sp.carry) {
         char *ws = static_cast<char *>(a->workspace);
         p.ws_S = reinterpret_cast<float *>(ws);
-        p.ws_hin = reinterpret_cast<float *>(ws + sp.off_hin);
+        p.ws_hin = sp.off_hin ? reinterpret_cast<float *>(ws + sp.off_hin) : nullptr;
         p.ws_start = reinterpret_cast<float *>(ws + sp.off_start);
         p.ws_dA = reinterpret_cast<float *>(ws + sp.off_dA);
     }

@@ -137,6 +137,15 @@ __global__ void __launch_bounds__(kThr, 2) packed_state_kernel(PackedScanParams 
     const int g = (int)((int64_t)h * p.G / p.H);
     float *xs = sm, *bs = xs + kQ * (P + 1), *hs = bs + kQ * (N + 1), *dts = hs + P * (N + 1), *cs = dts + kQ;
     for (int i = threadIdx.x; i < P * (N + 1); i += kThr) hs[i] = 0.0f;
+    if (t.begins) {
+        // the state that the sequence starts from, before its slot may be written
+        const PackedSeq q = p.plan.seqs[t.seq];
+        if (p.h_in && q.resume) {
+            const float4 *src = reinterpret_cast<const float4 *>(p.h_in + ((int64_t)q.slot * p.H + h) * P * N);
+            float4 *dst = reinterpret_cast<float4 *>(p.ws_start + ((int64_t)k * p.H + h) * P * N);
+            for (int i = threadIdx.x; i < P * N / 4; i += kThr) dst[i] = src[i];
+        }
+    }
     float dA = 0.0f;
     for (int c = t.c0; c < t.c1; ++c) {
         const int4 d = p.plan.chunk64[c];
@@ -186,10 +195,13 @@ __global__ void __launch_bounds__(kThr) packed_output_kernel(PackedScanParams p)
         load_dt(p, d.x, rows, h, dts, cs);
         if (c == c0 || (d.y & kChunkFirst)) {
             // a new sequence, or the window's first chunk of one that came before it
-            const float *src = (d.y & kChunkFirst)
-                ? window_start<true>(p, d, k, c1, h)
-                : p.ws_hin + ((int64_t)k * p.H + h) * PN;
-            for (int i = threadIdx.x; i < PN; i += kThr) hs[i / N * (N + 1) + i % N] = src ? src[i] : 0.0f;
+            if (d.y & kChunkFirst) {
+                const float *src = window_start<true>(p, d, k, c1, h);
+                for (int i = threadIdx.x; i < PN; i += kThr) hs[i / N * (N + 1) + i % N] = src ? src[i] : 0.0f;
+            } else {
+                for (int i = threadIdx.x; i < PN; i += kThr)
+                    window_enter<true, 1>(p, d, k, per, h, i, 1, [&](int, float v) { hs[i / N * (N + 1) + i % N] = v; });
+            }
         }
         __syncthreads();
         // M[i][j] = e^{cs_i - cs_j} dt_j (C_i . B_j), j <= i
@@ -264,11 +276,7 @@ __global__ void __launch_bounds__(kThr) packed_chain_kernel(PackedScanParams p)
         const float4 s = *reinterpret_cast<const float4 *>(p.ws_S + at);
         if (t.begins) {
             const PackedSeq q = p.plan.seqs[t.seq];
-            st = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (p.h_in && q.resume && q.slot >= 0) {
-                st = *reinterpret_cast<const float4 *>(p.h_in + ((int64_t)q.slot * p.H + h) * PN + e);
-                *reinterpret_cast<float4 *>(p.ws_start + at) = st;
-            }
+            st = p.h_in && q.resume ? *reinterpret_cast<const float4 *>(p.ws_start + at) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         const float a = expf(p.ws_dA[(int64_t)k * p.H + h]);
         st = make_float4(fmaf(a, st.x, s.x), fmaf(a, st.y, s.y), fmaf(a, st.z, s.z), fmaf(a, st.w, s.w));
@@ -289,7 +297,7 @@ int launch_generic_t(const PackedScanParams &p, bool carry, cudaStream_t st)
         prof_begin(st, kKPackedState);
         packed_state_kernel<T><<<grid, kThr, smA, st>>>(p);
         prof_end(st, kKPackedState);
-        const int rc = launch_packed_chain(p, true, st);
+        const int rc = p.ws_hin ? launch_packed_chain(p, true, st) : 0;
         if (rc) return rc;
     }
     prof_begin(st, kKPackedOutput);

@@ -38,6 +38,7 @@ constexpr int kQ = 128, kP = 64, kN = 128, kPN = kP * kN;
 
 struct Maps {
     CUtensorMap x, B, C, y;
+    CUtensorMap x64, B64;    // the same in boxes of 64 rows (pass A)
 };
 
 __device__ __forceinline__ void raise_timeout(const PackedScanParams &p, volatile int *abort)
@@ -106,18 +107,20 @@ __device__ __forceinline__ void chunk_sums(const float2 (&d)[4], float A2a, floa
 
 // =============================================================== pass A
 // One CTA per (window, head pair) that a sequence leaves: S[n][(h,p)] = sum_j B[j][n] (w_h o X_h)[j][p] over the
-// window's chunks of that sequence (all of 128 rows), accumulated in TMEM.  The chunks are walked
-// backwards, so that the decay from each to the window's end is known when it is scaled.
-// Warps 0..15 scale X into its two bf16 parts (the rounding in place, the rest beside it), warp 16 loads
-// and issues the products (two stages), warp 17 runs the dt sums a chunk or two ahead.
-constexpr int kStagesA = 2;
+// window's chunks of that sequence (all of 128 rows), accumulated in TMEM.  The rows are walked
+// backwards, 64 at a time, so that the decay from each to the window's end is known when it is scaled.
+// Warps 0..15 scale X into its two bf16 parts (the rounding in place, the rest beside it), warp 16 issues the
+// products, warp 17 the loads, warps 18 and 19 run the dt sums of a head each, ahead of the others.
+constexpr int kStagesA = 4;
+constexpr int kQA = 64;                  // rows of a step
+constexpr uint32_t kBoxA = kQA * 128;    // 64 rows x 64 columns of bf16
 constexpr int kScaleWarpsA = 16;
-constexpr int kThreadsA = 32 * (kScaleWarpsA + 2);
-constexpr uint32_t kStageA = 6 * kBox;   // B (2 boxes), X of head a and b, the remainders of X a and b
+constexpr int kThreadsA = 32 * (kScaleWarpsA + 4);
+constexpr uint32_t kStageA = 6 * kBoxA;   // B (2 boxes), X of head a and b, the remainders of X a and b
 
 struct SmemA {
     uint8_t stage[kStagesA][kStageA];
-    float w[kStagesA][2][kQ];
+    float w[kStagesA][2][kQA];
     uint64_t full[kStagesA], w_ready[kStagesA], xw_ready[kStagesA], empty[kStagesA];
     uint64_t acc_full, fin;
     uint32_t tmem;
@@ -136,23 +139,32 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
     const WindowTail wt = window_tail<false>(p.plan, n, (n + p.nw - 1) / p.nw, k);
     if (!wt.crosses) return;
     const int g = (int)((int64_t)ha * p.G / p.H);
-    const int nc = wt.c1 - wt.c0;
+    const int nc = (wt.c1 - wt.c0) * (kQ / kQA);     // steps
     const int row0 = p.plan.chunk128[wt.c0].x;       // the chunks are consecutive rows of one sequence
     const uint64_t lim = p.wait_limit_ns;
 
+    if (wt.begins) {
+        // the state that the sequence starts from, before its slot may be written
+        const PackedSeq sq = p.plan.seqs[wt.seq];
+        if (p.h_in && sq.resume) {
+            const float4 *src = reinterpret_cast<const float4 *>(p.h_in + ((int64_t)sq.slot * p.H + ha) * kPN);
+            float4 *dst = reinterpret_cast<float4 *>(p.ws_start + ((int64_t)k * p.H + ha) * kPN);
+            for (int i = threadIdx.x; i < 2 * kPN / 4; i += kThreadsA) dst[i] = src[i];
+        }
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStagesA; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.w_ready[i], 1);
-            mbar_init(&s.xw_ready[i], kScaleWarpsA);
+            mbar_init(&s.w_ready[i], 2);
+            mbar_init(&s.xw_ready[i], kScaleWarpsA / 2);
             mbar_init(&s.empty[i], 1);
         }
         mbar_init(&s.acc_full, 1);
         mbar_init(&s.fin, 1);
         s.abort = 0;
         fence_mbar_init();
-        prefetch_tmap(&maps.x);
-        prefetch_tmap(&maps.B);
+        prefetch_tmap(&maps.x64);
+        prefetch_tmap(&maps.B64);
     }
     if (warp == 0) { tmem_alloc(&s.tmem, 128); tmem_relinquish(); }
     __syncthreads();
@@ -162,15 +174,16 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
     const bool live = (int64_t)blockIdx.x != p.test_drop_unit;
 
     if (warp < kScaleWarpsA) {
-        const int hd = warp >> 3, j = 32 * (warp & 3) + lane, c0 = 4 * ((warp >> 2) & 1);
+        // warps 0..7 take the even steps, 8..15 the odd ones
+        const int hd = (warp >> 2) & 1, ti = 32 * (warp & 3) + lane, j = ti >> 1, c0 = 4 * (ti & 1);
         bool ok = true;
-        for (int it = 0; it < nc; ++it) {
+        for (int it = warp >> 3; it < nc; it += 2) {
             const int st = it % kStagesA;
             const uint32_t ph = (uint32_t)(it / kStagesA) & 1;
             ok = ewait(&s.full[st], ph, abort, lim) && ewait(&s.w_ready[st], ph, abort, lim);
             if (!ok) break;
             const float w = s.w[st][hd][j];
-            uint8_t *xrow = s.stage[st] + (2 + hd) * kBox, *lrow = s.stage[st] + (4 + hd) * kBox;
+            uint8_t *xrow = s.stage[st] + (2 + hd) * kBoxA, *lrow = s.stage[st] + (4 + hd) * kBoxA;
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) {
                 const uint32_t o = swz(j, c0 + cc);
@@ -205,23 +218,9 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
             }
         }
     } else if (warp == kScaleWarpsA) {
-        int issued = 0;   // lane 0: loads issued
-        auto issue_load = [&](int it) {
-            const int st = it % kStagesA;
-            const int t0 = row0 + (nc - 1 - it) * kQ;
-            uint8_t *sb = s.stage[st];
-            mbar_arrive_expect_tx(&s.full[st], 4 * kBox);
-            tma_load_3d(sb, &maps.B, &s.full[st], g * kN, t0, 0);
-            tma_load_3d(sb + kBox, &maps.B, &s.full[st], g * kN + 64, t0, 0);
-            tma_load_3d(sb + 2 * kBox, &maps.x, &s.full[st], ha * kP, t0, 0);
-            tma_load_3d(sb + 3 * kBox, &maps.x, &s.full[st], (ha + 1) * kP, t0, 0);
-            ++issued;
-        };
+        // ================================================= issuing warp (the whole warp waits, lane 0 issues)
         const uint32_t id_s = idesc_bf16(128, 128, 1, 1);   // A = B^T (MN-major), B = w o X (MN-major)
         bool ok = live;
-        int mmas = 0;
-        if (ok && lane == 0)
-            for (int it = 0; it < min(nc, kStagesA); ++it) issue_load(it);
         for (int it = 0; ok && it < nc; ++it) {
             const int st = it % kStagesA;
             ok = ewait(&s.xw_ready[st], (uint32_t)(it / kStagesA) & 1, abort, lim);
@@ -229,71 +228,124 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
             tc_fence_after();
             if (lane == 0) {
                 const uint32_t sb = smem_u32(s.stage[0]) + (uint32_t)st * kStageA;
-                const uint64_t db = smem_desc(sb, kBox, 1024);
-                const uint64_t dh = smem_desc(sb + 2 * kBox, kBox, 1024), dl = smem_desc(sb + 4 * kBox, kBox, 1024);
+                const uint64_t db = smem_desc(sb, kBoxA, 1024);
+                const uint64_t dh = smem_desc(sb + 2 * kBoxA, kBoxA, 1024), dl = smem_desc(sb + 4 * kBoxA, kBoxA, 1024);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
+                for (int kk = 0; kk < kQA / 16; ++kk)
                     mma_ss(tS, db + (uint64_t)(kk * 128), dh + (uint64_t)(kk * 128), id_s, it > 0 || kk > 0);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) mma_ss(tS, db + (uint64_t)(kk * 128), dl + (uint64_t)(kk * 128), id_s, true);
+                for (int kk = 0; kk < kQA / 16; ++kk) mma_ss(tS, db + (uint64_t)(kk * 128), dl + (uint64_t)(kk * 128), id_s, true);
                 mma_commit(&s.empty[st]);
             }
-            ++mmas;
             __syncwarp();
-            if (it + kStagesA < nc) {
-                ok = ewait(&s.empty[st], (uint32_t)(it / kStagesA) & 1, abort, lim);
-                if (!ok) break;
-                if (lane == 0) issue_load(it + kStagesA);
-                __syncwarp();
-            }
         }
         if (lane == 0) {
             if (live && !ok) raise_timeout(p, abort);
             mma_commit(&s.acc_full);
             mma_commit(&s.fin);
             mbar_wait(&s.fin, 0, nullptr, 100000000ull);
-            if (*abort) {
-                // drain: every load issued but not consumed by a product
-                for (int it = mmas; it < issued; ++it)
-                    mbar_wait(&s.full[it % kStagesA], (uint32_t)(it / kStagesA) & 1, nullptr, 100000000ull);
-            }
         }
         __syncwarp();
-    } else {
-        const float A2a = p.A[ha] * kLog2e, A2b = p.A[ha + 1] * kLog2e;
-        float sufa = 0.0f, sufb = 0.0f;     // sum of dt A (log2 units) after the chunks scanned so far
-        float2 dn[4];
+    } else if (warp == kScaleWarpsA + 1) {
+        // ================================================= loading warp: a stage is refilled once its product has read it
+        // (kept off the issuing warp, which would otherwise wait for each product to end)
+        int issued = 0;
         bool ok = live;
-        if (ok) load_dt(p, row0 + (nc - 1) * kQ, kQ, lane, ha, dn);
         for (int it = 0; ok && it < nc; ++it) {
             const int st = it % kStagesA;
-            if (it >= kStagesA) {           // the scaling warps are done with w[st]
-                ok = ewait(&s.xw_ready[st], (uint32_t)(it / kStagesA - 1) & 1, abort, lim);
+            if (it >= kStagesA) {
+                ok = ewait(&s.empty[st], (uint32_t)(it / kStagesA - 1) & 1, abort, lim);
                 if (!ok) break;
             }
-            float2 dc[4] = {dn[0], dn[1], dn[2], dn[3]};
-            if (it + 1 < nc) load_dt(p, row0 + (nc - 2 - it) * kQ, kQ, lane, ha, dn);
-            use_dt(p, kQ, lane, ha, dc);
-            float ca[4], cb[4];
-            chunk_sums(dc, A2a, A2b, lane, ca, cb);
-            const float tota = __shfl_sync(0xffffffffu, ca[3], 31), totb = __shfl_sync(0xffffffffu, cb[3], 31);
-            reinterpret_cast<float4 *>(s.w[st][0])[lane] =
-                make_float4(dc[0].x * ex2(tota - ca[0] + sufa), dc[1].x * ex2(tota - ca[1] + sufa),
-                            dc[2].x * ex2(tota - ca[2] + sufa), dc[3].x * ex2(tota - ca[3] + sufa));
-            reinterpret_cast<float4 *>(s.w[st][1])[lane] =
-                make_float4(dc[0].y * ex2(totb - cb[0] + sufb), dc[1].y * ex2(totb - cb[1] + sufb),
-                            dc[2].y * ex2(totb - cb[2] + sufb), dc[3].y * ex2(totb - cb[3] + sufb));
-            sufa += tota;
-            sufb += totb;
+            if (lane == 0) {
+                const int t0 = row0 + (nc - 1 - it) * kQA;
+                uint8_t *sb = s.stage[st];
+                mbar_arrive_expect_tx(&s.full[st], 4 * kBoxA);
+                tma_load_3d(sb, &maps.B64, &s.full[st], g * kN, t0, 0);
+                tma_load_3d(sb + kBoxA, &maps.B64, &s.full[st], g * kN + 64, t0, 0);
+                tma_load_3d(sb + 2 * kBoxA, &maps.x64, &s.full[st], ha * kP, t0, 0);
+                tma_load_3d(sb + 3 * kBoxA, &maps.x64, &s.full[st], (ha + 1) * kP, t0, 0);
+            }
+            ++issued;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.w_ready[st]);
         }
         if (lane == 0) {
             if (live && !ok) raise_timeout(p, abort);
-            if (ok && !*abort) {
-                p.ws_dA[(int64_t)k * p.H + ha] = sufa * kLn2;
-                p.ws_dA[(int64_t)k * p.H + ha + 1] = sufb * kLn2;
+            // the last load issued into each stage lands before the CTA's shared memory is released (an
+            // earlier one into the same stage has been waited on by the scaling warps)
+            if (*abort)
+                for (int it = issued > kStagesA ? issued - kStagesA : 0; it < issued; ++it)
+                    mbar_wait(&s.full[it % kStagesA], (uint32_t)(it / kStagesA) & 1, nullptr, 100000000ull);
+        }
+        __syncwarp();
+    } else {
+        // one warp per head: w of every chunk, ready in registers before its place is free
+        const int hd = warp - kScaleWarpsA - 2, h = ha + hd;
+        const float A2 = p.A[h] * kLog2e;
+        const bool used = p.dt_bias || p.dt_softplus || p.dt_max > 0.0f;
+        float suf = 0.0f;                   // sum of dt A (log2 units) after the chunks scanned so far
+        // dt of four steps at a time, loaded while the four before them are used
+        float dn[4][2], dc[4][2];
+        auto load = [&](int it0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int it = min(it0 + e, nc - 1);
+                const float *src = p.dt + ((int64_t)row0 + (int64_t)(nc - 1 - it) * kQA + 2 * lane) * p.H + h;
+                dn[e][0] = src[0];
+                dn[e][1] = src[p.H];
             }
+        };
+        bool ok = live;
+        load(0);
+#pragma unroll 1
+        for (int it0 = 0; ok && it0 < nc; it0 += 4) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { dc[e][0] = dn[e][0]; dc[e][1] = dn[e][1]; }
+            if (it0 + 4 < nc) load(it0 + 4);
+            // the four steps' sums side by side: one step's chain of shuffles alone took longer than its product
+            float d[4][2], c0[4], c1[4], inc[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    d[e][q] = used ? dt_effective(dc[e][q], p.dt_bias, h, p.dt_softplus, p.dt_min, p.dt_max) : dc[e][q];
+                c0[e] = d[e][0] * A2;
+                c1[e] = c0[e] + d[e][1] * A2;
+                inc[e] = c1[e];
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float t = __shfl_up_sync(0xffffffffu, inc[e], o);
+                    if (lane >= o) inc[e] += t;
+                }
+            float2 w2[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float ex = inc[e] - c1[e];
+                const float tot = __shfl_sync(0xffffffffu, inc[e], 31);
+                // decay from row j (exclusive) to the window's end: tot - cs_j + the later steps
+                w2[e] = make_float2(d[e][0] * ex2(tot - (c0[e] + ex) + suf), d[e][1] * ex2(tot - inc[e] + suf));
+                if (it0 + e < nc) suf += tot;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int it = it0 + e;
+                if (it >= nc) break;
+                const int st = it % kStagesA;
+                if (it >= kStagesA) {           // the scaling warps are done with w[st]
+                    ok = ewait(&s.xw_ready[st], (uint32_t)(it / kStagesA - 1) & 1, abort, lim);
+                    if (!ok) break;
+                }
+                reinterpret_cast<float2 *>(s.w[st][hd])[lane] = w2[e];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.w_ready[st]);
+            }
+        }
+        if (lane == 0) {
+            if (live && !ok) raise_timeout(p, abort);
+            if (ok && !*abort) p.ws_dA[(int64_t)k * p.H + h] = suf * kLn2;
         }
         __syncwarp();
     }
@@ -638,16 +690,16 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                 }
                 // where a sequence ends, its state goes to its slot and the next one's start takes its place; a
                 // start from zero needs no registers, so that the old state can leave after Ys was let go
-                const float *src = nullptr;
-                if (ends)
-                    src = (dn.y & kChunkFirst) ? window_start<false>(p, dn, k, first + nc, hh)
-                                               : p.ws_hin + ((int64_t)k * p.H + hh) * kPN;
+                const float *src = ends && (dn.y & kChunkFirst) ? window_start<false>(p, dn, k, first + nc, hh) : nullptr;
+                const bool inside = ends && !(dn.y & kChunkFirst);      // (the window's first chunk of a sequence from before)
+                if (inside)
+                    window_enter<false, 32>(p, dn, k, per, hh, (int64_t)p0 * kN + r, kN, [&](int e, float v) { hv[e] = __float_as_uint(v); });
                 if (src) {
                     if (slot >= 0) store_state(slot, hv);
 #pragma unroll
                     for (int pp = 0; pp < 32; ++pp) hv[pp] = __float_as_uint(src[(p0 + pp) * kN + r]);
                 }
-                if (ends && !src) state_zero();
+                if (ends && !src && !inside) state_zero();
                 else state_step(hv);
                 tmem_wait_st();
                 fence_proxy_async_smem();   // hp, read by Ys of chunk c+1
@@ -959,6 +1011,7 @@ int launch_packed_scan_tc(const PackedScanParams &p, bool carry, cudaStream_t st
     const int64_t gn = (int64_t)p.G * p.N, hp = (int64_t)p.H * p.P, rows = p.plan.total > 0 ? p.plan.total : 1;
     if (p.plan.total > 0 &&
         (!encode_bf16(enc, &maps.x, p.x, hp, rows, 1, p.xrs, 0) || !encode_bf16(enc, &maps.B, p.B, gn, rows, 1, p.Brs, 0) ||
+         !encode_bf16(enc, &maps.x64, p.x, hp, rows, 1, p.xrs, 0, kQA) || !encode_bf16(enc, &maps.B64, p.B, gn, rows, 1, p.Brs, 0, kQA) ||
          !encode_bf16(enc, &maps.C, p.C, gn, rows, 1, p.Crs, 0) || !encode_bf16(enc, &maps.y, p.y, hp, rows, 1, p.yrs, 0)))
         return 6;
     static std::atomic<int> done_a[64], done_c[64];
@@ -968,7 +1021,7 @@ int launch_packed_scan_tc(const PackedScanParams &p, bool carry, cudaStream_t st
         prof_begin(st, kKPackedState);
         packed_state_tc_kernel<<<units, kThreadsA, kSmemA, st>>>(maps, p);
         prof_end(st, kKPackedState);
-        const int rc = launch_packed_chain(p, false, st);
+        const int rc = p.ws_hin ? launch_packed_chain(p, false, st) : 0;
         if (rc) return rc;
     }
     prof_begin(st, kKPackedOutput);
