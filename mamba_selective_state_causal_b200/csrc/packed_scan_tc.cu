@@ -84,25 +84,31 @@ __device__ __forceinline__ void use_dt(const PackedScanParams &p, int rows, int 
         }
 }
 
-// inclusive sums of dt A (log2 units) over the chunk: rows 4 lane .. 4 lane + 3 of both heads
-__device__ __forceinline__ void chunk_sums(const float2 (&d)[4], float A2a, float A2b, int lane, float (&ca)[4], float (&cb)[4])
+// Sums of dt A (log2 units) over the chunk's rows AFTER each row (rows 4 lane .. 4 lane + 3 of both heads), and over all
+// of its rows.  Taken from the chunk's end, they are exact where they matter: a row near the end weighs most in the
+// state that leaves the chunk, and its sum is short (differences of sums from the front were off by the rounding of the
+// whole chunk's sum, three times the error of all else at A = -16).
+__device__ __forceinline__ void chunk_sums(const float2 (&d)[4], float A2a, float A2b, int lane, float (&sa)[4], float (&sb)[4],
+                                           float &ta, float &tb)
 {
-    float sa = 0.0f, sb = 0.0f;
+    float a[4], b[4], ia = 0.0f, ib = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        sa += d[k].x * A2a; ca[k] = sa;
-        sb += d[k].y * A2b; cb[k] = sb;
+    for (int k = 3; k >= 0; --k) {
+        a[k] = d[k].x * A2a; ia += a[k];
+        b[k] = d[k].y * A2b; ib += b[k];
     }
-    float ia = sa, ib = sb;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const float ta = __shfl_up_sync(0xffffffffu, ia, o), tb = __shfl_up_sync(0xffffffffu, ib, o);
-        if (lane >= o) { ia += ta; ib += tb; }
+        const float qa = __shfl_down_sync(0xffffffffu, ia, o), qb = __shfl_down_sync(0xffffffffu, ib, o);
+        if (lane + o < 32) { ia += qa; ib += qb; }
     }
-    float xa = __shfl_up_sync(0xffffffffu, ia, 1), xb = __shfl_up_sync(0xffffffffu, ib, 1);
-    if (lane == 0) { xa = 0.0f; xb = 0.0f; }
+    ta = __shfl_sync(0xffffffffu, ia, 0);
+    tb = __shfl_sync(0xffffffffu, ib, 0);
+    sa[3] = __shfl_down_sync(0xffffffffu, ia, 1);
+    sb[3] = __shfl_down_sync(0xffffffffu, ib, 1);
+    if (lane == 31) { sa[3] = 0.0f; sb[3] = 0.0f; }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) { ca[k] += xa; cb[k] += xb; }
+    for (int k = 2; k >= 0; --k) { sa[k] = sa[k + 1] + a[k + 1]; sb[k] = sb[k + 1] + b[k + 1]; }
 }
 
 // =============================================================== pass A
@@ -303,30 +309,30 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
             for (int e = 0; e < 4; ++e) { dc[e][0] = dn[e][0]; dc[e][1] = dn[e][1]; }
             if (it0 + 4 < nc) load(it0 + 4);
             // the four steps' sums side by side: one step's chain of shuffles alone took longer than its product
-            float d[4][2], c0[4], c1[4], inc[4];
+            float d[4][2], a1[4], inc[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
                     d[e][q] = used ? dt_effective(dc[e][q], p.dt_bias, h, p.dt_softplus, p.dt_min, p.dt_max) : dc[e][q];
-                c0[e] = d[e][0] * A2;
-                c1[e] = c0[e] + d[e][1] * A2;
-                inc[e] = c1[e];
+                a1[e] = d[e][1] * A2;
+                inc[e] = a1[e] + d[e][0] * A2;
             }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float t = __shfl_up_sync(0xffffffffu, inc[e], o);
-                    if (lane >= o) inc[e] += t;
+                    const float t = __shfl_down_sync(0xffffffffu, inc[e], o);
+                    if (lane + o < 32) inc[e] += t;
                 }
             float2 w2[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float ex = inc[e] - c1[e];
-                const float tot = __shfl_sync(0xffffffffu, inc[e], 31);
-                // decay from row j (exclusive) to the window's end: tot - cs_j + the later steps
-                w2[e] = make_float2(d[e][0] * ex2(tot - (c0[e] + ex) + suf), d[e][1] * ex2(tot - inc[e] + suf));
+                float after = __shfl_down_sync(0xffffffffu, inc[e], 1);
+                if (lane == 31) after = 0.0f;
+                const float tot = __shfl_sync(0xffffffffu, inc[e], 0);
+                // decay from row j (exclusive) to the window's end: the rows after it in the step, and the later steps
+                w2[e] = make_float2(d[e][0] * ex2(after + a1[e] + suf), d[e][1] * ex2(after + suf));
                 if (it0 + e < nc) suf += tot;
             }
 #pragma unroll
@@ -391,10 +397,11 @@ struct SmemC {
     uint8_t bc[2][4 * kBox];   // ring slot: C box 0, C box 1, B box 0, B box 1; later w o X in the C half
     uint8_t x[2][2 * kBox];    // X slot: head a box, head b box (X, then y)
     uint8_t hp[2 * kBox];      // bf16 state of head a, head b (rows n, cols p); later the remainder of w o X
-    float cvs[2][kQ];          // chunk-inclusive sums of dt A (log2 units), per head
+    float cvs[2][kQ];          // sums of dt A (log2 units) after each row of the chunk, per head
     float dvs[2][kQ];          // dt, per head
     float fs[2][3 * 32];       // dt_j e^{cs_end(J) - cs_j} for the 32-row blocks J = 0..2
     int4 desc[2];              // descriptors of chunks c and c+1
+    float tot[2];              // sums of dt A over the chunk
     uint64_t full_bc[2], full_x[2], g_done, ys_done, ymma_done, mma_done[2];
     uint64_t fin, fin2;
     uint64_t pmw, pm_ready, xw_ready, ys_go, scan_ready;
@@ -486,7 +493,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                 v.w = pack_bf16x2(__uint_as_float(hv[8 * c4 + 6]), __uint_as_float(hv[8 * c4 + 7]));
                 sts128(dst + swz(r, (p0 >> 3) + c4), v);
             }
-            const float dec = ex2(s.cvs[hd][kQ - 1]);
+            const float dec = ex2(s.tot[hd]);
 #pragma unroll
             for (int pp = 0; pp < 32; pp += 2) {
                 const float2 q2 = mul2(make_float2(__uint_as_float(hv[pp]), __uint_as_float(hv[pp + 1])), make_float2(dec, dec));
@@ -533,7 +540,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                 uint32_t pk[16];
                 if (J < q) {
                     // below the diagonal: e^{cs_r - cs_j} = e^{cs_r - m_J} e^{m_J - cs_j}
-                    const float E = ex2(csr - s.cvs[hd][32 * J + 31]);
+                    const float E = ex2(s.cvs[hd][32 * J + 31] - csr);
                     const float2 E2 = make_float2(E, E);
                     uint32_t gv[32];
                     tmem_ld32(tG + lane_base + 32 * J, gv);
@@ -558,8 +565,8 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                     const float *cvb = &s.cvs[hd][32 * J], *dvb = &s.dvs[hd][32 * J];
                     const float m16 = cvb[15];
                     const bool lo = lane < 16;
-                    const float a_r = ex2(csr - m16);                                   // <= 1 for lane >= 16
-                    const float b_own = dvb[lane & 15] * ex2(m16 - cvb[lane & 15]);     // <= dt for lane < 16
+                    const float a_r = ex2(m16 - csr);                                   // <= 1 for lane >= 16
+                    const float b_own = dvb[lane & 15] * ex2(cvb[lane & 15] - m16);     // <= dt for lane < 16
                     const int xo = lo ? 0 : 16;
 #pragma unroll
                     for (int k2 = 0; k2 < 8; ++k2) {
@@ -569,7 +576,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                             const int kc = 2 * k2 + e;
                             const int x = xo + kc;
                             const float g_x = __uint_as_float(lo ? gv[kc] : gv[16 + kc]);
-                            float t = g_x * ex2(csr - cvb[x]) * dvb[x];
+                            float t = g_x * ex2(cvb[x] - csr) * dvb[x];
                             t = x > lane ? 0.0f : t;
                             const float bk = __shfl_sync(0xffffffffu, b_own, kc);
                             vl[e] = lo ? t : __uint_as_float(gv[kc]) * (a_r * bk);
@@ -599,7 +606,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
             tc_fence_after();
             const int rows = s.desc[c & 1].y & kChunkRows;
             {
-                const float e_r = ex2(s.cvs[hd][r]);
+                const float e_r = ex2(s.tot[hd] - s.cvs[hd][r]);
                 uint32_t tv[32];
                 tmem_ld32(tT + lane_base + 32 * cs, tv);
                 tmem_wait_ld(tv);
@@ -631,7 +638,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
             {
                 const int ti = 32 * (warp & 7) + lane;
                 const int j = ti >> 1, ch = 4 * (ti & 1);
-                const float w = s.dvs[hd][j] * ex2(s.cvs[hd][kQ - 1] - s.cvs[hd][j]);
+                const float w = s.dvs[hd][j] * ex2(s.cvs[hd][j]);
                 const uint8_t *src = xs + hd * kBox;
                 uint8_t *dst = s.bc[c & 1] + hd * kBox, *rem = s.hp + hd * kBox;
 #pragma unroll 1
@@ -896,14 +903,14 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                 const int4 d = dn;
                 if (c + 1 < nc) dn = chunks[c + 1];
                 use_dt(p, d.y & kChunkRows, lane, ha, dt);
-                float ca[4], cb[4];
-                chunk_sums(dt, A2a, A2b, lane, ca, cb);
+                float ca[4], cb[4], ta, tb;
+                chunk_sums(dt, A2a, A2b, lane, ca, cb, ta, tb);
                 // the sum at the end of this lane's 32-row block (row 32 J + 31 = lane 8 J + 7)
                 const float ea = __shfl_sync(0xffffffffu, ca[3], lane | 7), eb = __shfl_sync(0xffffffffu, cb[3], lane | 7);
-                const float4 fa = make_float4(dt[0].x * ex2(ea - ca[0]), dt[1].x * ex2(ea - ca[1]),
-                                              dt[2].x * ex2(ea - ca[2]), dt[3].x * ex2(ea - ca[3]));
-                const float4 fb = make_float4(dt[0].y * ex2(eb - cb[0]), dt[1].y * ex2(eb - cb[1]),
-                                              dt[2].y * ex2(eb - cb[2]), dt[3].y * ex2(eb - cb[3]));
+                const float4 fa = make_float4(dt[0].x * ex2(ca[0] - ea), dt[1].x * ex2(ca[1] - ea),
+                                              dt[2].x * ex2(ca[2] - ea), dt[3].x * ex2(ca[3] - ea));
+                const float4 fb = make_float4(dt[0].y * ex2(cb[0] - eb), dt[1].y * ex2(cb[1] - eb),
+                                              dt[2].y * ex2(cb[2] - eb), dt[3].y * ex2(cb[3] - eb));
                 if (lane < 2 && c > 0 && (d.y & kChunkFirst)) {
                     const float *src = window_start<false>(p, d, k, first + nc, ha + lane);
                     if (src)
@@ -922,7 +929,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                     reinterpret_cast<float4 *>(s.fs[0])[lane] = fa;
                     reinterpret_cast<float4 *>(s.fs[1])[lane] = fb;
                 }
-                if (lane == 0) s.desc[c & 1] = d;
+                if (lane == 0) { s.desc[c & 1] = d; s.tot[0] = ta; s.tot[1] = tb; }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.scan_ready);
                 if (c + 1 < nc) load_dt(p, dn.x, dn.y & kChunkRows, lane, ha, dt);
