@@ -170,6 +170,27 @@ struct PackedScanParams {
     int64_t test_drop_unit;
 };
 
+// The tensor-core gradient of the packed scan (packed_grad_tc.cu)
+struct PackedGradParams {
+    PackedPlan plan;
+    int H, G;
+    const void *x, *B, *C, *dy;
+    int64_t xrs, Brs, Crs, dyrs;
+    const float *dt, *A, *D;
+    const float *h_in;          // [slots][H][P][N] or NULL
+    const float *dh_out;        // [nseq][H][P][N] or NULL
+    float *dx, *dB, *dC, *ddt, *dA, *dD, *dh_in;
+    uint8_t *ws_img;            // [m64][H][2] h entering the chunk and Gam arriving at its last row, as operands
+    float *ws_part;             // [blocks of heads][dB, dC][64][N]
+    float *ws_sums;             // [CTAs][2] partial sums of an item
+    float *ws_pA, *ws_pD;       // [H][m64]
+    unsigned int *status;
+    uint64_t wait_limit_ns;
+};
+struct PackedGradLayout {
+    size_t off_part, off_sums, off_pA, off_pD, bytes;
+};
+
 // Whether window k hands a sequence on to window k + 1, and from which chunk of window k that
 // sequence's state is built: c0 = first chunk (of the sequence, or of the window when the sequence
 // began before it), c1 = end of the window.
@@ -267,6 +288,8 @@ int launch_packed_conv_backward(const PackedConvBwdParams &p, int dtype, cudaStr
 bool packed_scan_tc_shape(int dtype, int H, int P, int N, int G);
 int launch_packed_scan_tc(const PackedScanParams &p, bool carry, cudaStream_t st);
 int launch_packed_scan_generic(const PackedScanParams &p, bool carry, int dtype, cudaStream_t st);
+PackedGradLayout packed_grad_layout(int64_t nseq, int64_t total, int H, int ctas);
+int launch_packed_grad_tc(const PackedGradParams &p, int ctas, cudaStream_t st);
 int launch_packed_chain(const PackedScanParams &p, bool k64, cudaStream_t st);
 constexpr int kPackedMaxSlotted = 16384;   // sequences of one plan that names slots
 

@@ -95,7 +95,9 @@ ScanPlan scan_plan(int nseq, int64_t total, int64_t longest, int H, int P, int N
     // a sequence is handed on between windows only if it has more than one chunk
     s.carry = std::min<int64_t>(longest, total) > (s.tc ? 128 : 64);
     int64_t best = -1;
-    for (int64_t nw = 1; nw <= std::min<int64_t>(chunks, 1024); ++nw) {
+    // (beyond four waves a window more changes nothing)
+    const int64_t most = std::min<int64_t>(chunks, std::max<int64_t>(4, 4 * slots / units));
+    for (int64_t nw = 1; nw <= most; ++nw) {
         const int64_t per = (chunks + nw - 1) / nw, waves = (nw * units + slots - 1) / slots;
         const int64_t cost = waves * (per + 2);
         if (best < 0 || cost < best) { best = cost; s.nw = (int)nw; }
@@ -134,6 +136,8 @@ ScanBwdPlan scan_bwd_plan(int nseq, int64_t total, int H, int P, int N)
     s.off_dB = s.off_pD + parts;
     s.off_dC = s.off_dB + rows;
     s.bytes = s.off_dC + rows;
+    // (the tensor-core form's, where a call of these sizes may take it)
+    if (P == 64 && N == 128 && total > 0) s.bytes = std::max(s.bytes, packed_grad_layout(nseq, total, H, api_sm_count()).bytes);
     return s;
 }
 
@@ -324,6 +328,28 @@ int ssd_packed_scan_backward(const ssd_packed_scan_bwd_args *a, ssd_stream_t str
         if (!api_aligned(v)) return api_fail(SSD_ERR_ALIGN, "states and gradient outputs must be 16-byte aligned");
     const ScanBwdPlan pl = scan_bwd_plan(a->nseq, a->total, a->H, a->P, a->N);
     if ((rc = check_workspace(a->workspace, a->workspace_bytes, pl.bytes))) return rc;
+    if (a->total > 0 && a->dtype == SSD_BF16 && a->P == 64 && a->N == 128) {
+        const int ctas = api_sm_count();
+        const PackedGradLayout l = packed_grad_layout(a->nseq, a->total, a->H, ctas);
+        PackedGradParams q{};
+        if ((rc = status_or_fail(&q.status))) return rc;
+        q.plan = packed_view(a->plan, a->nseq, a->total);
+        q.H = a->H; q.G = a->G;
+        q.x = a->x; q.xrs = a->x_row_stride; q.B = a->B; q.Brs = a->B_row_stride; q.C = a->C; q.Crs = a->C_row_stride;
+        q.dy = a->dy; q.dyrs = a->dy_row_stride;
+        q.dt = a->dt; q.A = a->A; q.D = a->D; q.h_in = a->h_in; q.dh_out = a->dh_out;
+        q.dx = a->dx; q.dB = a->dB; q.dC = a->dC; q.ddt = a->ddt; q.dA = a->dA; q.dD = a->dD; q.dh_in = a->dh_in;
+        uint8_t *ws = static_cast<uint8_t *>(a->workspace);
+        q.ws_img = ws;
+        q.ws_part = reinterpret_cast<float *>(ws + l.off_part);
+        q.ws_sums = reinterpret_cast<float *>(ws + l.off_sums);
+        q.ws_pA = reinterpret_cast<float *>(ws + l.off_pA);
+        q.ws_pD = reinterpret_cast<float *>(ws + l.off_pD);
+        q.wait_limit_ns = api_wait_limit_ns();
+        rc = launch_packed_grad_tc(q, ctas, st);
+        if (rc == 2) return api_fail(SSD_ERR_SHAPE, "packed scan backward grid too large");
+        return rc ? cuda_fail("packed scan backward") : api_ok();
+    }
     int dev = 0, smem = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
         return api_fail(SSD_ERR_LAUNCH, "no CUDA device available");

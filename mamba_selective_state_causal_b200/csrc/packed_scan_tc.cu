@@ -361,18 +361,6 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
 }
 
 // =============================================================== pass C
-// A bounded wait whose loop is out of line: the output kernel has some thirty of them, and with the loops in place
-// the warps waited for instructions (298 against 282 us at 65536 rows of 32 heads).
-static __device__ __noinline__ bool wait_loop(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns)
-{
-    return mbar_wait(bar, parity, abort, limit_ns);
-}
-__device__ __forceinline__ bool cwait(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns)
-{
-    const bool ok = mbar_try_wait(bar, parity) || wait_loop(bar, parity, abort, limit_ns);
-    return __all_sync(0xffffffffu, ok);
-}
-
 // One CTA per (window, head pair): 16 compute warps, an issuing warp, a store warp, a B/C warp and a scan warp.
 // The output accumulator T of a chunk first receives Ys = C [h_a | h_b]^T, which the compute warps scale
 // row by row by e^{cs_i}; Y = Pm X then accumulates onto it, so the epilogue only adds D x.  Per chunk c:

@@ -171,7 +171,6 @@ __device__ __forceinline__ void split8(uint4 v, float w, uint4 &hi, uint4 &lo)
     lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-template <bool kPacked>
 __global__ void __launch_bounds__(kSumTcThreads) bwd_chunk_summary_tc_kernel(BwdParams p)
 {
     extern __shared__ __align__(1024) uint8_t sst_raw[];
@@ -180,9 +179,8 @@ __global__ void __launch_bounds__(kSumTcThreads) bwd_chunk_summary_tc_kernel(Bwd
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int P = 64, N = 128;
     const int g = (int)((int64_t)h * p.G / p.H);
-    int64_t t0;
-    int rows;
-    if (!bwd_chunk<kPacked>(p, c, t0, rows)) return;
+    const int64_t t0 = (int64_t)c * kQb;
+    const int rows = (int)(p.L - t0 < kQb ? p.L - t0 : kQb);
     if (tid == 0) {
         mbar_init(&s.done, 1);
         fence_mbar_init();
@@ -891,7 +889,6 @@ __device__ __forceinline__ void store_pieces3(uint8_t (&dst)[3][2 * kSumBox], co
 // launch at 32 and 48, 0.509 at 74, 0.512 at 110, no gain at a whole wave (296), 0.535 without
 constexpr int kGradAhead = 32;
 
-template <bool kPacked>
 __global__ void __launch_bounds__(kGradTcThreads, 2) bwd_chunk_grad_tc_kernel(BwdParams p)
 {
     extern __shared__ __align__(1024) uint8_t sgt_raw[];
@@ -900,9 +897,8 @@ __global__ void __launch_bounds__(kGradTcThreads, 2) bwd_chunk_grad_tc_kernel(Bw
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int P = 64, N = 128;
     const int g = (int)((int64_t)h * p.G / p.H);
-    int64_t t0;
-    int rows;
-    if (!bwd_chunk<kPacked>(p, c, t0, rows)) return;
+    const int64_t t0 = (int64_t)c * kQb;
+    const int rows = (int)(p.L - t0 < kQb ? p.L - t0 : kQb);
     const int64_t unit = ((int64_t)bi * p.H + h) * p.nch + c;
     const float Ah = p.A[h];
     const float Dh = p.D ? p.D[h] : 0.0f;
@@ -1445,17 +1441,18 @@ int launch_bwd_t(BwdParams p, cudaStream_t st)
         return 7;
     const dim3 grid((unsigned)p.nch, (unsigned)p.H, (unsigned)p.b);
     // bf16 inputs at P = 64, N = 128: the summaries and the gradients on the tensor cores
-    const bool tc_summary = std::is_same<T, __nv_bfloat16>::value && p.P == 64 && p.N == 128;
+    // (a packed batch of that kind goes to packed_grad_tc.cu, unless it has no rows)
+    const bool tc_summary = !kPacked && std::is_same<T, __nv_bfloat16>::value && p.P == 64 && p.N == 128;
     const size_t s_tc = sizeof(SmemSumTc) + 1024, s_gt = sizeof(SmemGradTc) + 1024;
-    if (tc_summary && (cudaFuncSetAttribute(bwd_chunk_summary_tc_kernel<kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (tc_summary && (cudaFuncSetAttribute(bwd_chunk_summary_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             (int)s_tc) != cudaSuccess ||
-                       cudaFuncSetAttribute(bwd_chunk_grad_tc_kernel<kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       cudaFuncSetAttribute(bwd_chunk_grad_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             (int)s_gt) != cudaSuccess ||
-                       cudaFuncSetAttribute(bwd_chunk_grad_tc_kernel<kPacked>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                       cudaFuncSetAttribute(bwd_chunk_grad_tc_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                             (int)cudaSharedmemCarveoutMaxShared) != cudaSuccess))
         return 7;
     prof_begin(st, kKBwdSummary);
-    if (tc_summary) bwd_chunk_summary_tc_kernel<kPacked><<<grid, kSumTcThreads, s_tc, st>>>(p);
+    if (tc_summary) bwd_chunk_summary_tc_kernel<<<grid, kSumTcThreads, s_tc, st>>>(p);
     else bwd_chunk_summary_kernel<T, kPacked><<<grid, kBwdThreads, s1, st>>>(p);
     prof_end(st, kKBwdSummary);
     const int64_t PN = (int64_t)p.P * p.N;
@@ -1468,7 +1465,7 @@ int launch_bwd_t(BwdParams p, cudaStream_t st)
     bwd_adjoint_chain_kernel<kPacked><<<dim3(slices * (unsigned)(kPacked ? p.nseq : 1), (unsigned)p.H, (unsigned)p.b), kBwdThreads, 0, st>>>(p);
     prof_end(st, kKBwdAdjoint);
     prof_begin(st, kKBwdGrad);
-    if (tc_summary) bwd_chunk_grad_tc_kernel<kPacked><<<grid, kGradTcThreads, s_gt, st>>>(p);
+    if (tc_summary) bwd_chunk_grad_tc_kernel<<<grid, kGradTcThreads, s_gt, st>>>(p);
     else bwd_chunk_grad_kernel<T, kPacked><<<grid, kGradThreads, s2, st>>>(p);
     prof_end(st, kKBwdGrad);
     prof_begin(st, kKBwdReduce);
