@@ -85,16 +85,6 @@ __device__ __forceinline__ void tmem_wait_ld8(uint32_t (&r)[8])
                  : "memory");
 }
 
-// One lane of a converged warp, in the form in which the compiler knows that it is one: products issued under
-// lane == 0 came 130 cycles apart
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-    return e != 0;
-}
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
-
 // n K-steps, their operands' descriptors sa and sb apart
 template <int n>
 __device__ __forceinline__ void mma_steps(uint32_t d, uint64_t a, uint64_t b, uint32_t sa, uint32_t sb, uint32_t idesc, bool accumulate)

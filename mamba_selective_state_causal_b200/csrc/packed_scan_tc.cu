@@ -226,26 +226,28 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
     } else if (warp == kScaleWarpsA) {
         // ================================================= issuing warp (the whole warp waits, lane 0 issues)
         const uint32_t id_s = idesc_bf16(128, 128, 1, 1);   // A = B^T (MN-major), B = w o X (MN-major)
+        const uint32_t tSu = uniform(tS);
         bool ok = live;
         for (int it = 0; ok && it < nc; ++it) {
             const int st = it % kStagesA;
             ok = ewait(&s.xw_ready[st], (uint32_t)(it / kStagesA) & 1, abort, lim);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t sb = smem_u32(s.stage[0]) + (uint32_t)st * kStageA;
+            const uint32_t sb = smem_u32(s.stage[0]) + uniform(st) * kStageA;
+            if (elect_one()) {
                 const uint64_t db = smem_desc(sb, kBoxA, 1024);
                 const uint64_t dh = smem_desc(sb + 2 * kBoxA, kBoxA, 1024), dl = smem_desc(sb + 4 * kBoxA, kBoxA, 1024);
 #pragma unroll
                 for (int kk = 0; kk < kQA / 16; ++kk)
-                    mma_ss(tS, db + (uint64_t)(kk * 128), dh + (uint64_t)(kk * 128), id_s, it > 0 || kk > 0);
+                    mma_ss(tSu, db + (uint64_t)(kk * 128), dh + (uint64_t)(kk * 128), id_s, it > 0 || kk > 0);
 #pragma unroll
-                for (int kk = 0; kk < kQA / 16; ++kk) mma_ss(tS, db + (uint64_t)(kk * 128), dl + (uint64_t)(kk * 128), id_s, true);
+                for (int kk = 0; kk < kQA / 16; ++kk) mma_ss(tSu, db + (uint64_t)(kk * 128), dl + (uint64_t)(kk * 128), id_s, true);
                 mma_commit(&s.empty[st]);
             }
             __syncwarp();
         }
-        if (lane == 0) {
+        __syncwarp();
+        if (elect_one()) {
             if (live && !ok) raise_timeout(p, abort);
             mma_commit(&s.acc_full);
             mma_commit(&s.fin);
@@ -447,7 +449,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
     if (warp == 0) { tmem_alloc(&s.tmem, 512); tmem_relinquish(); }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = s.tmem;
+    const uint32_t tm = uniform(s.tmem);
     const uint32_t tG = tm, tPm = tm + 128, tT = tm + 256, tH = tm + 384;
     volatile int *abort = &s.abort;
     const bool live = (int64_t)blockIdx.x != p.test_drop_unit;
@@ -742,7 +744,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
             for (int kk = 0; kk < 8; ++kk) mma_ss(tG, dc + koff(kk), db + koff(kk), id_g, kk > 0);
             mma_commit(&s.g_done);
         };
-        // The whole warp waits (warp-uniform outcome); lane 0 issues.
+        // The whole warp waits (warp-uniform outcome); one lane issues.
         if (warp == kComputeWarps) {
             // ============================================= issuing warp: Y, S, Ys (and G of chunk 0)
             auto issue_ys = [&](int c) {
@@ -759,12 +761,12 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                 ok = cwait(&s.full_bc[0], 0, abort, lim);
                 if (ok) {
                     tc_fence_after();
-                    if (lane == 0) issue_g(0);
+                    if (elect_one()) issue_g(0);
                     __syncwarp();
                     ok = cwait(&s.ys_go, 0, abort, lim);
                     if (ok) {
                         tc_fence_after();
-                        if (lane == 0) issue_ys(0);
+                        if (elect_one()) issue_ys(0);
                         __syncwarp();
                     }
                 }
@@ -773,8 +775,8 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                 ok = cwait(&s.pm_ready, c & 1, abort, lim) && cwait(&s.full_x[c & 1], (c >> 1) & 1, abort, lim);
                 if (!ok) break;
                 tc_fence_after();
-                const int steps = ((s.desc[c & 1].y & kChunkRows) + 15) >> 4;
-                if (lane == 0) {
+                const int steps = (int)uniform(((s.desc[c & 1].y & kChunkRows) + 15) >> 4);
+                if (elect_one()) {
                     const uint64_t dx = (c & 1) ? dX1 : dX0;
                     if (steps == 8) {
 #pragma unroll 1
@@ -795,7 +797,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                 ok = cwait(&s.xw_ready, c & 1, abort, lim);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint64_t dbt = (c & 1) ? dBt1 : dBt0, dxw = (c & 1) ? dXw1 : dXw0;
                     if (steps == 8) {
 #pragma unroll 2
@@ -816,11 +818,12 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                     ok = cwait(&s.ys_go, (c + 1) & 1, abort, lim);
                     if (!ok) break;
                     tc_fence_after();
-                    if (lane == 0) issue_ys(c + 1);
+                    if (elect_one()) issue_ys(c + 1);
                     __syncwarp();
                 }
             }
-            if (lane == 0) {
+            __syncwarp();
+            if (elect_one()) {
                 if (live && !ok) raise_timeout(p, abort);
                 // every MMA of this warp complete before TMEM is freed
                 mma_commit(&s.fin);
@@ -948,7 +951,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                     ok = cwait(&s.pmw, 0, abort, lim) && cwait(&s.full_bc[1], 0, abort, lim);
                     if (ok) {
                         tc_fence_after();
-                        if (lane == 0) issue_g(1);
+                        if (elect_one()) issue_g(1);
                         __syncwarp();
                     }
                 }
@@ -966,13 +969,17 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                      cwait(&s.ymma_done, (c + 1) & 1, abort, lim);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) issue_g(c + 2);
+                if (elect_one()) issue_g(c + 2);
                 __syncwarp();
             }
-            if (lane == 0) {
+            __syncwarp();
+            if (elect_one()) {
                 if (live && !ok) raise_timeout(p, abort);
                 mma_commit(&s.fin2);
                 wait_loop(&s.fin2, 0, nullptr, 100000000ull);
+            }
+            __syncwarp();
+            if (lane == 0) {
                 if (*abort) {
                     for (int i = bc_issued > 2 ? bc_issued - 2 : 0; i < bc_issued; ++i)
                         wait_loop(&s.full_bc[i & 1], (i >> 1) & 1, nullptr, 100000000ull);
