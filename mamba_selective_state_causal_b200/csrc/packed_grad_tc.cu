@@ -420,17 +420,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
 // =============================================================== gradients
 // The items (chunk, head), chunk after chunk, are dealt out in equal runs of blocks of heads, one CTA per SM: a CTA meets
 // few chunks, loads C and B of a group once, and keeps dB and dC in TMEM through a block.
-// Per item i (tensor pipe | 16 compute warps):
-//   GX = dy x^T                                     |
-//   dxI = B Gam^T, YI = C h^T                       |
-//   dB += Gam (w x), dC += h (e^{cs} dy)            | (S) w x and e^{cs} dy, each in two parts; (F) <Gam, h>
-//   dx = (E CB)^T dy, dB += C^T M, dC += B^T M^T    | (M) E o CB and M in two parts; the row and column sums of M o CB
-//                                                   | (A) x_j . dxI_j and dy_t . YI_t; (S) of item i + 1; (D) dx
+// Per item, on the tensor pipe: GX = dy x^T;  dxI = B Gam^T, YI = C h^T;  dB += Gam (w x), dC += h (e^{cs} dy);
+// dx = (E CB)^T dy, dB += C^T M, dC += B^T M^T.  Warps 0..7: (M) E o CB and M in two parts, the row and column sums of
+// M o CB; (A) x_j . dxI_j and dy_t . YI_t; (D) dx.  Warps 8..15, ahead of them: (S) w x and e^{cs} dy in two parts;
+// (F) <Gam, h>.  (All 16 warps on one step after the other took 4.2 us per item, each step waiting for its own
+// latencies; so HERE.)
 // M = 64 accumulators use 16 of each 32 TMEM lanes: GX keeps columns 0..31 in the lower and 32..63 in the upper
 // 16, dxI and YI share their columns that way.  The sums that make ddt are finished by a warp of their own.
 // TMEM: dB 0..63, dC 64..127 (lanes n, columns rows), dxI | YI 128..191 and 192..255, GX 256..287 and 288..319,
 // dx 320..383, CB 384..415.
-constexpr int kGradWarps = 16, kGradThreads = 32 * (kGradWarps + 4);
+constexpr int kMathWarps = 8, kWeighWarps = 8, kGradWarps = kMathWarps + kWeighWarps, kGradThreads = 32 * (kGradWarps + 4);
 constexpr uint32_t kColB = 0, kColC = 64, kColI = 128, kColG = 256, kColDx = 320, kColCB = 384;
 constexpr uint32_t kUpper = 16u << 16;    // lanes 16..31 of each 32
 
@@ -450,7 +449,7 @@ struct SmemGrad {
 static_assert(sizeof(SmemGrad) <= 232448, "the gradient kernel's shared memory");
 
 // partial sums of an item on their way to the warp that finishes them (in global memory: shared memory is full)
-constexpr int kSumRow = 0, kSumCol = 256, kSumBe = 512, kSumAl = 768, kSumDiag = 1024, kSumD = 1088, kSumF = 1152, kSumFloats = 1184;
+constexpr int kSumCol = 0, kSumRow = 256, kSumBe = 384, kSumAl = 512, kSumDiag = 640, kSumD = 704, kSumF = 768, kSumFloats = 800;
 
 // How the heads of the chunks are dealt out: in blocks of S heads of a group, nb blocks to a group.  The sums over the
 // heads of a block are formed in TMEM, where each addition is cut off instead of rounded, so a block has at most
@@ -459,21 +458,21 @@ constexpr int kSumRow = 0, kSumCol = 256, kSumBe = 512, kSumAl = 768, kSumDiag =
 constexpr int kMaxBlock = 8;
 struct GradSplit {
     int S, nb;
-    int64_t blocks, per;        // blocks in all, and per CTA
+    int blocks, per;            // blocks in all (no more than chunks x heads), and per CTA
     __device__ __forceinline__ GradSplit(const PackedGradParams &p, int nch, int ctas)
     {
         const int R = p.H / p.G;
         const int64_t fair = (int64_t)nch * p.H / ctas;
         S = min(max(1, (int)min(fair, (int64_t)kMaxBlock)), R);
         nb = (R + S - 1) / S;
-        blocks = (int64_t)nch * p.G * nb;
+        blocks = nch * p.G * nb;
         per = (blocks + ctas - 1) / ctas;
     }
 };
 
 // The items of a CTA, in order, without those of empty sequences
 struct Items {
-    int64_t v, end;             // its blocks of heads
+    int v, end;                 // its blocks of heads
     int S, nb, G, R, it;
     int4 d;
     int chunk, h, h1;
@@ -485,11 +484,11 @@ struct Items {
     {
         valid = false;
         while (v < end) {
-            const int c = (int)(v / (G * nb)), rem = (int)(v - (int64_t)c * (G * nb)), blk = rem % nb;
+            const int c = v / (G * nb), rem = v - c * (G * nb), blk = rem % nb;
             if (fresh || rem == 0) {
                 d = __ldg(tab + c);
                 chunk = c;
-                if ((d.y & kChunkRows) == 0) { v = (int64_t)(c + 1) * (G * nb); continue; }
+                if ((d.y & kChunkRows) == 0) { v = (c + 1) * (G * nb); continue; }
             }
             const int g = rem / nb;
             h = g * R + blk * S;
@@ -503,7 +502,7 @@ struct Items {
         }
     }
     __device__ __forceinline__ Items(const PackedGradParams &p, const GradSplit &sp)
-        : v(blockIdx.x * sp.per), end(min(v + sp.per, sp.blocks)), S(sp.S), nb(sp.nb), G(p.G), R(p.H / p.G), it(0), d{}, chunk(0), h(0), h1(0), first(false), last(false), enter(false), leave(false), tab(p.plan.chunk64)
+        : v((int)min((int64_t)blockIdx.x * sp.per, (int64_t)sp.blocks)), end(min(v + sp.per, sp.blocks)), S(sp.S), nb(sp.nb), G(p.G), R(p.H / p.G), it(0), d{}, chunk(0), h(0), h1(0), first(false), last(false), enter(false), leave(false), tab(p.plan.chunk64)
     {
         settle(true);
     }
@@ -538,10 +537,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
             mbar_init(&s.cs_ready[i], 1); mbar_init(&s.gx_done[i], 1); mbar_init(&s.in_done[i], 1);
             mbar_init(&s.sums_ready[i], kGradWarps); mbar_init(&s.sums_free[i], 1);
         }
-        for (int i = 0; i < 3; ++i) { mbar_init(&s.st_full[i], 1); mbar_init(&s.st_empty[i], 1 + kGradWarps); }
-        mbar_init(&s.cbt_done, 1); mbar_init(&s.sc_ready, kGradWarps); mbar_init(&s.inter_done, 1);
-        mbar_init(&s.mk_ready, kGradWarps); mbar_init(&s.dx_done, 1); mbar_init(&s.intra_done, 1);
-        mbar_init(&s.acc_free, kGradWarps); mbar_init(&s.fin, 1);
+        for (int i = 0; i < 3; ++i) { mbar_init(&s.st_full[i], 1); mbar_init(&s.st_empty[i], 1 + kWeighWarps); }
+        mbar_init(&s.cbt_done, 1); mbar_init(&s.sc_ready, kWeighWarps); mbar_init(&s.inter_done, 1);
+        mbar_init(&s.mk_ready, kMathWarps); mbar_init(&s.dx_done, 1); mbar_init(&s.intra_done, 1);
+        mbar_init(&s.acc_free, kMathWarps); mbar_init(&s.fin, 1);
         s.abort = 0;
         fence_mbar_init();
     }
@@ -553,49 +552,231 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
     volatile int *abort = &s.abort;
     bool ok = true;
 
-    if (warp < kGradWarps) {
+    if (warp < kMathWarps) {
+        // ================================================= (M), (A), (D) of each item, dB and dC of each block
         const int q = warp & 3, e = warp >> 2, half = lane >> 4;
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
         const int mrow = 16 * q + (lane & 15);         // row of an M = 64 accumulator
         float *sums = p.ws_sums + (int64_t)blockIdx.x * 2 * kSumFloats;
-        float cbv[8];                                  // C_t . B_j of row mrow, columns 32 half + 8 e ..
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cbv[i] = 0.0f;
         uint32_t unit = 0;
-
-        // (S) the weighted operands of item `it`
-        auto weigh = [&](int it) -> bool {
-            const int b = it & 1;
+        for (; ok && m.valid; m.next()) {
+            const int it = m.it, b = it & 1;
             const uint32_t ph = (uint32_t)(it >> 1) & 1;
-            if (!cwait(&s.xd_full[b], ph, abort, lim) || !cwait(&s.cs_ready[b], ph, abort, lim)) return false;
-            if (it > 0 && !cwait(&s.inter_done, (uint32_t)(it - 1) & 1, abort, lim)) return false;
-            const int r = tid >> 3, c = tid & 7;
-            const uint32_t o = swz(r, c);
-            const uint4 x = lds128(s.xd[b] + o), dy = lds128(s.xd[b] + kTile + o);
-            uint4 hi, lo;
-            split_scaled8(x, s.dt[b][r] * ex2(s.suf[b][r]), hi, lo);
-            sts128(s.sc + o, hi);
-            sts128(s.sc + kTile + o, lo);
-            split_scaled8(dy, ex2(s.cs[b][r]), hi, lo);
-            sts128(s.sc + 2 * kTile + o, hi);
-            sts128(s.sc + 3 * kTile + o, lo);
+            float *sm = sums + b * kSumFloats;
+            // ---- (M)
+            if (m.enter && !(ok = cwait(&s.cbt_done, unit++ & 1, abort, lim))) break;
+            ok = cwait(&s.cs_ready[b], ph, abort, lim) && cwait(&s.gx_done[b], ph, abort, lim);
+            if (ok && it > 0) ok = cwait(&s.intra_done, (uint32_t)(it - 1) & 1, abort, lim);
+            if (ok && it > 1) ok = cwait(&s.sums_free[b], (uint32_t)((it >> 1) - 1) & 1, abort, lim);
+            if (!ok) break;
+            tc_fence_after();
+            {
+                const float ct = s.cs[b][mrow];
+                float row = 0.0f, k0 = 0.0f, k1 = 0.0f;
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u) {
+                    const int j0 = 32 * half + 16 * e + 8 * u;
+                    uint32_t gx[8], cb[8];
+                    tmem_ld8(tm + lanes + kColG + 32 * b + 16 * e + 8 * u, gx);
+                    tmem_ld8(tm + lanes + kColCB + 16 * e + 8 * u, cb);
+                    float cj[8], dj[8];
+                    *reinterpret_cast<float4 *>(cj) = *reinterpret_cast<const float4 *>(&s.cs[b][j0]);
+                    *reinterpret_cast<float4 *>(cj + 4) = *reinterpret_cast<const float4 *>(&s.cs[b][j0 + 4]);
+                    *reinterpret_cast<float4 *>(dj) = *reinterpret_cast<const float4 *>(&s.dt[b][j0]);
+                    *reinterpret_cast<float4 *>(dj + 4) = *reinterpret_cast<const float4 *>(&s.dt[b][j0 + 4]);
+                    tmem_wait_ld8(gx);
+                    tmem_wait_ld8(cb);
+                    float kp[8], ec[8], mm[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float E = j0 + i <= mrow ? ex2(ct - cj[i]) : 0.0f, cbi = __uint_as_float(cb[i]);
+                        const float eg = E * __uint_as_float(gx[i]);
+                        ec[i] = E * cbi;
+                        mm[i] = eg * dj[i];
+                        kp[i] = eg * cbi;
+                        if (j0 + i < mrow) row = fmaf(mm[i], cbi, row);
+                        if (j0 + i == mrow) {
+                            sm[kSumDiag + mrow] = kp[i];
+                            sm[kSumD + mrow] = __uint_as_float(gx[i]);
+                        }
+                    }
+                    uint32_t hi[4], lo[4];
+                    const uint32_t o = swz(mrow, (j0 >> 3));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) split2(make_float2(ec[2 * i], ec[2 * i + 1]), hi[i], lo[i]);
+                    sts128(s.mk + o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                    sts128(s.mk + kTile + o, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) split2(make_float2(mm[2 * i], mm[2 * i + 1]), hi[i], lo[i]);
+                    sts128(s.mk + 2 * kTile + o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                    sts128(s.mk + 3 * kTile + o, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    // column sums over the 16 rows: each halving step keeps half of the columns and adds the partner's copy
+                    // of them
+                    float k4[4], k2[2];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool up = lane & 8;
+                        const float keep = up ? kp[i + 4] : kp[i], give = up ? kp[i] : kp[i + 4];
+                        k4[i] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const bool up = lane & 4;
+                        const float keep = up ? k4[i + 2] : k4[i], give = up ? k4[i] : k4[i + 2];
+                        k2[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
+                    }
+                    const bool up = lane & 2;
+                    const float keep = up ? k2[1] : k2[0], give = up ? k2[0] : k2[1];
+                    k0 = k1;
+                    k1 = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.mk_ready);
+                // (lane bits 3, 2, 1 name the column of the eight)
+                k0 += __shfl_xor_sync(0xffffffffu, k0, 1);
+                k1 += __shfl_xor_sync(0xffffffffu, k1, 1);
+                sm[kSumCol + 64 * q + 32 * half + 16 * e + 8 * (lane & 1) + ((lane >> 1) & 1) + ((lane >> 2) & 1) * 2 + ((lane >> 3) & 1) * 4] =
+                    lane & 1 ? k1 : k0;
+                row += __shfl_xor_sync(0xffffffffu, row, 16);
+                if (lane < 16) sm[kSumRow + 64 * e + mrow] = row;
+            }
+            // ---- (A)
+            if (!(ok = cwait(&s.in_done[b], ph, abort, lim))) break;
+            tc_fence_after();
+            {
+                float2 a = make_float2(0.0f, 0.0f);
+                const uint8_t *v = s.xd[b] + half * kTile;
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t r[16];
+                    tmem_ld16(tm + lanes + kColI + 64 * b + 32 * e + 16 * u, r);
+                    const uint4 v0 = lds128(v + swz(mrow, 4 * e + 2 * u)), v1 = lds128(v + swz(mrow, 4 * e + 2 * u + 1));
+                    const uint32_t vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                    tmem_wait_ld(r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        a = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), unpack2(vv[i]), a);
+                }
+                sm[(half ? kSumAl : kSumBe) + 64 * e + mrow] = a.x + a.y;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.sums_ready[b]);
+            // ---- (D)
+            if (!(ok = cwait(&s.dx_done, (uint32_t)it & 1, abort, lim))) break;
+            tc_fence_after();
+            {
+                const float Dh = p.D ? __ldg(p.D + m.h) : 0.0f;
+                const int rows = m.d.y & kChunkRows;
+                float *dst = p.dx + (int64_t)m.d.x * ((int64_t)p.H * kP) + (int64_t)m.h * kP + 32 * e + 2 * (lane & 3);
+                float dtj[2], ew[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int j = 16 * q + (lane >> 2) + 8 * u;
+                    dtj[u] = s.dt[b][j];
+                    ew[u] = ex2(s.suf[b][j]);
+                }
+#pragma unroll 1
+                for (int w = 0; w < 2; ++w) {
+                    uint32_t a[8], in[8];
+                    tmem_ld_rows16(tm + lanes + kColDx + 32 * e + 16 * w, a);
+                    tmem_ld_rows16(tm + lanes + kColI + 64 * b + 32 * e + 16 * w, in);
+                    tmem_wait_ld8(a);
+                    tmem_wait_ld8(in);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int j = 16 * q + (lane >> 2) + 8 * u;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float2 dy = unpack2(*reinterpret_cast<const uint32_t *>(s.xd[b] + kTile + swz(j, 4 * e + 2 * w + k) + 4 * (lane & 3)));
+                            const float ax = __uint_as_float(a[4 * k + 2 * u]), ay = __uint_as_float(a[4 * k + 2 * u + 1]);
+                            const float ix = __uint_as_float(in[4 * k + 2 * u]), iy = __uint_as_float(in[4 * k + 2 * u + 1]);
+                            const float2 o = make_float2(fmaf(dtj[u], fmaf(ew[u], ix, ax), Dh * dy.x), fmaf(dtj[u], fmaf(ew[u], iy, ay), Dh * dy.y));
+                            if (j < rows) *reinterpret_cast<float2 *>(dst + (int64_t)j * ((int64_t)p.H * kP) + 16 * w + 8 * k) = o;
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.xd_empty[b]);
+            // ---- the block's dB and dC
+            if (m.last) {
+                if (!(ok = cwait(&s.intra_done, (uint32_t)it & 1, abort, lim))) break;
+                tc_fence_after();
+                const int nn = 32 * q + lane, g = m.h / R, rows = m.d.y & kChunkRows;
+                float *dB, *dC;
+                int64_t rs;
+                if (m.nb == 1) {
+                    dB = p.dB + ((int64_t)m.d.x * p.G + g) * kN;
+                    dC = p.dC + ((int64_t)m.d.x * p.G + g) * kN;
+                    rs = (int64_t)p.G * kN;
+                } else {
+                    dB = p.ws_part + (int64_t)m.v * (2 * kQ * kN);
+                    dC = dB + kQ * kN;
+                    rs = kN;
+                }
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u) {
+                    const int t0 = 32 * e + 16 * u;
+                    uint32_t ab[16], ac[16];
+                    tmem_ld16(tm + lanes + kColB + t0, ab);
+                    tmem_ld16(tm + lanes + kColC + t0, ac);
+                    tmem_wait_ld(ab, ac);
+                    if (u == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s.acc_free);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (t0 + i < rows) {
+                            dB[(t0 + i) * rs + nn] = __uint_as_float(ab[i]);
+                            dC[(t0 + i) * rs + nn] = __uint_as_float(ac[i]);
+                        }
+                }
+            }
+        }
+        if (!ok && lane == 0) raise_timeout(p, abort);
+        __syncwarp();
+    } else if (warp < kGradWarps) {
+        // ================================================= (S), (F) of each item
+        const int t = tid - 32 * kMathWarps;
+        float *sums = p.ws_sums + (int64_t)blockIdx.x * 2 * kSumFloats;
+        for (; ok && m.valid; m.next()) {
+            const int it = m.it, b = it & 1;
+            const uint32_t ph = (uint32_t)(it >> 1) & 1;
+            // ---- (S)
+            if (!(ok = cwait(&s.xd_full[b], ph, abort, lim) && cwait(&s.cs_ready[b], ph, abort, lim))) break;
+            if (it > 0 && !(ok = cwait(&s.inter_done, (uint32_t)(it - 1) & 1, abort, lim))) break;
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u) {
+                const int r = (t >> 3) + 32 * u, c = t & 7;
+                const uint32_t o = swz(r, c);
+                const uint4 x = lds128(s.xd[b] + o), dy = lds128(s.xd[b] + kTile + o);
+                uint4 hi, lo;
+                split_scaled8(x, s.dt[b][r] * ex2(s.suf[b][r]), hi, lo);
+                sts128(s.sc + o, hi);
+                sts128(s.sc + kTile + o, lo);
+                split_scaled8(dy, ex2(s.cs[b][r]), hi, lo);
+                sts128(s.sc + 2 * kTile + o, hi);
+                sts128(s.sc + 3 * kTile + o, lo);
+            }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.sc_ready);
-            return true;
-        };
-        // (F) <Gam, h> of item `it`
-        auto inner = [&](int it) -> bool {
+            if (lane == 0) {
+                mbar_arrive(&s.sc_ready);
+                mbar_arrive(&s.xd_empty[b]);
+            }
+            // ---- (F)
             const int ug = 2 * it, uh = 2 * it + 1;
-            if (!cwait(&s.st_full[ug % 3], (uint32_t)(ug / 3) & 1, abort, lim) ||
-                !cwait(&s.st_full[uh % 3], (uint32_t)(uh / 3) & 1, abort, lim))
-                return false;
-            if (it >= 2 && !cwait(&s.sums_free[it & 1], (uint32_t)((it >> 1) - 1) & 1, abort, lim)) return false;
+            if (!(ok = cwait(&s.st_full[ug % 3], (uint32_t)(ug / 3) & 1, abort, lim) && cwait(&s.st_full[uh % 3], (uint32_t)(uh / 3) & 1, abort, lim))) break;
             const uint8_t *G = s.st[ug % 3], *h = s.st[uh % 3];
             float2 a = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t o = 16 * (tid + 512 * k);
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t o = 16 * (t + 256 * k);
                 const uint4 gh = lds128(G + o), gl = lds128(G + kPiece + o), hh = lds128(h + o), hl = lds128(h + kPiece + o);
                 const uint32_t gx[4] = {gh.x, gh.y, gh.z, gh.w}, gy[4] = {gl.x, gl.y, gl.z, gl.w};
                 const uint32_t hx[4] = {hh.x, hh.y, hh.z, hh.w}, hy[4] = {hl.x, hl.y, hl.z, hl.w};
@@ -607,187 +788,23 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
                     a = fma2(unpack2(gy[i]), h1, a);
                 }
             }
-            float v = a.x + a.y;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            __syncwarp();
             if (lane == 0) {
-                sums[(it & 1) * kSumFloats + kSumF + warp] = v;
                 mbar_arrive(&s.st_empty[ug % 3]);
                 mbar_arrive(&s.st_empty[uh % 3]);
             }
-            __syncwarp();
-            return true;
-        };
-
-        ok = weigh(0) && inner(0);
-        while (ok && m.valid) {
-            const int it = m.it, b = it & 1;
-            const uint32_t ph = (uint32_t)(it >> 1) & 1;
-            float *sm = sums + b * kSumFloats;
-            // ---- (M)
-            if (m.enter) {
-                if (!(ok = cwait(&s.cbt_done, unit & 1, abort, lim))) break;
-                ++unit;
-                tc_fence_after();
-                uint32_t r[8];
-                tmem_ld8(tm + lanes + kColCB + 8 * e, r);
-                tmem_wait_ld8(r);
+            float v = a.x + a.y;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) cbv[i] = __uint_as_float(r[i]);
-            }
-            ok = cwait(&s.gx_done[b], ph, abort, lim);
-            if (ok && it > 0) ok = cwait(&s.intra_done, (uint32_t)(it - 1) & 1, abort, lim);
-            if (!ok) break;
-            tc_fence_after();
-            {
-                uint32_t gx[8];
-                tmem_ld8(tm + lanes + kColG + 32 * b + 8 * e, gx);
-                const int j0 = 32 * half + 8 * e;
-                const float ct = s.cs[b][mrow];
-                float cj[8], dj[8];
-                *reinterpret_cast<float4 *>(cj) = *reinterpret_cast<const float4 *>(&s.cs[b][j0]);
-                *reinterpret_cast<float4 *>(cj + 4) = *reinterpret_cast<const float4 *>(&s.cs[b][j0 + 4]);
-                *reinterpret_cast<float4 *>(dj) = *reinterpret_cast<const float4 *>(&s.dt[b][j0]);
-                *reinterpret_cast<float4 *>(dj + 4) = *reinterpret_cast<const float4 *>(&s.dt[b][j0 + 4]);
-                tmem_wait_ld8(gx);
-                float kp[8], ec[8], mm[8], row = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float E = j0 + i <= mrow ? ex2(ct - cj[i]) : 0.0f;
-                    const float eg = E * __uint_as_float(gx[i]);
-                    ec[i] = E * cbv[i];
-                    mm[i] = eg * dj[i];
-                    kp[i] = eg * cbv[i];
-                    if (j0 + i < mrow) row = fmaf(mm[i], cbv[i], row);
-                    if (j0 + i == mrow) {
-                        sm[kSumDiag + mrow] = kp[i];
-                        sm[kSumD + mrow] = __uint_as_float(gx[i]);
-                    }
-                }
-                uint32_t hi[4], lo[4];
-                const uint32_t o = swz(mrow, (j0 >> 3));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) split2(make_float2(ec[2 * i], ec[2 * i + 1]), hi[i], lo[i]);
-                sts128(s.mk + o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                sts128(s.mk + kTile + o, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) split2(make_float2(mm[2 * i], mm[2 * i + 1]), hi[i], lo[i]);
-                sts128(s.mk + 2 * kTile + o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                sts128(s.mk + 3 * kTile + o, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.mk_ready);
-                // row sums over the 8 columns, joined with the other half's; column sums over the 16 rows: each halving
-                // step keeps half of the columns and adds the partner's copy of them
-                row += __shfl_xor_sync(0xffffffffu, row, 16);
-                if (lane < 16) sm[kSumRow + 64 * e + mrow] = row;
-                float k4[4], k2[2], k1;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool up = lane & 8;
-                    const float keep = up ? kp[i + 4] : kp[i], give = up ? kp[i] : kp[i + 4];
-                    k4[i] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool up = lane & 4;
-                    const float keep = up ? k4[i + 2] : k4[i], give = up ? k4[i] : k4[i + 2];
-                    k2[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
-                }
-                {
-                    const bool up = lane & 2;
-                    const float keep = up ? k2[1] : k2[0], give = up ? k2[0] : k2[1];
-                    k1 = keep + __shfl_xor_sync(0xffffffffu, give, 2);
-                }
-                k1 += __shfl_xor_sync(0xffffffffu, k1, 1);
-                if (!(lane & 1)) sm[kSumCol + 64 * q + j0 + ((lane >> 1) & 1) + ((lane >> 2) & 1) * 2 + ((lane >> 3) & 1) * 4] = k1;
-            }
-            // ---- (A)
-            if (!(ok = cwait(&s.in_done[b], ph, abort, lim))) break;
-            tc_fence_after();
-            {
-                uint32_t r[16];
-                tmem_ld16(tm + lanes + kColI + 64 * b + 16 * e, r);
-                const uint8_t *v = s.xd[b] + half * kTile;
-                const uint4 v0 = lds128(v + swz(mrow, 2 * e)), v1 = lds128(v + swz(mrow, 2 * e + 1));
-                const uint32_t vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-                tmem_wait_ld(r);
-                float2 a = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    a = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), unpack2(vv[i]), a);
-                sm[(half ? kSumAl : kSumBe) + 64 * e + mrow] = a.x + a.y;
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (it > 1 && !(ok = cwait(&s.sums_free[b], (uint32_t)((it >> 1) - 1) & 1, abort, lim))) break;
+            if (lane == 0) {
+                sums[b * kSumFloats + kSumF + warp - kMathWarps] = v;
+                mbar_arrive(&s.sums_ready[b]);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.sums_ready[b]);
-            const Items cur = m;
-            m.next();
-            // ---- (S) of the next item
-            if (m.valid && !(ok = weigh(m.it))) break;
-            // ---- (D)
-            if (!(ok = cwait(&s.dx_done, (uint32_t)it & 1, abort, lim))) break;
-            tc_fence_after();
-            {
-                uint32_t a[8], in[8];
-                tmem_ld_rows16(tm + lanes + kColDx + 16 * e, a);
-                tmem_ld_rows16(tm + lanes + kColI + 64 * b + 16 * e, in);
-                const float Dh = p.D ? __ldg(p.D + cur.h) : 0.0f;
-                const int rows = cur.d.y & kChunkRows;
-                tmem_wait_ld8(a);
-                tmem_wait_ld8(in);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int j = 16 * q + (lane >> 2) + 8 * u;
-                    const float dtj = s.dt[b][j], ew = ex2(s.suf[b][j]);
-                    float *dst = p.dx + ((int64_t)cur.d.x + j) * ((int64_t)p.H * kP) + (int64_t)cur.h * kP + 16 * e + 2 * (lane & 3);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float2 dy = unpack2(*reinterpret_cast<const uint32_t *>(s.xd[b] + kTile + swz(j, 2 * e + k) + 4 * (lane & 3)));
-                        const float ax = __uint_as_float(a[4 * k + 2 * u]), ay = __uint_as_float(a[4 * k + 2 * u + 1]);
-                        const float ix = __uint_as_float(in[4 * k + 2 * u]), iy = __uint_as_float(in[4 * k + 2 * u + 1]);
-                        const float2 o = make_float2(fmaf(dtj, fmaf(ew, ix, ax), Dh * dy.x), fmaf(dtj, fmaf(ew, iy, ay), Dh * dy.y));
-                        if (j < rows) *reinterpret_cast<float2 *>(dst + 8 * k) = o;
-                    }
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.xd_empty[b]);
-            // ---- the unit's dB and dC
-            if (cur.last) {
-                if (!(ok = cwait(&s.intra_done, (uint32_t)it & 1, abort, lim))) break;
-                tc_fence_after();
-                const int nn = 32 * q + lane, g = cur.h / R, rows = cur.d.y & kChunkRows;
-                float *dB, *dC;
-                int64_t rs;
-                if (cur.nb == 1) {
-                    dB = p.dB + ((int64_t)cur.d.x * p.G + g) * kN;
-                    dC = p.dC + ((int64_t)cur.d.x * p.G + g) * kN;
-                    rs = (int64_t)p.G * kN;
-                } else {
-                    dB = p.ws_part + cur.v * (2 * kQ * kN);
-                    dC = dB + kQ * kN;
-                    rs = kN;
-                }
-                uint32_t ab[16], ac[16];
-                tmem_ld16(tm + lanes + kColB + 16 * e, ab);
-                tmem_ld16(tm + lanes + kColC + 16 * e, ac);
-                tmem_wait_ld(ab, ac);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.acc_free);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (16 * e + i < rows) {
-                        dB[(16 * e + i) * rs + nn] = __uint_as_float(ab[i]);
-                        dC[(16 * e + i) * rs + nn] = __uint_as_float(ac[i]);
-                    }
-            }
-            // ---- (F) of the next item
-            if (m.valid) ok = inner(m.it);
         }
         if (!ok && lane == 0) raise_timeout(p, abort);
+        __syncwarp();
     } else if (warp == kGradWarps) {
         // ================================================= issuing warp (the whole warp waits, one lane issues)
         const uint32_t cC = smem_u32(s.cb), cB = cC + 2 * kTile;
@@ -804,7 +821,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
             if (elect_one()) {
                 const uint32_t x = smem_u32(s.xd[b]);
                 const uint64_t dx = smem_desc(x, 16, 1024), dd = smem_desc(x + kTile, 16, 1024);
-#pragma unroll
+#pragma unroll 1
                 for (int hf = 0; hf < 2; ++hf)
                     mma_steps<4>(tu + kColG + 32 * b + hf * kUpper, dd, dx + (uint64_t)(hf * (4096 >> 4)), 2, 2, id_g, false);
                 mma_commit(&s.gx_done[b]);
@@ -819,7 +836,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
                 ++unit;
                 tc_fence_after();
                 if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
                         const int hf = k >> 1;
                         const uint64_t box = (uint64_t)((k & 1) * (kTile >> 4));
@@ -836,7 +853,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
                 if (elect_one()) {
                     const uint64_t ds = smem_desc(w ? h : G, kTile, 1024);
                     const uint64_t da = w ? dCk : dBk;
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < 4; ++k)      // both parts, both halves of n
                         mma_steps<4>(tu + kColI + 64 * b + w * kUpper, da + (uint64_t)((k & 1) * (kTile >> 4)),
                                   ds + (uint64_t)((k >> 1) * (kPiece >> 4) + (k & 1) * 512), 2, 128, id_i, k > 0);
@@ -851,10 +868,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
             if (elect_one()) {
                 // dB^T[n][j] += Gam^T[n][p] (w x)[j][p], dC^T likewise: M = n rows of the image, K = p
                 const uint32_t sc = smem_u32(s.sc);
-#pragma unroll
+#pragma unroll 1
                 for (int w = 0; w < 2; ++w) {
                     const uint64_t da = smem_desc(w ? h : G, 16, 1024), db = smem_desc(sc + (uint32_t)w * 2 * kTile, 16, 1024);
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < 3; ++part)
                         mma_steps<4>(tu + (w ? kColC : kColB), da + (uint64_t)(part == 2 ? kPiece >> 4 : 0), db + (uint64_t)(part == 1 ? kTile >> 4 : 0), 2, 2,
                                   id_kk, acc || part > 0);
@@ -872,7 +889,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
         while (ok && m.valid) {
             const int it = m.it;
             nx.next();
-            if (nx.valid && !(ok = gx(nx.it))) break;
             if (!(ok = cwait(&s.mk_ready, (uint32_t)it & 1, abort, lim))) break;
             tc_fence_after();
             const uint32_t bi = uniform(it & 1);
@@ -881,18 +897,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
                 const uint64_t de = smem_desc(mk, kTile, 1024), dm = smem_desc(mk + 2 * kTile, kTile, 1024), dmk = smem_desc(mk + 2 * kTile, 16, 1024);
                 const uint64_t dd = smem_desc(smem_u32(s.xd[bi]) + kTile, kTile, 1024);
                 const uint64_t lo = kTile >> 4;
-                mma_steps<4>(tu + kColDx, de, dd, 128, 128, id_x, false);
-                mma_steps<4>(tu + kColDx, de + lo, dd, 128, 128, id_x, true);
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part) mma_steps<4>(tu + kColDx, de + part * lo, dd, 128, 128, id_x, part);
                 mma_commit(&s.dx_done);
-                mma_steps<4>(tu + kColB, dCm, dm, 128, 128, id_mm, true);
-                mma_steps<4>(tu + kColB, dCm, dm + lo, 128, 128, id_mm, true);
-                mma_steps<4>(tu + kColC, dBm, dmk, 128, 2, id_mk, true);
-                mma_steps<4>(tu + kColC, dBm, dmk + lo, 128, 2, id_mk, true);
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part) {
+                    mma_steps<4>(tu + kColB, dCm, dm + part * lo, 128, 128, id_mm, true);
+                    mma_steps<4>(tu + kColC, dBm, dmk + part * lo, 128, 2, id_mk, true);
+                }
                 mma_commit(&s.intra_done);
                 if (m.leave) mma_commit(&s.cb_empty);
             }
             __syncwarp();
-            if (nx.valid && !(ok = from_states(nx.it, nx.first, nx.enter))) break;
+            if (nx.valid && !(ok = gx(nx.it) && from_states(nx.it, nx.first, nx.enter))) break;
             m = nx;
         }
         __syncwarp();
@@ -1005,13 +1022,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
             float2 row = make_float2(0.0f, 0.0f), col = row, be = row, al = row;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 r = reinterpret_cast<const float2 *>(sm + kSumRow + 64 * k)[lane], c = reinterpret_cast<const float2 *>(sm + kSumCol + 64 * k)[lane];
-                const float2 u = reinterpret_cast<const float2 *>(sm + kSumBe + 64 * k)[lane], a = reinterpret_cast<const float2 *>(sm + kSumAl + 64 * k)[lane];
-                row.x += r.x; row.y += r.y; col.x += c.x; col.y += c.y;
-                be.x += u.x; be.y += u.y; al.x += a.x; al.y += a.y;
+                const float2 c = reinterpret_cast<const float2 *>(sm + kSumCol + 64 * k)[lane];
+                col.x += c.x; col.y += c.y;
+                if (k < 2) {
+                    const float2 r = reinterpret_cast<const float2 *>(sm + kSumRow + 64 * k)[lane];
+                    const float2 u = reinterpret_cast<const float2 *>(sm + kSumBe + 64 * k)[lane], a = reinterpret_cast<const float2 *>(sm + kSumAl + 64 * k)[lane];
+                    row.x += r.x; row.y += r.y;
+                    be.x += u.x; be.y += u.y; al.x += a.x; al.y += a.y;
+                }
             }
             const float2 dg = reinterpret_cast<const float2 *>(sm + kSumDiag)[lane], gd = reinterpret_cast<const float2 *>(sm + kSumD)[lane];
-            float F = lane < kGradWarps ? sm[kSumF + lane] : 0.0f;
+            float F = lane < kWeighWarps ? sm[kSumF + lane] : 0.0f;
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.sums_free[b]);
             // e^{lam-cs_j} x_j Gam B_j; and times dt_j
