@@ -425,8 +425,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
 // M o CB; (A) x_j . dxI_j and dy_t . YI_t; (D) dx.  Warps 8..15, ahead of them: (S) w x and e^{cs} dy in two parts;
 // (F) <Gam, h>.  (All 16 warps on one step after the other took 4.2 us per item, each step waiting for its own
 // latencies; so HERE.)
-// M = 64 accumulators use 16 of each 32 TMEM lanes: GX keeps columns 0..31 in the lower and 32..63 in the upper
-// 16, dxI and YI share their columns that way.  The sums that make ddt are finished by a warp of their own.
+// M = 64 accumulators use 16 of each 32 TMEM lanes: GX and CB keep columns 16 k .. 16 k + 7 in the lower and the eight
+// behind them in the upper 16, so that a warp's 16 rows and 16 columns lie on or off the triangle together; dxI and
+// YI share their columns that way.  The sums that make ddt are finished by a warp of their own.
 // TMEM: dB 0..63, dC 64..127 (lanes n, columns rows), dxI | YI 128..191 and 192..255, GX 256..287 and 288..319,
 // dx 320..383, CB 384..415.
 constexpr int kMathWarps = 8, kWeighWarps = 8, kGradWarps = kMathWarps + kWeighWarps, kGradThreads = 32 * (kGradWarps + 4);
@@ -477,7 +478,7 @@ struct Items {
     int4 d;
     int chunk, h, h1;
     bool valid, first, last;    // first and last of its block
-    bool enter, leave;          // first and last of its chunk and group in this CTA
+    bool enter, leave, tail;    // first and last of its chunk and group in this CTA; in the last block of them
     const int4 *tab;
 
     __device__ __forceinline__ void settle(bool fresh)
@@ -496,13 +497,14 @@ struct Items {
             first = true;
             enter = fresh || blk == 0;
             last = h + 1 == h1;
-            leave = last && (blk == nb - 1 || v + 1 == end);
+            tail = blk == nb - 1 || v + 1 == end;
+            leave = last && tail;
             valid = true;
             return;
         }
     }
     __device__ __forceinline__ Items(const PackedGradParams &p, const GradSplit &sp)
-        : v((int)min((int64_t)blockIdx.x * sp.per, (int64_t)sp.blocks)), end(min(v + sp.per, sp.blocks)), S(sp.S), nb(sp.nb), G(p.G), R(p.H / p.G), it(0), d{}, chunk(0), h(0), h1(0), first(false), last(false), enter(false), leave(false), tab(p.plan.chunk64)
+        : v((int)min((int64_t)blockIdx.x * sp.per, (int64_t)sp.blocks)), end(min(v + sp.per, sp.blocks)), S(sp.S), nb(sp.nb), G(p.G), R(p.H / p.G), it(0), d{}, chunk(0), h(0), h1(0), first(false), last(false), enter(false), leave(false), tail(false), tab(p.plan.chunk64)
     {
         settle(true);
     }
@@ -512,7 +514,7 @@ struct Items {
         if (++h < h1) {
             first = enter = false;
             last = h + 1 == h1;
-            leave = last && (h1 % R == 0 || v + 1 == end);
+            leave = last && tail;
         } else {
             ++v;
             settle(false);
@@ -545,6 +547,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
         fence_mbar_init();
     }
     if (warp == 0) { tmem_alloc(&s.tmem, 512); tmem_relinquish(); }
+    // what lies behind the triangle
+    for (int i = tid; i < (int)(4 * kTile / 16); i += kGradThreads) sts128(s.mk + 16 * i, make_uint4(0, 0, 0, 0));
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -572,13 +577,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
             tc_fence_after();
             {
                 const float ct = s.cs[b][mrow];
-                float row = 0.0f, k0 = 0.0f, k1 = 0.0f;
+                float row = 0.0f;
+                // columns 16 k .. of its rows 16 q ..: those behind the triangle stay zero
 #pragma unroll 1
-                for (int u = 0; u < 2; ++u) {
-                    const int j0 = 32 * half + 16 * e + 8 * u;
+                for (int k = e; k <= q; k += 2) {
+                    const int j0 = 16 * k + 8 * half;
                     uint32_t gx[8], cb[8];
-                    tmem_ld8(tm + lanes + kColG + 32 * b + 16 * e + 8 * u, gx);
-                    tmem_ld8(tm + lanes + kColCB + 16 * e + 8 * u, cb);
+                    tmem_ld8(tm + lanes + kColG + 32 * b + 8 * k, gx);
+                    tmem_ld8(tm + lanes + kColCB + 8 * k, cb);
                     float cj[8], dj[8];
                     *reinterpret_cast<float4 *>(cj) = *reinterpret_cast<const float4 *>(&s.cs[b][j0]);
                     *reinterpret_cast<float4 *>(cj + 4) = *reinterpret_cast<const float4 *>(&s.cs[b][j0 + 4]);
@@ -627,18 +633,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
                     }
                     const bool up = lane & 2;
                     const float keep = up ? k2[1] : k2[0], give = up ? k2[0] : k2[1];
-                    k0 = k1;
-                    k1 = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+                    float kc = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+                    kc += __shfl_xor_sync(0xffffffffu, kc, 1);
+                    // (lane bits 3, 2, 1 name the column of the eight)
+                    if (!(lane & 1)) sm[kSumCol + 64 * q + j0 + ((lane >> 1) & 1) + ((lane >> 2) & 1) * 2 + ((lane >> 3) & 1) * 4] = kc;
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.mk_ready);
-                // (lane bits 3, 2, 1 name the column of the eight)
-                k0 += __shfl_xor_sync(0xffffffffu, k0, 1);
-                k1 += __shfl_xor_sync(0xffffffffu, k1, 1);
-                sm[kSumCol + 64 * q + 32 * half + 16 * e + 8 * (lane & 1) + ((lane >> 1) & 1) + ((lane >> 2) & 1) * 2 + ((lane >> 3) & 1) * 4] =
-                    lane & 1 ? k1 : k0;
                 row += __shfl_xor_sync(0xffffffffu, row, 16);
                 if (lane < 16) sm[kSumRow + 64 * e + mrow] = row;
             }
@@ -809,6 +812,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
         // ================================================= issuing warp (the whole warp waits, one lane issues)
         const uint32_t cC = smem_u32(s.cb), cB = cC + 2 * kTile;
         const uint64_t dCk = smem_desc(cC, 16, 1024), dBk = smem_desc(cB, 16, 1024);          // rows x K = n
+        const uint64_t dBh = smem_desc(cB, 16, 2048);                                         // every other 8 rows of B
         const uint64_t dCm = smem_desc(cC, kTile, 1024), dBm = smem_desc(cB, kTile, 1024);    // M = n, K = rows
         const uint32_t id_g = idesc_bf16(64, 32, 0, 0), id_i = idesc_bf16(64, 64, 0, 1), id_x = idesc_bf16(64, 64, 1, 1);
         const uint32_t id_kk = idesc_bf16(128, 64, 0, 0), id_mm = idesc_bf16(128, 64, 1, 1), id_mk = idesc_bf16(128, 64, 1, 0);
@@ -820,10 +824,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
             tc_fence_after();
             if (elect_one()) {
                 const uint32_t x = smem_u32(s.xd[b]);
-                const uint64_t dx = smem_desc(x, 16, 1024), dd = smem_desc(x + kTile, 16, 1024);
+                const uint64_t dx = smem_desc(x, 16, 2048), dd = smem_desc(x + kTile, 16, 1024);     // (every other 8 rows of x)
 #pragma unroll 1
                 for (int hf = 0; hf < 2; ++hf)
-                    mma_steps<4>(tu + kColG + 32 * b + hf * kUpper, dd, dx + (uint64_t)(hf * (4096 >> 4)), 2, 2, id_g, false);
+                    mma_steps<4>(tu + kColG + 32 * b + hf * kUpper, dd, dx + (uint64_t)(hf * (1024 >> 4)), 2, 2, id_g, false);
                 mma_commit(&s.gx_done[b]);
             }
             __syncwarp();
@@ -840,7 +844,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
                     for (int k = 0; k < 4; ++k) {
                         const int hf = k >> 1;
                         const uint64_t box = (uint64_t)((k & 1) * (kTile >> 4));
-                        mma_steps<4>(tu + kColCB + hf * kUpper, dCk + box, dBk + box + (uint64_t)(hf * (4096 >> 4)), 2, 2, id_g, k & 1);
+                        mma_steps<4>(tu + kColCB + hf * kUpper, dCk + box, dBh + box + (uint64_t)(hf * (1024 >> 4)), 2, 2, id_g, k & 1);
                     }
                     mma_commit(&s.cbt_done);
                 }
@@ -1022,8 +1026,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
             float2 row = make_float2(0.0f, 0.0f), col = row, be = row, al = row;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 c = reinterpret_cast<const float2 *>(sm + kSumCol + 64 * k)[lane];
-                col.x += c.x; col.y += c.y;
+                if (k >= lane >> 3) {       // (rows 16 k .. reach columns 2 lane, 2 lane + 1)
+                    const float2 c = reinterpret_cast<const float2 *>(sm + kSumCol + 64 * k)[lane];
+                    col.x += c.x; col.y += c.y;
+                }
                 if (k < 2) {
                     const float2 r = reinterpret_cast<const float2 *>(sm + kSumRow + 64 * k)[lane];
                     const float2 u = reinterpret_cast<const float2 *>(sm + kSumBe + 64 * k)[lane], a = reinterpret_cast<const float2 *>(sm + kSumAl + 64 * k)[lane];
