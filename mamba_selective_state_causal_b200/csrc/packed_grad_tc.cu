@@ -118,7 +118,7 @@ __device__ __forceinline__ int grad_chunks(const PackedGradParams &p) { return p
 // Warps 0..7 keep the state (lane = n, 32 of p each), warps 8..15 fetch rows three chunks ahead and weigh them, warp
 // 16 issues the products, warp 17 runs the sums of dt A, warp 18 the copies out.
 constexpr int kWalkState = 8, kWalkScale = 8, kWalkThreads = 32 * (kWalkState + kWalkScale + 3);
-constexpr int kWalkStages = 4;
+constexpr int kWalkStages = 5;
 
 struct SmemWalk {
     uint8_t op[kWalkStages][2 * kTile];     // B (or C): columns 0..63, 64..127
@@ -274,11 +274,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
             cp_commit();
         };
 #pragma unroll 1
-        for (int it = 0; it < kWalkStages - 1; ++it) fetch(it);
+        for (int it = 0; it < kWalkStages - 2; ++it) fetch(it);
 #pragma unroll 1
         for (int it = 0; it < n; ++it) {
             const int st = it % kWalkStages, b = it & 1;
-            cp_wait<kWalkStages - 2>();
+            cp_wait<kWalkStages - 3>();
             if (!(ok = cwait(&s.w_ready[it & 7], (uint32_t)(it >> 3) & 1, abort, lim))) break;
             if (it >= 2 && !(ok = cwait(&s.mma_done[(it - 2) & 3], (uint32_t)((it - 2) >> 2) & 1, abort, lim))) break;
 #pragma unroll
@@ -292,9 +292,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.xs_ready[it & 3]);
-            // the stage of chunk it - 1 for chunk it + 3
-            if (it >= 1 && !(ok = cwait(&s.mma_done[(it - 1) & 3], (uint32_t)((it - 1) >> 2) & 1, abort, lim))) break;
-            fetch(it + kWalkStages - 1);
+            fetch(it + kWalkStages - 2);            // the stage of chunk it - 2
         }
         if (!ok && lane == 0) raise_timeout(p, abort);
         cp_wait<0>();
@@ -310,7 +308,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
             const uint32_t b = uniform(it & 1), st = uniform(it % kWalkStages);
             if (elect_one()) {
                 mma_steps<kQ / 16>(tSu + 128 * b, smem_desc(smem_u32(s.op[st]), kTile, 1024), smem_desc(smem_u32(s.xs[b]), kTile, 1024), 128, 128, id, false);
-                mma_commit(&s.mma_done[st]);
+                mma_commit(&s.mma_done[it & 3]);
                 mma_commit(&s.acc_full[b]);
             }
             __syncwarp();
@@ -1090,20 +1088,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
 }
 
 // =============================================================== sums
-// Blocks 0 .. units - 1: dB and dC of a (chunk, group) whose heads make several blocks, in their order; the H blocks
+// The first kSumParts x units blocks: dB and dC of a (chunk, group) whose heads make several blocks, in their order; the H blocks
 // behind them: dA and dD of a head, in a fixed order.
+constexpr int kSumParts = 4;        // blocks to a unit
+
 __global__ void __launch_bounds__(256) packed_grad_sum_kernel(const PackedGradParams p, int ctas)
 {
     const int nch = grad_chunks(p);
     const int64_t units = p.plan.m64 * p.G;
-    if (blockIdx.x < units) {
+    if (blockIdx.x < kSumParts * units) {
         const GradSplit sp(p, nch, ctas);
-        const int64_t u = blockIdx.x;
+        const int64_t u = blockIdx.x / kSumParts;
         const int c = (int)(u / p.G), g = (int)(u % p.G);
         if (c >= nch || sp.nb == 1) return;
         const int4 d = p.plan.chunk64[c];
         const int rows = d.y & kChunkRows;
-        for (int i = threadIdx.x; i < rows * (kN / 4); i += blockDim.x) {
+        for (int i = threadIdx.x + blockDim.x * (blockIdx.x % kSumParts); i < rows * (kN / 4); i += kSumParts * blockDim.x) {
             const int r = i / (kN / 4), n4 = i % (kN / 4);
             float4 sb = make_float4(0.f, 0.f, 0.f, 0.f), sc = sb;
 #pragma unroll 4
@@ -1120,7 +1120,7 @@ __global__ void __launch_bounds__(256) packed_grad_sum_kernel(const PackedGradPa
         return;
     }
     __shared__ float sa[256], sd[256];
-    const int h = (int)(blockIdx.x - units);
+    const int h = (int)(blockIdx.x - kSumParts * units);
     float a = 0.0f, d = 0.0f;
     for (int c = threadIdx.x; c < nch; c += blockDim.x)
         if (p.plan.chunk64[c].y & kChunkRows) {
@@ -1168,7 +1168,7 @@ int launch_packed_grad_tc(const PackedGradParams &p, int ctas, cudaStream_t st)
     // parts of the chunk list: two waves of one CTA per SM, no more parts than sequences (they begin between sequences)
     const int64_t wide = 2 * (int64_t)p.H;
     const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(p.plan.nseq, (2 * (int64_t)ctas + wide - 1) / wide));
-    const int64_t units = p.plan.m64 * p.G + p.H;
+    const int64_t units = kSumParts * p.plan.m64 * p.G + p.H;
     if (units > 0x7fffffff) return 2;
     prof_begin(st, kKBwdChain);
     packed_grad_walk_kernel<<<dim3((unsigned)wide, (unsigned)parts), kWalkThreads, sizeof(SmemWalk), st>>>(p);
