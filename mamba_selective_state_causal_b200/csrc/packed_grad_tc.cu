@@ -7,12 +7,13 @@
 //   dB_j  = sum_{t>=j} M_tj C_t + w_j x_j^T Gam           w_j = dt_j e^{lam-cs_j}
 //   dC_t  = sum_{j<=t} M_tj B_j + e^{cs_t} dy_t^T h
 //   with E_tj = e^{cs_t-cs_j}, CB = C B^T, M_tj = E_tj dt_j (dy_t . x_j)
-// Three kernels:
+// Three kernels (16384 rows of 32 heads, 9 sequences, the longest of 7000: 448 us; the bytes that go in and out
+// would take 48, with h and Gam, which go through memory once, 210):
 //   walk      the states and the adjoints, chunk after chunk, from the first or the last of a sequence,
 //             kept in registers in fp32; only what the gradients multiply by leaves the kernel
 //   gradient  a CTA takes the heads of a chunk one after the other: dB and dC, sums over the heads of a
 //             group, stay in TMEM meanwhile, and C B^T is formed once
-//   sums      dB and dC of the chunks whose heads are shared by several CTAs; dA and dD
+//   sums      dB and dC of the groups that were done in several blocks of heads; dA and dD
 //
 // Precision.  Products take bf16 operands with fp32 sums; x, dy, B and C are bf16 as given.  An operand
 // that is not (the weighted x and dy, M, E o CB, and h and Gam) enters as its bf16 rounding plus the
@@ -114,7 +115,8 @@ __device__ __forceinline__ int grad_chunks(const PackedGradParams &p) { return p
 // One CTA per (part of the chunk list, state or adjoint, head): a part begins and ends between sequences.  Per chunk
 // the product S[n][p] = sum_j B[j][n] (w_j x_j[p]) (adjoint: C, e^{cs_j} dy) gets both parts of the weighted
 // operand side by side as 128 columns, and the state follows in registers, h = e^lam h + S.  What enters each chunk
-// goes out as the gradient kernel's operand, one bulk copy of 32 KB.
+// goes out as the gradient kernel's operand, one bulk copy of 32 KB.  What bounds it is a chunk's chain of waits,
+// 1.2 us, times the chunks of the longest part (136 in that batch): 166 us, at 3.3 TB/s of images.
 // Warps 0..7 keep the state (lane = n, 32 of p each), warps 8..15 fetch rows three chunks ahead and weigh them, warp
 // 16 issues the products, warp 17 runs the sums of dt A, warp 18 the copies out.
 constexpr int kWalkState = 8, kWalkScale = 8, kWalkThreads = 32 * (kWalkState + kWalkScale + 3);
@@ -422,12 +424,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
 // dx = (E CB)^T dy, dB += C^T M, dC += B^T M^T.  Warps 0..7: (M) E o CB and M in two parts, the row and column sums of
 // M o CB; (A) x_j . dxI_j and dy_t . YI_t; (D) dx.  Warps 8..15, ahead of them: (S) w x and e^{cs} dy in two parts;
 // (F) <Gam, h>.  (All 16 warps on one step after the other took 4.2 us per item, each step waiting for its own
-// latencies; so HERE.)
+// latencies; so 3.9.)
 // M = 64 accumulators use 16 of each 32 TMEM lanes: GX and CB keep columns 16 k .. 16 k + 7 in the lower and the eight
 // behind them in the upper 16, so that a warp's 16 rows and 16 columns lie on or off the triangle together; dxI and
 // YI share their columns that way.  The sums that make ddt are finished by a warp of their own.
 // TMEM: dB 0..63, dC 64..127 (lanes n, columns rows), dxI | YI 128..191 and 192..255, GX 256..287 and 288..319,
-// dx 320..383, CB 384..415.
+// dx 320..383, CB 384..415.  257 us for 8352 items: 4.6 us per item and SM, the tensor pipe busy a third of it.  Dealt
+// out to two issuing warps it took 290 (the registers of a 21st warp), with products under lane == 0 430.
 constexpr int kMathWarps = 8, kWeighWarps = 8, kGradWarps = kMathWarps + kWeighWarps, kGradThreads = 32 * (kGradWarps + 4);
 constexpr uint32_t kColB = 0, kColC = 64, kColI = 128, kColG = 256, kColDx = 320, kColCB = 384;
 constexpr uint32_t kUpper = 16u << 16;    // lanes 16..31 of each 32
@@ -452,7 +455,7 @@ constexpr int kSumCol = 0, kSumRow = 256, kSumBe = 384, kSumAl = 512, kSumDiag =
 
 // How the heads of the chunks are dealt out: in blocks of S heads of a group, nb blocks to a group.  The sums over the
 // heads of a block are formed in TMEM, where each addition is cut off instead of rounded, so a block has at most
-// kMaxBlock heads, added up in fp32 behind (blocks of 32 heads were off by 7.8e-6 of 64 bits, of 8 by HERE);
+// kMaxBlock heads, added up in fp32 behind (blocks of 32 heads were off by 7.8e-6 of 64 bits, of 8 by 3.8e-6);
 // a short batch gets smaller blocks, to load all SMs.
 constexpr int kMaxBlock = 8;
 struct GradSplit {

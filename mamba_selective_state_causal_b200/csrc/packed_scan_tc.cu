@@ -117,6 +117,7 @@ __device__ __forceinline__ void chunk_sums(const float2 (&d)[4], float A2a, floa
 // backwards, 64 at a time, so that the decay from each to the window's end is known when it is scaled.
 // Warps 0..15 scale X into its two bf16 parts (the rounding in place, the rest beside it), warp 16 issues the
 // products, warp 17 the loads, warps 18 and 19 run the dt sums of a head each, ahead of the others.
+// 65536 rows of 32 heads: 107 us, 0.97 us per step of 64 rows and two heads; of the bytes' time (x and B once) 0.4.
 constexpr int kStagesA = 4;
 constexpr int kQA = 64;                  // rows of a step
 constexpr uint32_t kBoxA = kQA * 128;    // 64 rows x 64 columns of bf16
@@ -372,13 +373,14 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
 //   store warp: y staged -> stored (TMA, or row by row for a short chunk), X of chunk c+2 into its slot
 //   compute warp (lane quarter q = warp & 3, column slice cs = warp >> 2 of the 128 (head, p) columns):
 //       T scaled; under Y, w o X into the C half of the B/C slot (spent once G and Ys have read C) and its
-//       remainder into hp (spent once Ys has read it); under S, y; then the state step of chunk c+1 -- or, where a
-//       sequence ends, its state to its slot and the next one's start in its place -- and under Ys the masked
-//       decay of chunk c+1
+//       remainder into hp (spent once Ys has read it); under S, y and the masked decay of chunk c+1; then the state
+//       step of chunk c+1 -- or, where a sequence ends, its state to its slot and the next one's start in its place
 //   scan warp: the running sums of chunk c+1, ready in registers, into shared memory as soon as every warp has
 //       used those of chunk c; it also starts the slot's state of a sequence about to begin into L2
-// The decay is kept away from S: both live off TMEM, and together they took 1.9 us where one after the other
-// takes 1.5.  A chunk of fewer than 128 rows takes only the K-steps (of 16 rows) of Y and S that have rows.
+// A chunk of fewer than 128 rows takes only the K-steps (of 16 rows) of Y and S that have rows.
+// What bounds it: the compute warps' chain of steps, 4.7 us per chunk and head pair (T 0.3, w o X 0.7, waiting for Y
+// 0.4, y 0.6, decay 1.3, state 0.9, waiting for Ys 0.3), with the tensor pipe busy for about half of it; the bytes
+// would take 1.6.  65536 rows of 32 heads: 261 us, of 8191 rows in 256 sequences 158.
 // TMEM (512 columns): R0 = 0..127 G; R1 = 128..255 Pm_a | Pm_b (bf16); T = 256..383; H = 384..511 (rows n).
 constexpr int kComputeWarps = 16;
 constexpr int kThreadsC = 32 * (kComputeWarps + 4);
@@ -667,13 +669,20 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.y_ready[c & 1]);
-
-            // ---- S is done too
-            if (!cwait(&s.mma_done[c & 1], (c >> 1) & 1, abort, lim)) { fail(); break; }
           }
-            // ---- the state step of chunk c+1, then its masked decay while its Ys runs
+            // ---- the masked decay of chunk c+1 while S runs
             if (c + 1 < nc) {
-                if (!cwait(&s.scan_ready, (c + 1) & 1, abort, lim)) { fail(); break; }
+                if (!(cwait(&s.scan_ready, (c + 1) & 1, abort, lim) && cwait(&s.g_done, (c + 1) & 1, abort, lim))) { fail(); break; }
+                tc_fence_after();
+                decay(s.desc[(c + 1) & 1].y & kChunkRows);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.pmw);
+            }
+            // ---- S is done too; the state step of chunk c+1
+            if (c >= 0 && !cwait(&s.mma_done[c & 1], (c >> 1) & 1, abort, lim)) { fail(); break; }
+            if (c + 1 < nc) {
                 tc_fence_after();
                 uint32_t hv[32];
                 const int4 dn = s.desc[(c + 1) & 1];
@@ -704,13 +713,6 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.ys_go);
                 if (slot >= 0 && !src) store_state(slot, hv);
-                if (!cwait(&s.g_done, (c + 1) & 1, abort, lim)) { fail(); break; }
-                tc_fence_after();
-                decay(dn.y & kChunkRows);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.pmw);
             }
         }
         if (!__any_sync(0xffffffffu, *abort != 0)) {
