@@ -186,6 +186,7 @@ struct PackedGradParams {
     float *ws_pA, *ws_pD;       // [H][m64]
     unsigned int *status;
     uint64_t wait_limit_ns;
+    int64_t test_drop_unit;
 };
 struct PackedGradLayout {
     size_t off_part, off_sums, off_pA, off_pD, bytes;

@@ -346,6 +346,7 @@ int ssd_packed_scan_backward(const ssd_packed_scan_bwd_args *a, ssd_stream_t str
         q.ws_pA = reinterpret_cast<float *>(ws + l.off_pA);
         q.ws_pD = reinterpret_cast<float *>(ws + l.off_pD);
         q.wait_limit_ns = api_wait_limit_ns();
+        q.test_drop_unit = api_take_drop_unit();
         rc = launch_packed_grad_tc(q, ctas, st);
         if (rc == 2) return api_fail(SSD_ERR_SHAPE, "packed scan backward grid too large");
         return rc ? cuda_fail("packed scan backward") : api_ok();

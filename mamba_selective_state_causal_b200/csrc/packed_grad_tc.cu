@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
         // ================================================= issuing warp
         const uint32_t id = idesc_bf16(128, 128, 1, 1);   // A = B^T (MN-major), B = the weighted rows and their remainders (MN-major)
         const uint32_t tSu = uniform(tS);
-        for (int it = 0; it < n; ++it) {
+        const bool live = (int64_t)(blockIdx.y * gridDim.x + blockIdx.x) != p.test_drop_unit;
+        for (int it = 0; live && it < n; ++it) {
             ok = cwait(&s.xs_ready[it & 3], (uint32_t)(it >> 2) & 1, abort, lim) &&
                  (it < 2 || cwait(&s.acc_free[it & 1], (uint32_t)((it >> 1) - 1) & 1, abort, lim));
             if (!ok) break;

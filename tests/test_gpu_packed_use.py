@@ -1,0 +1,237 @@
+"""The packed operators as a program uses them: gradients whose heads are dealt out in blocks, batches of nothing but empty
+sequences, refused offsets and slots, two streams at once, captured and replayed batches, a wait that runs out.
+
+Tolerances as in test_gpu_packed_scan.py and test_gpu_packed_conv.py (relL2 1e-5 against 64 bits for fp32 outputs); dB
+and dC of the tensor-core form add at most 8 heads' sums in TMEM, each addition cut off at 2^-23 of it: 160 additions
+of 2^-24 on average are 1e-5 if no term had a sign, and a tenth of that with signs at random.
+"""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+if __name__ == "__main__":
+    sys.path[:0] = [HERE, os.path.dirname(HERE)]
+
+import mamba_selective_state_causal_b200 as ssd
+import packed_ref as ref
+from test_gpu_packed_scan import DEV, F64, _data, _parts, _plan, _ref_in, _run
+
+pytestmark = pytest.mark.gpu
+
+
+def _grad_inputs(d, seed):
+    g = torch.Generator().manual_seed(seed)
+    n = len(d["slots"])
+    return (torch.randn(d["total"], d["H"] * d["P"], generator=g).to(d["dtype"]),
+            torch.randn(n, d["H"], d["P"], d["N"], generator=g))
+
+
+def _grads(d, dy, dh, plan=None, **kw):
+    x, B, C = _parts(d, d["v"].to(DEV))
+    return ssd.packed_scan_backward(x, B, C, d["dt"].to(DEV), d["A"].to(DEV), d["D"].to(DEV), dy.to(DEV), plan=plan or _plan(d),
+                                    H=d["H"], G=d["G"], h_in=d["h"].to(DEV), dh_out=dh.to(DEV), **kw)
+
+
+@pytest.mark.parametrize("lens,H,G,resume", [
+    ([130, 64], 3, 1, [1, 0]),                  # an odd number of heads, one to a block
+    ([200, 10, 0, 70], 6, 6, [1, 1, 1, 0]),     # every head its own group
+    ([300, 65, 700], 24, 1, [0, 1, 1]),         # blocks of two heads
+    ([1500, 1, 2339], 20, 1, [1, 1, 0]),        # blocks of eight heads, the last of four
+    ([900, 0, 0, 33, 800], 32, 2, [1, 1, 0, 0, 1]),
+])
+def test_gradient_blocks_of_heads(lens, H, G, resume):
+    """(the 64-bit recurrence runs on the GPU)"""
+    n = len(lens)
+    d = _data(lens, H, 64, 128, G, torch.bfloat16, 51, slots=list(range(n))[::-1], resume=resume, before=1, behind=2, n_slots=n)
+    dy, dh = _grad_inputs(d, 52)
+    x, B, C = (t.to(DEV) for t in _ref_in(d))
+    with torch.device(DEV):
+        r = ref.scan_grad(x, B, C, d["dt"].to(DEV), d["A"].to(DEV), d["D"].to(DEV), d["cu"], d["slots"], resume, d["h"].to(DEV),
+                          dy.to(DEV).view(-1, H, 64), dh.to(DEV), G)
+    plan = _plan(d)
+    o = _grads(d, dy, dh, plan)
+    a, b = d["cu"][0], d["cu"][-1]
+    for k in r:
+        got, want = (o[k], r[k]) if k in ("dA", "dD", "dh_in") else (o[k][a:b], r[k][a:b])
+        assert ref.rel(got, want) <= 1e-5, (k, ref.rel(got, want))
+    p = _grads(d, dy, dh, plan)
+    ssd.sync_status()
+    for k in r:                                 # sums in a fixed order
+        u, v = (o[k], p[k]) if k in ("dA", "dD", "dh_in") else (o[k][a:b], p[k][a:b])
+        assert torch.equal(u, v), k
+
+
+@pytest.mark.parametrize("dtype,P,N", [(torch.bfloat16, 64, 128), (torch.float32, 16, 16)])
+@pytest.mark.parametrize("behind", [0, 5])
+def test_nothing_but_empty_sequences(dtype, P, N, behind):
+    """States pass through, gradients of the weights are zero, rows of no sequence stay."""
+    d = _data([0, 0, 0], 2, P, N, 1, dtype, 53, slots=[2, 0, 1], resume=[1, 0, 1], behind=behind, n_slots=3)
+    pool = d["h"].to(DEV)
+    _run(d, h_in=pool, h_out=pool)
+    want = d["h"].clone()
+    want[0] = 0
+    assert torch.equal(pool.cpu(), want)
+    dy, dh = _grad_inputs(d, 54)
+    o = _grads(d, dy, dh)
+    ssd.sync_status()
+    assert (o["dA"] == 0).all() and (o["dD"] == 0).all()
+    assert torch.equal(o["dh_in"].cpu(), dh * torch.tensor([1.0, 0.0, 1.0])[:, None, None, None])
+
+
+def _refused():
+    with pytest.raises(ssd.SSDError) as e:
+        ssd.sync_status()
+    assert e.value.code == 10
+
+
+@pytest.mark.parametrize("cu,slots,kept", [
+    ([0, 40, 30, 100], [0, 1, 2], [0]),             # an offset behind the next one
+    ([0, 40, 70, 999], [0, 1, 2], [0, 1]),          # behind the rows
+    ([-3, 40, 70, 100], [0, 1, 2], [1, 2]),         # before them
+    ([0, 40, 70, 100], [0, 7, -9], [0]),            # slots that are none: computed, not kept
+    ([0, 40, 70, 100], [1, 1, 1], [0]),             # a slot named twice belongs to the first
+])
+@pytest.mark.parametrize("dtype,P,N", [(torch.bfloat16, 64, 128), (torch.float32, 16, 16)])
+def test_refused_offsets_and_slots(cu, slots, kept, dtype, P, N):
+    """What a plan refuses is reported, reads and writes nothing out of place, and leaves the other sequences as they are."""
+    total = 100
+    d = _data([total], 2, P, N, 1, dtype, 55, n_slots=3)
+    pool = d["h"].to(DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    plan = ssd.packed_plan(torch.tensor(cu, **i32), total, slots=torch.tensor(slots, **i32), resume=torch.ones(3, **i32), n_slots=3)
+    y = torch.full((total, 2, P), 7.0, dtype=dtype, device=DEV)
+    _run(d, plan=plan, h_in=pool, h_out=pool, y=y)
+    dy, _ = _grad_inputs(d, 56)
+    o = _grads(d, dy, torch.zeros(3, 2, P, N), plan)
+    torch.cuda.synchronize()
+    _refused()
+    assert all(torch.isfinite(o[k]).all() for k in ("dA", "dD"))
+    touched = {slots[i] for i in kept}
+    for i in kept:
+        a, b = cu[i], cu[i + 1]
+        e = dict(d, cu=[0, b - a], total=b - a, slots=[slots[i]], resume=[1], v=d["v"][a:b], dt=d["dt"][a:b])
+        p1 = d["h"].to(DEV)
+        y1, _ = _run(e, h_in=p1, h_out=p1)
+        ssd.sync_status()
+        assert torch.equal(p1[slots[i]], pool[slots[i]]) and torch.equal(y1, y[a:b])
+    for k in set(range(3)) - touched:
+        assert torch.equal(pool[k].cpu(), d["h"][k])
+
+
+@pytest.mark.parametrize("dtype,P,N", [(torch.bfloat16, 64, 128), (torch.float32, 32, 16)])
+def test_two_streams_at_once(dtype, P, N):
+    """Two batches in flight on two streams, each with its own workspace, get what each gets alone."""
+    ds = [_data([900, 40, 128], 4, P, N, 1, dtype, 57), _data([33, 700, 64, 1], 4, P, N, 2, dtype, 58)]
+    alone = []
+    for d in ds:
+        dy, dh = _grad_inputs(d, 59)
+        plan = _plan(d)
+        y, h = _run(d, plan=plan, h_in=d["h"].to(DEV), h_out=d["h"].to(DEV))
+        alone.append((d, dy, dh, plan, y, h, _grads(d, dy, dh, plan)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ds]
+    for _ in range(3):
+        got = []
+        for s, (d, dy, dh, plan, *_x) in zip(streams, alone):
+            with torch.cuda.stream(s):
+                got.append((*_run(d, plan=plan, h_in=d["h"].to(DEV), h_out=d["h"].to(DEV)), _grads(d, dy, dh, plan)))
+        torch.cuda.synchronize()
+        for (y, h, o), (d, _a, _b, _c, y0, h0, o0) in zip(got, alone):
+            assert torch.equal(y, y0) and torch.equal(h, h0)
+            for k in o0:
+                assert torch.equal(o[k], o0[k]), k
+    ssd.sync_status()
+
+
+def test_captured_batch_replayed_with_other_offsets():
+    """Plan, convolution, scan and their gradients in one graph, replayed for batches of other lengths in the same buffers."""
+    H, P, N, G, total, nseq = 4, 64, 128, 1, 512, 4
+    cch, g = H * P + 2 * G * N, torch.Generator().manual_seed(60)
+    u = torch.randn(total, cch, generator=g).to(DEV, torch.bfloat16)
+    w, bias = (torch.randn(cch, 4, generator=g) / 2).to(DEV), torch.randn(cch, generator=g).to(DEV)
+    dt = (torch.rand(total, H, generator=g) * 0.1).to(DEV)
+    A, D = -torch.exp(torch.rand(H, generator=g) * 2.77).to(DEV), torch.randn(H, generator=g).to(DEV)
+    dy = torch.randn(total, H * P, generator=g).to(DEV, torch.bfloat16)
+    tail0, h0 = torch.randn(nseq, 3, cch, generator=g).to(DEV, torch.bfloat16), torch.randn(nseq, H, P, N, generator=g).to(DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    cu, slots, resume = torch.tensor([0, 100, 100, 300, 512], **i32), torch.tensor([0, 1, 2, 3], **i32), torch.ones(nseq, **i32)
+    tail, h = tail0.clone(), h0.clone()
+    keep = {}
+
+    def step():
+        plan = ssd.packed_plan(cu, total, slots=slots, resume=resume, n_slots=nseq)
+        t_in, h_in = tail.clone(), h.clone()
+        v = ssd.packed_conv_forward(u, w, plan, bias, tail_in=t_in, tail_out=tail)
+        v = v[0] if isinstance(v, tuple) else v
+        x, B, C = v[:, :H * P], v[:, H * P:H * P + N], v[:, H * P + N:]
+        y, _ = ssd.packed_scan_forward(x, B, C, dt, A, D, plan=plan, H=H, G=G, h_in=h_in, h_out=h)
+        o = ssd.packed_scan_backward(x, B, C, dt, A, D, dy, plan=plan, H=H, G=G, h_in=h_in)
+        c = ssd.packed_conv_backward(u, w, plan, o["dx"].view(total, -1), o["dB"].view(total, -1), o["dC"].view(total, -1), bias=bias, tail_in=t_in)
+        keep.update(y=y, **{"s_" + k: t for k, t in o.items()}, **{"c_" + k: t for k, t in c.items() if t is not None})
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    graphed = dict(keep)
+    for c, k, r in (([0, 100, 100, 300, 512], [0, 1, 2, 3], [1, 1, 1, 1]), ([0, 512, 512, 512, 512], [3, 1, 0, 2], [1, 0, 1, 1]),
+                    ([7, 8, 200, 201, 500], [2, -1, 0, 3], [0, 1, 1, 1])):
+        for t, v in ((cu, c), (slots, k), (resume, r)):
+            t.copy_(torch.tensor(v, dtype=torch.int32))
+        tail.copy_(tail0)
+        h.copy_(h0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got, gt, gh = {n: t.clone() for n, t in graphed.items()}, tail.clone(), h.clone()
+        tail.copy_(tail0)
+        h.copy_(h0)
+        step()
+        ssd.sync_status()
+        assert torch.equal(gt, tail) and torch.equal(gh, h)
+        for n, t in keep.items():
+            a, b = (c[0], c[-1]) if t.shape[0] == total else (0, t.shape[0])
+            assert torch.equal(got[n][a:b], t[a:b]), n
+
+
+def _child(backward):
+    d = _data([700, 300], 4, 64, 128, 1, torch.bfloat16, 61)
+    dy, dh = _grad_inputs(d, 62)
+
+    def call():
+        if backward:
+            return _grads(d, dy, dh)["dx"]
+        return _run(d, h_in=d["h"].to(DEV), h_out=d["h"].to(DEV))[0]
+
+    call()
+    try:
+        ssd.sync_status()
+    except ssd.SSDError as e:
+        assert e.code == 8, e
+    else:
+        raise AssertionError("the dropped unit did not time out")
+    ssd.sync_status()
+    a, b = call(), call()
+    ssd.sync_status()
+    assert torch.isfinite(a).all() and torch.equal(a, b)
+    print("child ok")
+
+
+@pytest.mark.parametrize("backward", [0, 1])
+def test_wait_that_runs_out_is_reported(backward):
+    """One CTA's products are left out in the first call of a process (its hook): every wait for them is bounded, the status
+    says so, and the calls after it are right."""
+    env = dict(os.environ, SSD_TEST_DROP_UNIT="0", SSD_WAIT_LIMIT_MS="200")
+    r = subprocess.run([sys.executable, os.path.abspath(__file__), str(backward)], env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "child ok" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+
+
+if __name__ == "__main__":
+    _child(int(sys.argv[1]))
