@@ -7,7 +7,7 @@
 //   dB_j  = sum_{t>=j} M_tj C_t + w_j x_j^T Gam           w_j = dt_j e^{lam-cs_j}
 //   dC_t  = sum_{j<=t} M_tj B_j + e^{cs_t} dy_t^T h
 //   with E_tj = e^{cs_t-cs_j}, CB = C B^T, M_tj = E_tj dt_j (dy_t . x_j)
-// Three kernels (16384 rows of 32 heads, 9 sequences, the longest of 7000: 448 us; the bytes that go in and out
+// Three kernels (16384 rows of 32 heads, 9 sequences, the longest of 7000: 453 us; the bytes that go in and out
 // would take 48, with h and Gam, which go through memory once, 210):
 //   walk      the states and the adjoints, chunk after chunk, from the first or the last of a sequence,
 //             kept in registers in fp32; only what the gradients multiply by leaves the kernel
@@ -18,7 +18,8 @@
 // Precision.  Products take bf16 operands with fp32 sums; x, dy, B and C are bf16 as given.  An operand
 // that is not (the weighted x and dy, M, E o CB, and h and Gam) enters as its bf16 rounding plus the
 // bf16 rounding of what that leaves, 16 significant bits, and of such pairs all but the product of the
-// two remainders is formed: each term is off by about 2^-17.  State and adjoint are walked in fp32.
+// two remainders is formed: each term is off by about 2^-17.  State and adjoint are walked in fp32; where
+// few rows or heads are summed, they enter <Gam, h>, dxI and YI (below) in three parts, 24 bits (two_parts).
 //
 // All waits are bounded (tc::mbar_wait): on a timeout the CTA raises an abort flag, every thread
 // unwinds, copies and products in flight are drained, TMEM is freed and the status word reports it.
@@ -36,7 +37,13 @@ using namespace tc;
 constexpr int kQ = 64, kP = 64, kN = 128, kPN = kP * kN;
 constexpr uint32_t kTile = 64 * 128;      // 64 rows of 128 bytes, 128B-swizzled
 constexpr uint32_t kPiece = 128 * 128;    // a state's bf16 part: rows n, columns p, 128B-swizzled
-constexpr uint32_t kImage = 2 * kPiece;   // its rounding and the remainder
+// A state as the gradient's operand: kParts bf16 parts, each the rounding of what those before it leave
+template <int kParts> constexpr uint32_t kImage = kParts * kPiece;
+// Two parts where dA, one number per head, is made of many rows of many heads, three elsewhere: among random batches of
+// few rows or few heads two parts left dA off by up to 1.3e-5 of 64 bits, three by 2.4e-6 (worst of 120); from 1024
+// rows of 16 heads on two are off by 2e-6 as well (16384 rows of 32 heads: 1.9e-6), and three take 553 us instead
+// of 453 there.
+inline bool two_parts(int64_t total, int H) { return total >= 1024 && H >= 16; }
 
 __device__ __forceinline__ void raise_timeout(const PackedGradParams &p, volatile int *abort)
 {
@@ -115,18 +122,19 @@ __device__ __forceinline__ int grad_chunks(const PackedGradParams &p) { return p
 // One CTA per (part of the chunk list, state or adjoint, head): a part begins and ends between sequences.  Per chunk
 // the product S[n][p] = sum_j B[j][n] (w_j x_j[p]) (adjoint: C, e^{cs_j} dy) gets both parts of the weighted
 // operand side by side as 128 columns, and the state follows in registers, h = e^lam h + S.  What enters each chunk
-// goes out as the gradient kernel's operand, one bulk copy of 32 KB.  What bounds it is a chunk's chain of waits,
-// 1.2 us, times the chunks of the longest part (136 in that batch): 166 us, at 3.3 TB/s of images.
+// goes out as the gradient kernel's operand, one bulk copy each.  What bounds it is a chunk's chain of waits,
+// 1.2 us, times the chunks of the longest part (136 in that batch): 166 us, at 3.3 TB/s of states.
 // Warps 0..7 keep the state (lane = n, 32 of p each), warps 8..15 fetch rows three chunks ahead and weigh them, warp
 // 16 issues the products, warp 17 runs the sums of dt A, warp 18 the copies out.
 constexpr int kWalkState = 8, kWalkScale = 8, kWalkThreads = 32 * (kWalkState + kWalkScale + 3);
-constexpr int kWalkStages = 5;
+template <int kParts> constexpr int kWalkStages = kParts == 2 ? 5 : 4;    // (what shared memory has room for)
 
+template <int kParts>
 struct SmemWalk {
-    uint8_t op[kWalkStages][2 * kTile];     // B (or C): columns 0..63, 64..127
-    uint8_t xr[kWalkStages][kTile];         // x (or dy) as given, each thread its own 16 bytes
+    uint8_t op[kWalkStages<kParts>][2 * kTile];     // B (or C): columns 0..63, 64..127
+    uint8_t xr[kWalkStages<kParts>][kTile];         // x (or dy) as given, each thread its own 16 bytes
     uint8_t xs[2][2 * kTile];               // the weighted x (or dy), and what its rounding leaves
-    uint8_t img[2][kImage];
+    uint8_t img[2][kImage<kParts>];
     float w[8][kQ];
     float f[8];
     uint64_t w_ready[8], xs_ready[4], mma_done[4], acc_full[2], acc_free[2], img_ready[2], img_free[2], fin;
@@ -144,10 +152,15 @@ __device__ __forceinline__ int sequence_begin(const PackedPlan &p, int n, int64_
     return s.c64 + s.n64;
 }
 
+static_assert(sizeof(SmemWalk<2>) <= 232448 && sizeof(SmemWalk<3>) <= 232448, "the walk's shared memory");
+
+template <int kParts>
 __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const PackedGradParams p)
 {
     extern __shared__ __align__(1024) uint8_t sw_raw[];
-    SmemWalk &s = *reinterpret_cast<SmemWalk *>(sw_raw);
+    SmemWalk<kParts> &s = *reinterpret_cast<SmemWalk<kParts> *>(sw_raw);
+    constexpr int kStages = kWalkStages<kParts>;
+    constexpr uint32_t kImg = kImage<kParts>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = (int)(blockIdx.x % p.H);
     const bool adj = blockIdx.x >= p.H;
@@ -212,12 +225,18 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
             if (it >= 2 && !(ok = cwait(&s.img_free[b], (uint32_t)((it >> 1) - 1) & 1, abort, lim))) break;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                uint32_t hi[4], lo[4];
+                uint32_t v[kParts][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) split2(make_float2(hv[8 * k + 2 * i], hv[8 * k + 2 * i + 1]), hi[i], lo[i]);
-                const uint32_t o = swz(nn, 4 * e + k);
-                sts128(s.img[b] + o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                sts128(s.img[b] + kPiece + o, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                for (int i = 0; i < 4; ++i) {
+                    float2 r = make_float2(hv[8 * k + 2 * i], hv[8 * k + 2 * i + 1]);
+#pragma unroll
+                    for (int w = 0; w < kParts; ++w) {
+                        v[w][i] = pack_bf16x2(r.x, r.y);
+                        r = make_float2(r.x - bf16_lo(v[w][i]), r.y - bf16_hi(v[w][i]));
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < kParts; ++w) sts128(s.img[b] + w * kPiece + swz(nn, 4 * e + k), make_uint4(v[w][0], v[w][1], v[w][2], v[w][3]));
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -260,7 +279,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
         auto fetch = [&](int it) {
             if (it < n) {
                 const int4 d = __ldg(tab + chunk_of(it));
-                const int rows = d.y & kChunkRows, st = it % kWalkStages;
+                const int rows = d.y & kChunkRows, st = it % kStages;
                 const char *xs = xg + d.x * xrs + 16 * cx, *os = og + d.x * ors + 16 * co;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -276,11 +295,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
             cp_commit();
         };
 #pragma unroll 1
-        for (int it = 0; it < kWalkStages - 2; ++it) fetch(it);
+        for (int it = 0; it < kStages - 2; ++it) fetch(it);
 #pragma unroll 1
         for (int it = 0; it < n; ++it) {
-            const int st = it % kWalkStages, b = it & 1;
-            cp_wait<kWalkStages - 3>();
+            const int st = it % kStages, b = it & 1;
+            cp_wait<kStages - 3>();
             if (!(ok = cwait(&s.w_ready[it & 7], (uint32_t)(it >> 3) & 1, abort, lim))) break;
             if (it >= 2 && !(ok = cwait(&s.mma_done[(it - 2) & 3], (uint32_t)((it - 2) >> 2) & 1, abort, lim))) break;
 #pragma unroll
@@ -294,7 +313,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.xs_ready[it & 3]);
-            fetch(it + kWalkStages - 2);            // the stage of chunk it - 2
+            fetch(it + kStages - 2);            // the stage of chunk it - 2
         }
         if (!ok && lane == 0) raise_timeout(p, abort);
         cp_wait<0>();
@@ -308,7 +327,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
                  (it < 2 || cwait(&s.acc_free[it & 1], (uint32_t)((it >> 1) - 1) & 1, abort, lim));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t b = uniform(it & 1), st = uniform(it % kWalkStages);
+            const uint32_t b = uniform(it & 1), st = uniform(it % kStages);
             if (elect_one()) {
                 mma_steps<kQ / 16>(tSu + 128 * b, smem_desc(smem_u32(s.op[st]), kTile, 1024), smem_desc(smem_u32(s.xs[b]), kTile, 1024), 128, 128, id, false);
                 mma_commit(&s.mma_done[it & 3]);
@@ -399,7 +418,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
             const int b = it & 1;
             if (!(ok = cwait(&s.img_ready[b], (uint32_t)(it >> 1) & 1, abort, lim))) break;
             if (lane == 0) {
-                bulk_store(p.ws_img + (((int64_t)chunk_of(it) * p.H + h) * 2 + (adj ? 1 : 0)) * (int64_t)kImage, s.img[b], kImage);
+                bulk_store(p.ws_img + (((int64_t)chunk_of(it) * p.H + h) * 2 + (adj ? 1 : 0)) * (int64_t)kImg, s.img[b], kImg);
                 tma_store_commit();
                 // the copy before it has read its image
                 tma_store_wait_read<1>();
@@ -430,29 +449,32 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
 // behind them in the upper 16, so that a warp's 16 rows and 16 columns lie on or off the triangle together; dxI and
 // YI share their columns that way.  The sums that make ddt are finished by a warp of their own.
 // TMEM: dB 0..63, dC 64..127 (lanes n, columns rows), dxI | YI 128..191 and 192..255, GX 256..287 and 288..319,
-// dx 320..383, CB 384..415.  257 us for 8352 items: 4.6 us per item and SM, the tensor pipe busy a third of it.  Dealt
+// dx 320..383, CB 384..415.  261 us for 8352 items: 4.6 us per item and SM, the tensor pipe busy a third of it.  Dealt
 // out to two issuing warps it took 290 (the registers of a 21st warp), with products under lane == 0 430.
 constexpr int kMathWarps = 8, kWeighWarps = 8, kGradWarps = kMathWarps + kWeighWarps, kGradThreads = 32 * (kGradWarps + 4);
 constexpr uint32_t kColB = 0, kColC = 64, kColI = 128, kColG = 256, kColDx = 320, kColCB = 384;
 constexpr uint32_t kUpper = 16u << 16;    // lanes 16..31 of each 32
 
+template <int kParts> constexpr int kGradSlots = kParts == 2 ? 3 : 2;
+
+template <int kParts>
 struct SmemGrad {
     uint8_t cb[4 * kTile];                // C columns 0..63, 64..127, B likewise
     uint8_t xd[2][2 * kTile];             // x, dy of items i, i + 1
-    uint8_t st[3][kImage];                // Gam and h in turn
+    uint8_t st[kGradSlots<kParts>][kImage<kParts>];           // Gam and h in turn
     uint8_t sc[4 * kTile];                // w x, its remainder, e^{cs} dy, its remainder
     uint8_t mk[4 * kTile];                // E o CB, its remainder, M, its remainder
     float cs[2][kQ], dt[2][kQ], suf[2][kQ];   // sums of dt A (log2 units) up to each row, dt, sums after each row
     uint64_t cb_full, cb_empty, xd_full[2], xd_empty[2], st_full[3], st_empty[3];
-    uint64_t cs_ready[2], gx_done[2], in_done[2], cbt_done, sc_ready, inter_done, mk_ready, dx_done, intra_done, acc_free;
+    uint64_t cs_ready[2], gx_done[2], in_done[2], cbt_done, sc_ready, inter_done, mk_ready, dx_done, intra_done, acc_free, res_ready;
     uint64_t sums_ready[2], sums_free[2], fin;
     uint32_t tmem;
     int abort;
 };
-static_assert(sizeof(SmemGrad) <= 232448, "the gradient kernel's shared memory");
+static_assert(sizeof(SmemGrad<2>) <= 232448 && sizeof(SmemGrad<3>) <= 232448, "the gradient kernel's shared memory");
 
 // partial sums of an item on their way to the warp that finishes them (in global memory: shared memory is full)
-constexpr int kSumCol = 0, kSumRow = 256, kSumBe = 384, kSumAl = 512, kSumDiag = 640, kSumD = 704, kSumF = 768, kSumFloats = 800;
+constexpr int kSumCol = 0, kSumRow = 256, kSumBe = 384, kSumAl = 512, kSumDiag = 640, kSumD = 704, kSumF = 768, kSumRes = 800, kSumFloats = 864;
 
 // How the heads of the chunks are dealt out: in blocks of S heads of a group, nb blocks to a group.  The sums over the
 // heads of a block are formed in TMEM, where each addition is cut off instead of rounded, so a block has at most
@@ -524,10 +546,13 @@ struct Items {
     }
 };
 
+template <int kParts>
 __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const PackedGradParams p)
 {
     extern __shared__ __align__(1024) uint8_t sg_raw[];
-    SmemGrad &s = *reinterpret_cast<SmemGrad *>(sg_raw);
+    SmemGrad<kParts> &s = *reinterpret_cast<SmemGrad<kParts> *>(sg_raw);
+    constexpr int kSlots = kGradSlots<kParts>;
+    constexpr uint32_t kImg = kImage<kParts>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const GradSplit split(p, grad_chunks(p), gridDim.x);
     Items m(p, split);
@@ -541,10 +566,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
             mbar_init(&s.cs_ready[i], 1); mbar_init(&s.gx_done[i], 1); mbar_init(&s.in_done[i], 1);
             mbar_init(&s.sums_ready[i], kGradWarps); mbar_init(&s.sums_free[i], 1);
         }
-        for (int i = 0; i < 3; ++i) { mbar_init(&s.st_full[i], 1); mbar_init(&s.st_empty[i], 1 + kWeighWarps); }
+        for (int i = 0; i < kSlots; ++i) { mbar_init(&s.st_full[i], 1); mbar_init(&s.st_empty[i], 1 + kWeighWarps); }
         mbar_init(&s.cbt_done, 1); mbar_init(&s.sc_ready, kWeighWarps); mbar_init(&s.inter_done, 1);
         mbar_init(&s.mk_ready, kMathWarps); mbar_init(&s.dx_done, 1); mbar_init(&s.intra_done, 1);
-        mbar_init(&s.acc_free, kMathWarps); mbar_init(&s.fin, 1);
+        mbar_init(&s.acc_free, kMathWarps); mbar_init(&s.res_ready, kMathWarps); mbar_init(&s.fin, 1);
         s.abort = 0;
         fence_mbar_init();
     }
@@ -565,7 +590,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
         const int mrow = 16 * q + (lane & 15);         // row of an M = 64 accumulator
         float *sums = p.ws_sums + (int64_t)blockIdx.x * 2 * kSumFloats;
-        uint32_t unit = 0;
+        uint32_t unit = 0, block = 0;
+        // With states in three parts: what the two parts of M leave out on its diagonal, of the block's heads, added to dB
+        // and dC in fp32.  Where every sequence is a token or two, dC_t is M_tt summed over the heads times B_t, and one
+        // scalar's error, however the heads cancel, is all of dC_t's: 1.3e-5 at five sequences of one token without this.
+        float res = 0.0f;
         for (; ok && m.valid; m.next()) {
             const int it = m.it, b = it & 1;
             const uint32_t ph = (uint32_t)(it >> 1) & 1;
@@ -603,10 +632,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
                         mm[i] = eg * dj[i];
                         kp[i] = eg * cbi;
                         if (j0 + i < mrow) row = fmaf(mm[i], cbi, row);
-                        if (j0 + i == mrow) {
-                            sm[kSumDiag + mrow] = kp[i];
-                            sm[kSumD + mrow] = __uint_as_float(gx[i]);
-                        }
                     }
                     uint32_t hi[4], lo[4];
                     const uint32_t o = swz(mrow, (j0 >> 3));
@@ -618,6 +643,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
                     for (int i = 0; i < 4; ++i) split2(make_float2(mm[2 * i], mm[2 * i + 1]), hi[i], lo[i]);
                     sts128(s.mk + 2 * kTile + o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
                     sts128(s.mk + 3 * kTile + o, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    if (k == q) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (j0 + i == mrow) {
+                                sm[kSumDiag + mrow] = kp[i];
+                                sm[kSumD + mrow] = __uint_as_float(gx[i]);
+                                if (kParts == 3) res += mm[i] - (i & 1 ? bf16_hi(hi[i / 2]) : bf16_lo(hi[i / 2])) - (i & 1 ? bf16_hi(lo[i / 2]) : bf16_lo(lo[i / 2]));
+                                if (kParts == 3 && m.last) {
+                                    sm[kSumRes + mrow] = res;
+                                    res = 0.0f;
+                                }
+                            }
+                    }
                     // column sums over the 16 rows: each halving step keeps half of the columns and adds the partner's copy
                     // of them
                     float k4[4], k2[2];
@@ -646,6 +684,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
                 if (lane == 0) mbar_arrive(&s.mk_ready);
                 row += __shfl_xor_sync(0xffffffffu, row, 16);
                 if (lane < 16) sm[kSumRow + 64 * e + mrow] = row;
+                if (kParts == 3 && m.last) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.res_ready);
+                }
             }
             // ---- (A)
             if (!(ok = cwait(&s.in_done[b], ph, abort, lim))) break;
@@ -708,9 +750,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
             if (lane == 0) mbar_arrive(&s.xd_empty[b]);
             // ---- the block's dB and dC
             if (m.last) {
+                if (kParts == 3 && !(ok = cwait(&s.res_ready, block++ & 1, abort, lim))) break;
                 if (!(ok = cwait(&s.intra_done, (uint32_t)it & 1, abort, lim))) break;
                 tc_fence_after();
                 const int nn = 32 * q + lane, g = m.h / R, rows = m.d.y & kChunkRows;
+                const __nv_bfloat16 *Bn = static_cast<const __nv_bfloat16 *>(p.B) + m.d.x * p.Brs + g * kN + nn;
+                const __nv_bfloat16 *Cn = static_cast<const __nv_bfloat16 *>(p.C) + m.d.x * p.Crs + g * kN + nn;
                 float *dB, *dC;
                 int64_t rs;
                 if (m.nb == 1) {
@@ -723,22 +768,35 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
                     rs = kN;
                 }
 #pragma unroll 1
-                for (int u = 0; u < 2; ++u) {
-                    const int t0 = 32 * e + 16 * u;
-                    uint32_t ab[16], ac[16];
-                    tmem_ld16(tm + lanes + kColB + t0, ab);
-                    tmem_ld16(tm + lanes + kColC + t0, ac);
-                    tmem_wait_ld(ab, ac);
-                    if (u == 1) {
+                for (int u = 0; u < 4; ++u) {
+                    const int t0 = 32 * e + 8 * u;
+                    uint32_t ab[8], ac[8];
+                    tmem_ld8(tm + lanes + kColB + t0, ab);
+                    tmem_ld8(tm + lanes + kColC + t0, ac);
+                    // (three parts) what M's diagonal left out
+                    float r[8];
+                    __nv_bfloat16 bn[8], cn[8];
+                    if (kParts == 3) {
+                        *reinterpret_cast<float4 *>(r) = *reinterpret_cast<const float4 *>(sm + kSumRes + t0);
+                        *reinterpret_cast<float4 *>(r + 4) = *reinterpret_cast<const float4 *>(sm + kSumRes + t0 + 4);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            bn[i] = t0 + i < rows ? __ldg(Bn + (t0 + i) * p.Brs) : __float2bfloat16(0.0f);
+                            cn[i] = t0 + i < rows ? __ldg(Cn + (t0 + i) * p.Crs) : __float2bfloat16(0.0f);
+                        }
+                    }
+                    tmem_wait_ld8(ab);
+                    tmem_wait_ld8(ac);
+                    if (u == 3) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&s.acc_free);
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
+                    for (int i = 0; i < 8; ++i)
                         if (t0 + i < rows) {
-                            dB[(t0 + i) * rs + nn] = __uint_as_float(ab[i]);
-                            dC[(t0 + i) * rs + nn] = __uint_as_float(ac[i]);
+                            dB[(t0 + i) * rs + nn] = kParts == 3 ? fmaf(r[i], __bfloat162float(cn[i]), __uint_as_float(ab[i])) : __uint_as_float(ab[i]);
+                            dC[(t0 + i) * rs + nn] = kParts == 3 ? fmaf(r[i], __bfloat162float(bn[i]), __uint_as_float(ac[i])) : __uint_as_float(ac[i]);
                         }
                 }
             }
@@ -776,27 +834,37 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
             }
             // ---- (F)
             const int ug = 2 * it, uh = 2 * it + 1;
-            if (!(ok = cwait(&s.st_full[ug % 3], (uint32_t)(ug / 3) & 1, abort, lim) && cwait(&s.st_full[uh % 3], (uint32_t)(uh / 3) & 1, abort, lim))) break;
-            const uint8_t *G = s.st[ug % 3], *h = s.st[uh % 3];
+            if (!(ok = cwait(&s.st_full[ug % kSlots], (uint32_t)(ug / kSlots) & 1, abort, lim) && cwait(&s.st_full[uh % kSlots], (uint32_t)(uh / kSlots) & 1, abort, lim))) break;
+            const uint8_t *G = s.st[ug % kSlots], *h = s.st[uh % kSlots];
             float2 a = make_float2(0.0f, 0.0f);
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 const uint32_t o = 16 * (t + 256 * k);
-                const uint4 gh = lds128(G + o), gl = lds128(G + kPiece + o), hh = lds128(h + o), hl = lds128(h + kPiece + o);
-                const uint32_t gx[4] = {gh.x, gh.y, gh.z, gh.w}, gy[4] = {gl.x, gl.y, gl.z, gl.w};
-                const uint32_t hx[4] = {hh.x, hh.y, hh.z, hh.w}, hy[4] = {hl.x, hl.y, hl.z, hl.w};
+                uint4 gv[kParts], hv[kParts];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 g1 = unpack2(gx[i]), h1 = unpack2(hx[i]);
-                    a = fma2(g1, h1, a);
-                    a = fma2(g1, unpack2(hy[i]), a);
-                    a = fma2(unpack2(gy[i]), h1, a);
+                for (int i = 0; i < kParts; ++i) { gv[i] = lds128(G + i * kPiece + o); hv[i] = lds128(h + i * kPiece + o); }
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    float2 g2[kParts], h2[kParts];
+#pragma unroll
+                    for (int i = 0; i < kParts; ++i) {
+                        const uint32_t gw[4] = {gv[i].x, gv[i].y, gv[i].z, gv[i].w}, hw[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w};
+                        g2[i] = unpack2(gw[w]);
+                        h2[i] = unpack2(hw[w]);
+                    }
+                    // the sum of a value's parts, smallest first
+#pragma unroll
+                    for (int i = kParts - 2; i >= 0; --i) {
+                        g2[i] = make_float2(g2[i].x + g2[i + 1].x, g2[i].y + g2[i + 1].y);
+                        h2[i] = make_float2(h2[i].x + h2[i + 1].x, h2[i].y + h2[i + 1].y);
+                    }
+                    a = fma2(g2[0], h2[0], a);
                 }
             }
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&s.st_empty[ug % 3]);
-                mbar_arrive(&s.st_empty[uh % 3]);
+                mbar_arrive(&s.st_empty[ug % kSlots]);
+                mbar_arrive(&s.st_empty[uh % kSlots]);
             }
             float v = a.x + a.y;
 #pragma unroll
@@ -836,7 +904,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
             return true;
         };
         auto from_states = [&](int it, bool first, bool enter) -> bool {
-            const uint32_t b = uniform(it & 1), sg = uniform((2 * it) % 3), sh = uniform((2 * it + 1) % 3), acc = uniform(first ? 0 : 1);
+            const uint32_t b = uniform(it & 1), sg = uniform((2 * it) % kSlots), sh = uniform((2 * it + 1) % kSlots), acc = uniform(first ? 0 : 1);
             if (enter) {
                 if (!cwait(&s.cb_full, unit & 1, abort, lim)) return false;
                 ++unit;
@@ -855,12 +923,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
             const uint32_t G = smem_u32(s.st[sg]), h = smem_u32(s.st[sh]);
             for (int w = 0; w < 2; ++w) {
                 const int u = 2 * it + w;
-                if (!cwait(&s.st_full[u % 3], (uint32_t)(u / 3) & 1, abort, lim)) return false;
+                if (!cwait(&s.st_full[u % kSlots], (uint32_t)(u / kSlots) & 1, abort, lim)) return false;
                 if (elect_one()) {
                     const uint64_t ds = smem_desc(w ? h : G, kTile, 1024);
                     const uint64_t da = w ? dCk : dBk;
 #pragma unroll 1
-                    for (int k = 0; k < 4; ++k)      // both parts, both halves of n
+                    for (int k = 0; k < 2 * kParts; ++k)      // every part, both halves of n
                         mma_steps<4>(tu + kColI + 64 * b + w * kUpper, da + (uint64_t)((k & 1) * (kTile >> 4)),
                                   ds + (uint64_t)((k >> 1) * (kPiece >> 4) + (k & 1) * 512), 2, 128, id_i, k > 0);
                 }
@@ -974,11 +1042,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
         int issued = 0;
         for (; ok && m.valid; m.next()) {
             for (int w = 0; ok && w < 2; ++w) {
-                const int u = 2 * m.it + w, k = u % 3;
-                if (u >= 3 && !(ok = cwait(&s.st_empty[k], (uint32_t)(u / 3 - 1) & 1, abort, lim))) break;
+                const int u = 2 * m.it + w, k = u % kSlots;
+                if (u >= kSlots && !(ok = cwait(&s.st_empty[k], (uint32_t)(u / kSlots - 1) & 1, abort, lim))) break;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&s.st_full[k], kImage);
-                    bulk_load(s.st[k], p.ws_img + (((int64_t)m.chunk * p.H + m.h) * 2 + (w ? 0 : 1)) * (int64_t)kImage, kImage, &s.st_full[k]);
+                    mbar_arrive_expect_tx(&s.st_full[k], kImg);
+                    bulk_load(s.st[k], p.ws_img + (((int64_t)m.chunk * p.H + m.h) * 2 + (w ? 0 : 1)) * (int64_t)kImg, kImg, &s.st_full[k]);
                 }
                 ++issued;
                 __syncwarp();
@@ -987,7 +1055,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
         if (lane == 0) {
             if (!ok) raise_timeout(p, abort);
             // the last copy into each place lands before the CTA's shared memory is released
-            for (int u = issued > 3 ? issued - 3 : 0; u < issued; ++u) mbar_wait(&s.st_full[u % 3], (uint32_t)(u / 3) & 1, nullptr, 100000000ull);
+            for (int u = issued > kSlots ? issued - kSlots : 0; u < issued; ++u) mbar_wait(&s.st_full[u % kSlots], (uint32_t)(u / kSlots) & 1, nullptr, 100000000ull);
         }
         __syncwarp();
     } else {
@@ -1156,7 +1224,7 @@ PackedGradLayout packed_grad_layout(int64_t nseq, int64_t total, int H, int ctas
     const int64_t m64 = packed_layout(nseq, total).m64, blocks = std::max<int64_t>(4 * ctas, 2 * m64 * H / kMaxBlock);
     auto round = [](size_t b) { return (b + 255) & ~size_t(255); };
     PackedGradLayout l;
-    l.off_part = (size_t)m64 * H * 2 * kImage;
+    l.off_part = (size_t)m64 * H * 2 * (two_parts(total, H) ? kImage<2> : kImage<3>);
     l.off_sums = l.off_part + (size_t)blocks * (2 * kQ * kN) * sizeof(float);
     l.off_pA = l.off_sums + round((size_t)ctas * 2 * kSumFloats * sizeof(float));
     l.off_pD = l.off_pA + round((size_t)m64 * H * sizeof(float));
@@ -1164,10 +1232,12 @@ PackedGradLayout packed_grad_layout(int64_t nseq, int64_t total, int H, int ctas
     return l;
 }
 
-int launch_packed_grad_tc(const PackedGradParams &p, int ctas, cudaStream_t st)
+template <int kParts>
+static int launch_parts(const PackedGradParams &p, int ctas, cudaStream_t st)
 {
     static std::atomic<int> walk_done[64], grad_done[64];
-    if (!allow_smem(packed_grad_walk_kernel, (int)sizeof(SmemWalk), walk_done) || !allow_smem(packed_grad_tc_kernel, (int)sizeof(SmemGrad), grad_done))
+    if (!allow_smem(packed_grad_walk_kernel<kParts>, (int)sizeof(SmemWalk<kParts>), walk_done) ||
+        !allow_smem(packed_grad_tc_kernel<kParts>, (int)sizeof(SmemGrad<kParts>), grad_done))
         return 7;
     // parts of the chunk list: two waves of one CTA per SM, no more parts than sequences (they begin between sequences)
     const int64_t wide = 2 * (int64_t)p.H;
@@ -1175,15 +1245,20 @@ int launch_packed_grad_tc(const PackedGradParams &p, int ctas, cudaStream_t st)
     const int64_t units = kSumParts * p.plan.m64 * p.G + p.H;
     if (units > 0x7fffffff) return 2;
     prof_begin(st, kKBwdChain);
-    packed_grad_walk_kernel<<<dim3((unsigned)wide, (unsigned)parts), kWalkThreads, sizeof(SmemWalk), st>>>(p);
+    packed_grad_walk_kernel<kParts><<<dim3((unsigned)wide, (unsigned)parts), kWalkThreads, sizeof(SmemWalk<kParts>), st>>>(p);
     prof_end(st, kKBwdChain);
     prof_begin(st, kKBwdGrad);
-    packed_grad_tc_kernel<<<(unsigned)ctas, kGradThreads, sizeof(SmemGrad), st>>>(p);
+    packed_grad_tc_kernel<kParts><<<(unsigned)ctas, kGradThreads, sizeof(SmemGrad<kParts>), st>>>(p);
     prof_end(st, kKBwdGrad);
     prof_begin(st, kKBwdReduce);
     packed_grad_sum_kernel<<<(unsigned)units, 256, 0, st>>>(p, ctas);
     prof_end(st, kKBwdReduce);
     return cudaGetLastError() == cudaSuccess ? 0 : 7;
+}
+
+int launch_packed_grad_tc(const PackedGradParams &p, int ctas, cudaStream_t st)
+{
+    return two_parts(p.plan.total, p.H) ? launch_parts<2>(p, ctas, st) : launch_parts<3>(p, ctas, st);
 }
 
 }  // namespace ssd
