@@ -64,6 +64,29 @@ __device__ __forceinline__ void split8(uint4 v, float w, uint4 &hi, uint4 &lo)
     lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// dt as the scan uses it (dt_effective), with softplus(v) = max(v, 0) + log(1 + e^-|v|) from one exponential and one
+// quotient: log(1 + e) = 2 artanh(s) = 2 (s + s^3 / 3 + s^5 / 5 + ..), s = e / (2 + e) <= 1/3, cut off at s^17 (2e-9 of
+// it).  The scan warps take eight of them per lane and step: with log1p they, not the products, set pass A's pace.
+__device__ __forceinline__ float dt_used(const PackedScanParams &p, float raw, float bias)
+{
+    float v = raw + bias;
+    if (p.dt_softplus) {
+        const float e = ex2(-fabsf(v) * kLog2e), q = __fdividef(e, 2.0f + e), q2 = q * q;
+        float t = 1.0f / 17.0f;
+        t = fmaf(t, q2, 1.0f / 15.0f);
+        t = fmaf(t, q2, 1.0f / 13.0f);
+        t = fmaf(t, q2, 1.0f / 11.0f);
+        t = fmaf(t, q2, 1.0f / 9.0f);
+        t = fmaf(t, q2, 1.0f / 7.0f);
+        t = fmaf(t, q2, 1.0f / 5.0f);
+        t = fmaf(t, q2, 1.0f / 3.0f);
+        const float r = 2.0f * q;
+        v = fmaxf(v, 0.0f) + fmaf(r * q2, t, r);
+    }
+    if (p.dt_max > 0.0f) v = fminf(fmaxf(v, p.dt_min), p.dt_max);
+    return v;
+}
+
 // dt of rows 4 lane .. 4 lane + 3 of a chunk for the two heads ha, ha + 1, as the scan uses it (0 past its rows)
 __device__ __forceinline__ void load_dt(const PackedScanParams &p, int row0, int rows, int lane, int ha, float2 (&d)[4])
 {
@@ -73,14 +96,14 @@ __device__ __forceinline__ void load_dt(const PackedScanParams &p, int row0, int
         d[k] = i < rows ? *reinterpret_cast<const float2 *>(p.dt + ((int64_t)row0 + i) * p.H + ha) : make_float2(0.0f, 0.0f);
     }
 }
-__device__ __forceinline__ void use_dt(const PackedScanParams &p, int rows, int lane, int ha, float2 (&d)[4])
+__device__ __forceinline__ void use_dt(const PackedScanParams &p, int rows, int lane, float2 bias, float2 (&d)[4])
 {
     if (!p.dt_bias && !p.dt_softplus && !(p.dt_max > 0.0f)) return;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (4 * lane + k < rows) {
-            d[k].x = dt_effective(d[k].x, p.dt_bias, ha, p.dt_softplus, p.dt_min, p.dt_max);
-            d[k].y = dt_effective(d[k].y, p.dt_bias, ha + 1, p.dt_softplus, p.dt_min, p.dt_max);
+            d[k].x = dt_used(p, d[k].x, bias.x);
+            d[k].y = dt_used(p, d[k].y, bias.y);
         }
 }
 
@@ -292,6 +315,7 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
         const int hd = warp - kScaleWarpsA - 2, h = ha + hd;
         const float A2 = p.A[h] * kLog2e;
         const bool used = p.dt_bias || p.dt_softplus || p.dt_max > 0.0f;
+        const float bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
         float suf = 0.0f;                   // sum of dt A (log2 units) after the chunks scanned so far
         // dt of four steps at a time, loaded while the four before them are used
         float dn[4][2], dc[4][2];
@@ -317,7 +341,7 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
             for (int e = 0; e < 4; ++e) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    d[e][q] = used ? dt_effective(dc[e][q], p.dt_bias, h, p.dt_softplus, p.dt_min, p.dt_max) : dc[e][q];
+                    d[e][q] = used ? dt_used(p, dc[e][q], bias) : dc[e][q];
                 a1[e] = d[e][1] * A2;
                 inc[e] = a1[e] + d[e][0] * A2;
             }
@@ -888,6 +912,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
         } else if (warp == kComputeWarps + 3) {
             // ============================================= scan warp: lane l holds rows 4 l .. 4 l + 3
             const float A2a = p.A[ha] * kLog2e, A2b = p.A[ha + 1] * kLog2e;
+            const float2 bias = p.dt_bias ? make_float2(p.dt_bias[ha], p.dt_bias[ha + 1]) : make_float2(0.0f, 0.0f);
             bool ok = live;
             int4 dn = chunks[0];
             float2 dt[4];
@@ -895,7 +920,7 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
             for (int c = 0; ok && c < nc; ++c) {
                 const int4 d = dn;
                 if (c + 1 < nc) dn = chunks[c + 1];
-                use_dt(p, d.y & kChunkRows, lane, ha, dt);
+                use_dt(p, d.y & kChunkRows, lane, bias, dt);
                 float ca[4], cb[4], ta, tb;
                 chunk_sums(dt, A2a, A2b, lane, ca, cb, ta, tb);
                 // the sum at the end of this lane's 32-row block (row 32 J + 31 = lane 8 J + 7)
