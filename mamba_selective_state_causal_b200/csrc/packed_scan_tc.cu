@@ -140,16 +140,18 @@ __device__ __forceinline__ void chunk_sums(const float2 (&d)[4], float A2a, floa
 // backwards, 64 at a time, so that the decay from each to the window's end is known when it is scaled.
 // Warps 0..15 scale X into its two bf16 parts (the rounding in place, the rest beside it), warp 16 issues the
 // products, warp 17 the loads, warps 18 and 19 run the dt sums of a head each, ahead of the others.
-// 65536 rows of 32 heads: 107 us, 0.97 us per step of 64 rows and two heads; of the bytes' time (x and B once) 0.4.
-constexpr int kStagesA = 4;
+// 65536 rows of 32 heads: 97 us, 0.8 us per step of 64 rows and two heads, which the chain of load, scaling and
+// product through five stages sets; the bytes (x and B once) would take 44.
+constexpr int kStagesA = 5;
 constexpr int kQA = 64;                  // rows of a step
 constexpr uint32_t kBoxA = kQA * 128;    // 64 rows x 64 columns of bf16
 constexpr int kScaleWarpsA = 16;
 constexpr int kThreadsA = 32 * (kScaleWarpsA + 4);
-constexpr uint32_t kStageA = 6 * kBoxA;   // B (2 boxes), X of head a and b, the remainders of X a and b
+constexpr uint32_t kStageA = 4 * kBoxA;   // B (2 boxes), X of head a and b
 
 struct SmemA {
     uint8_t stage[kStagesA][kStageA];
+    uint8_t rem[2][2 * kBoxA];            // the remainders of w o X of two steps
     float w[kStagesA][2][kQA];
     uint64_t full[kStagesA], w_ready[kStagesA], xw_ready[kStagesA], empty[kStagesA];
     uint64_t acc_full, fin;
@@ -210,10 +212,13 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
         for (int it = warp >> 3; it < nc; it += 2) {
             const int st = it % kStagesA;
             const uint32_t ph = (uint32_t)(it / kStagesA) & 1;
-            ok = ewait(&s.full[st], ph, abort, lim) && ewait(&s.w_ready[st], ph, abort, lim);
+            // (the remainders' place is free once the step two before has been multiplied)
+            ok = ewait(&s.w_ready[st], ph, abort, lim) &&
+                 (it < 2 || ewait(&s.empty[(it - 2) % kStagesA], (uint32_t)((it - 2) / kStagesA) & 1, abort, lim)) &&
+                 ewait(&s.full[st], ph, abort, lim);
             if (!ok) break;
             const float w = s.w[st][hd][j];
-            uint8_t *xrow = s.stage[st] + (2 + hd) * kBoxA, *lrow = s.stage[st] + (4 + hd) * kBoxA;
+            uint8_t *xrow = s.stage[st] + (2 + hd) * kBoxA, *lrow = s.rem[it & 1] + hd * kBoxA;
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) {
                 const uint32_t o = swz(j, c0 + cc);
@@ -257,10 +262,10 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
             ok = ewait(&s.xw_ready[st], (uint32_t)(it / kStagesA) & 1, abort, lim);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t sb = smem_u32(s.stage[0]) + uniform(st) * kStageA;
+            const uint32_t sb = smem_u32(s.stage[0]) + uniform(st) * kStageA, sr = smem_u32(s.rem[0]) + uniform(it & 1) * 2 * kBoxA;
             if (elect_one()) {
                 const uint64_t db = smem_desc(sb, kBoxA, 1024);
-                const uint64_t dh = smem_desc(sb + 2 * kBoxA, kBoxA, 1024), dl = smem_desc(sb + 4 * kBoxA, kBoxA, 1024);
+                const uint64_t dh = smem_desc(sb + 2 * kBoxA, kBoxA, 1024), dl = smem_desc(sr, kBoxA, 1024);
 #pragma unroll
                 for (int kk = 0; kk < kQA / 16; ++kk)
                     mma_ss(tSu, db + (uint64_t)(kk * 128), dh + (uint64_t)(kk * 128), id_s, it > 0 || kk > 0);
