@@ -62,9 +62,11 @@ template <typename T> constexpr int kDepth = 96 / (3 * (int)sizeof(Vec8<T>)) * 2
 
 // One CTA: `teams` rows side by side, d / 8 threads each; it walks the rows blockIdx.x * teams + team, a grid apart.
 // kMode: 0 groups of a power of two up to 32 threads, 1 of a multiple of 32, 2 any.
-// kMost bounds the threads (rows wider than 2048 channels need up to 1024).  Two CTAs of 256 threads per SM leave
-// the 128 registers that a thread needs: 222 us at 65536 rows of 2048 in bf16 (6.0 TB/s), against 294 with
-// three (80 registers, a few of them spilled) and 335 with four.
+// kMost bounds the threads, and with them the registers.  Two CTAs of 256 threads per SM leave the 128 registers that
+// a thread needs: 222 us at 65536 rows of 2048 in bf16 (6.0 TB/s), against 294 with three (80 registers, a few of
+// them spilled) and 335 with four.  Wider rows take one CTA per SM of 512 threads (122 registers; 4096 channels 0.8 to
+// 0.9 of the copy rate), 640 (96; 5120 channels 0.7 to 0.8, with the 64 registers that 1024 threads leave 0.33) or up
+// to 1024 (spilled; 8192 channels 0.43).
 template <typename T, int kMode, int kMost>
 __global__ void __launch_bounds__(kMost, kMost == 256 ? 2 : 1) gated_norm_bwd_kernel(NormBwdParams p, int teams)
 {
@@ -268,8 +270,11 @@ NormBwdPlan norm_bwd_plan(int64_t rows, int d, int sms)
 int launch_gated_norm_backward(const NormBwdParams &p, int dtype, int sms, cudaStream_t st)
 {
     const NormBwdPlan pl = norm_bwd_plan(p.rows, p.d, sms);
-    if (pl.threads > 256) return dtype == 1 ? launch_t<__nv_bfloat16, 1024>(p, pl, st) : launch_t<float, 1024>(p, pl, st);
-    return dtype == 1 ? launch_t<__nv_bfloat16, 256>(p, pl, st) : launch_t<float, 256>(p, pl, st);
+    const bool b = dtype == 1;
+    if (pl.threads <= 256) return b ? launch_t<__nv_bfloat16, 256>(p, pl, st) : launch_t<float, 256>(p, pl, st);
+    if (pl.threads <= 512) return b ? launch_t<__nv_bfloat16, 512>(p, pl, st) : launch_t<float, 512>(p, pl, st);
+    if (pl.threads <= 640) return b ? launch_t<__nv_bfloat16, 640>(p, pl, st) : launch_t<float, 640>(p, pl, st);
+    return b ? launch_t<__nv_bfloat16, 1024>(p, pl, st) : launch_t<float, 1024>(p, pl, st);
 }
 
 }  // namespace ssd
