@@ -259,29 +259,54 @@ __global__ void __launch_bounds__(kThr) packed_output_kernel(PackedScanParams p)
 }
 
 // the state entering each window: st = the start of a sequence that begins in window k (its slot's state
-// or zero), else the state that entered k;  h_in[k+1] = e^{dA_k} st + S_k.  One thread per four
-// state elements; a window that no sequence leaves ends the run.
+// or zero), else the state that entered k;  h_in[k+1] = e^{dA_k} st + S_k.  One thread per four state elements.  What
+// each window does is found by the threads side by side, kTails windows at a time, and S is loaded kAhead windows ahead
+// (a window after the other waited for three dependent loads each: 37 us for 87 windows, 21 now).
+constexpr int kTails = kThr, kAhead = 8;
 template <bool k64>
 __global__ void __launch_bounds__(kThr) packed_chain_kernel(PackedScanParams p)
 {
+    __shared__ int what[kTails];        // 1: a sequence leaves the window, 2: it begins there, 4: from the copy of its slot
+    __shared__ float decay[kTails];
     const int PN = p.P * p.N, h = blockIdx.y;
     const int e = 4 * (blockIdx.x * blockDim.x + threadIdx.x);
     const int n = k64 ? packed_n64(p.plan, p.status) : packed_n128(p.plan, p.status);
     const int per = (n + p.nw - 1) / p.nw;
-    if (e >= PN) return;
-    float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k + 1 < p.nw; ++k) {
-        const WindowTail t = window_tail<k64>(p.plan, n, per, k);
-        if (!t.crosses) continue;
-        const int64_t at = ((int64_t)k * p.H + h) * PN + e;
-        const float4 s = *reinterpret_cast<const float4 *>(p.ws_S + at);
-        if (t.begins) {
-            const PackedSeq q = p.plan.seqs[t.seq];
-            st = p.h_in && q.resume ? *reinterpret_cast<const float4 *>(p.ws_start + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool live = e < PN;
+    const float4 zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 st = zero4;
+    for (int k0 = 0; k0 + 1 < p.nw; k0 += kTails) {
+        const int kn = min(kTails, p.nw - 1 - k0);
+        __syncthreads();
+        if ((int)threadIdx.x < kn) {
+            const int k = k0 + threadIdx.x;
+            const WindowTail t = window_tail<k64>(p.plan, n, per, k);
+            int w = 0;
+            if (t.crosses) w = 1 | (t.begins ? 2 | (p.h_in && p.plan.seqs[t.seq].resume ? 4 : 0) : 0);
+            what[threadIdx.x] = w;
+            decay[threadIdx.x] = t.crosses ? expf(p.ws_dA[(int64_t)k * p.H + h]) : 0.0f;
         }
-        const float a = expf(p.ws_dA[(int64_t)k * p.H + h]);
-        st = make_float4(fmaf(a, st.x, s.x), fmaf(a, st.y, s.y), fmaf(a, st.z, s.z), fmaf(a, st.w, s.w));
-        *reinterpret_cast<float4 *>(p.ws_hin + at + (int64_t)p.H * PN) = st;
+        __syncthreads();
+        if (!live) continue;
+        for (int i0 = 0; i0 < kn; i0 += kAhead) {
+            float4 s[kAhead], b[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int w = i0 + i < kn ? what[i0 + i] : 0;
+                const int64_t at = ((int64_t)(k0 + i0 + i) * p.H + h) * PN + e;
+                s[i] = w & 1 ? *reinterpret_cast<const float4 *>(p.ws_S + at) : zero4;
+                b[i] = w & 4 ? *reinterpret_cast<const float4 *>(p.ws_start + at) : zero4;
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int w = i0 + i < kn ? what[i0 + i] : 0;
+                if (!(w & 1)) continue;
+                if (w & 2) st = b[i];
+                const float a = decay[i0 + i];
+                st = make_float4(fmaf(a, st.x, s[i].x), fmaf(a, st.y, s[i].y), fmaf(a, st.z, s[i].z), fmaf(a, st.w, s[i].w));
+                *reinterpret_cast<float4 *>(p.ws_hin + ((int64_t)(k0 + i0 + i + 1) * p.H + h) * PN + e) = st;
+            }
+        }
     }
 }
 
