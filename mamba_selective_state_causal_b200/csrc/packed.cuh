@@ -284,7 +284,7 @@ __device__ __forceinline__ void window_enter(const PackedScanParams &p, int4 d, 
 constexpr int kMaxOwnWindows = 16;         // up to so many windows each forms its entering state for itself
 
 int launch_packed_plan(const PackedPlanParams &p, cudaStream_t st);
-int launch_packed_conv(const PackedConvParams &p, int dtype, cudaStream_t st);
+int launch_packed_conv(const PackedConvParams &p, int dtype, int sms, cudaStream_t st);
 int launch_packed_conv_backward(const PackedConvBwdParams &p, int dtype, cudaStream_t st);
 bool packed_scan_tc_shape(int dtype, int H, int P, int N, int G);
 int launch_packed_scan_tc(const PackedScanParams &p, bool carry, cudaStream_t st);

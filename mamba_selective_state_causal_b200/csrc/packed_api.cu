@@ -196,7 +196,7 @@ int ssd_packed_conv_forward(const ssd_packed_conv_args *a, ssd_stream_t stream)
     p.plan = packed_view(a->plan, a->nseq, a->total);
     p.u = a->u; p.urs = a->u_row_stride; p.w = a->conv_w; p.bias = a->conv_bias;
     p.tail_in = a->tail_in; p.tail_out = a->tail_out; p.v = a->v; p.vrs = a->v_row_stride; p.C_ch = a->C_ch;
-    rc = launch_packed_conv(p, a->dtype, (cudaStream_t)stream);
+    rc = launch_packed_conv(p, a->dtype, api_sm_count(), (cudaStream_t)stream);
     if (rc == 2) return api_fail(SSD_ERR_SHAPE, "packed conv grid too large");
     return rc ? cuda_fail("packed conv") : api_ok();
 }

@@ -86,7 +86,7 @@ template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <typename T>
-__global__ void __launch_bounds__(kPackedConvThreads, 2) packed_conv_kernel(PackedConvParams p)
+__global__ void __launch_bounds__(kPackedConvThreads, 2) packed_conv_kernel(PackedConvParams p, int pieces)
 {
     using IO = ConvVec<T>;
     constexpr int V = IO::kN;
@@ -94,13 +94,15 @@ __global__ void __launch_bounds__(kPackedConvThreads, 2) packed_conv_kernel(Pack
     const int ncv = p.C_ch / V;
     const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int c0 = (int)(gid % ncv) * V;
-    const int64_t chunk = gid / ncv;
+    const int64_t chunk = gid / ncv / pieces;
+    const int r0 = (int)(gid / ncv % pieces) * (64 / pieces);
     int4 d;
     if (!packed_chunk64(p.plan, chunk, p.status, d)) return;
-    const int n = d.y & kChunkRows;
-    const bool head = (d.y & kChunkFirst) != 0;
+    const int n = min((d.y & kChunkRows) - r0, 64 / pieces);
+    if (r0 > 0 && n <= 0) return;
+    const bool head = (d.y & kChunkFirst) != 0 && r0 == 0;
     const T *u = reinterpret_cast<const T *>(p.u) + c0;
-    const int64_t t0 = d.x;
+    const int64_t t0 = d.x + r0;
     const T *up = u + t0 * p.urs;
     Vec16p *slot = ring + threadIdx.x;
     // one commit group per row (empty ones past the end keep the count uniform)
@@ -179,16 +181,20 @@ __global__ void __launch_bounds__(kPackedConvThreads, 2) packed_conv_kernel(Pack
 }
 
 template <typename T>
-int launch_conv_t(const PackedConvParams &p, cudaStream_t st)
+int launch_conv_t(const PackedConvParams &p, int sms, cudaStream_t st)
 {
+    // a chunk's rows in up to 8 pieces, while there are fewer CTAs than the SMs hold: what a small batch costs is one
+    // thread's rows, one after the other (169 rows of 288 channels in fp32: 25 us in one piece, 9 in eight, the time of the call)
     const int64_t threads = p.plan.m64 * (p.C_ch / ConvVec<T>::kN);
-    const int64_t blocks = (threads + kPackedConvThreads - 1) / kPackedConvThreads;
+    int pieces = 1;
+    while (pieces < 8 && 2 * pieces * threads <= 2 * (int64_t)sms * kPackedConvThreads) pieces *= 2;
+    const int64_t blocks = (pieces * threads + kPackedConvThreads - 1) / kPackedConvThreads;
     if (blocks > 0x7fffffffLL) return 2;
     constexpr int smem = kRing * kPackedConvThreads * (int)sizeof(Vec16p);
     static std::atomic<int> done[64];
     if (!allow_smem(packed_conv_kernel<T>, smem, done)) return 7;
     prof_begin(st, kKPackedConv);
-    packed_conv_kernel<T><<<(unsigned)blocks, kPackedConvThreads, smem, st>>>(p);
+    packed_conv_kernel<T><<<(unsigned)blocks, kPackedConvThreads, smem, st>>>(p, pieces);
     prof_end(st, kKPackedConv);
     return cudaGetLastError() == cudaSuccess ? 0 : 7;
 }
@@ -442,10 +448,10 @@ __global__ void __launch_bounds__(32 * kRedWarps) packed_conv_reduce_kernel(Pack
 
 }  // namespace
 
-int launch_packed_conv(const PackedConvParams &p, int dtype, cudaStream_t st)
+int launch_packed_conv(const PackedConvParams &p, int dtype, int sms, cudaStream_t st)
 {
     if (p.plan.m64 == 0) return 0;
-    return dtype == 1 ? launch_conv_t<__nv_bfloat16>(p, st) : launch_conv_t<float>(p, st);
+    return dtype == 1 ? launch_conv_t<__nv_bfloat16>(p, sms, st) : launch_conv_t<float>(p, sms, st);
 }
 
 int launch_packed_conv_backward(const PackedConvBwdParams &p, int dtype, cudaStream_t st)
