@@ -3,7 +3,7 @@
 //   v = silu(bias + w0 tail[0] + w1 tail[1] + w2 tail[2] + w3 u),   tail' = [tail[1], tail[2], u]
 //   h' = exp(dt A) h + dt x B^T,   y = C h' + D x           per head, x, B, C = v
 // The bytes are the states': 2 P N 4 per stream and head, read and written once; the rest is small.
-// A cluster of up to 8 CTAs serves one stream, each CTA a run of heads.  A CTA starts its first
+// A cluster of up to 8 (few streams: 16) CTAs serves one stream, each CTA a run of heads.  A CTA starts its first
 // states into shared memory (one bulk copy of P N floats each, kStages in flight) before it forms
 // the conv of its heads' x and their groups' B and C from the old buffer; then it updates state after
 // state in place in shared memory and sends each back with one bulk copy.  The cluster is what lets
@@ -231,11 +231,14 @@ __global__ void __launch_bounds__(kSlotThreads) decode_slots_kernel(SlotDecodePa
     if (tid == 0) tma_store_wait<0>();
 }
 
+constexpr int kNotWide = -1;
+constexpr int kRoom = 200 * 1024;         // shared memory of a CTA, at most
+
 template <typename T, int nq>
 int launch_slots_n(const SlotDecodeParams &p, int cluster, size_t smem, cudaStream_t st)
 {
     static std::atomic<int> done[64];
-    if (!allow_smem(decode_slots_kernel<T, nq>, (int)smem, done)) return 7;
+    if (!allow_smem(decode_slots_kernel<T, nq>, cluster > 8 ? kRoom : (int)smem, done)) return 7;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)p.b * (unsigned)cluster);
     cfg.blockDim = dim3(kSlotThreads);
@@ -248,6 +251,27 @@ int launch_slots_n(const SlotDecodeParams &p, int cluster, size_t smem, cudaStre
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    if (cluster > 8) {
+        // asked once per device: how many such clusters run at a time, each CTA with an SM to itself (plus 1; more
+        // streams than that would wait for others to end)
+        static std::atomic<int> wide[64];
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 7;
+        int w = wide[dev].load(std::memory_order_relaxed);
+        if (w == 0) {
+            int active = 0;
+            cudaLaunchConfig_t most = cfg;
+            most.dynamicSmemBytes = kRoom;
+            if (cudaFuncSetAttribute(decode_slots_kernel<T, nq>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+                cudaOccupancyMaxActiveClusters(&active, decode_slots_kernel<T, nq>, &most) != cudaSuccess) {
+                active = 0;
+                cudaGetLastError();
+            }
+            w = active + 1;
+            wide[dev].store(w, std::memory_order_relaxed);
+        }
+        if (p.b > w - 1) return kNotWide;
+    }
     prof_begin(st, kKSlotDecode);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_slots_kernel<T, nq>, p);
     prof_end(st, kKSlotDecode);
@@ -267,9 +291,8 @@ int launch_slots_t(const SlotDecodeParams &p, int cluster, size_t smem, cudaStre
 
 }  // namespace
 
-int launch_slot_decode(SlotDecodeParams p, int dtype, int sms, cudaStream_t st)
+static int launch_slots(SlotDecodeParams p, int cluster, int dtype, int sms, cudaStream_t st)
 {
-    int cluster = 8;
     while (cluster > 1 && cluster > p.H) cluster /= 2;
     p.heads_per_cta = (p.H + cluster - 1) / cluster;
     // groups that a run of heads can touch
@@ -277,7 +300,7 @@ int launch_slot_decode(SlotDecodeParams p, int dtype, int sms, cudaStream_t st)
     const int groups = p.heads_per_cta / hpg + 2 < p.G ? p.heads_per_cta / hpg + 2 : p.G;
     const size_t small = sizeof(float) * ((size_t)p.heads_per_cta * (p.P + 4) + (size_t)groups * 2 * p.N);
     const size_t piece = sizeof(float) * (size_t)(p.P / 2) * p.N;
-    const size_t room = 200 * 1024;
+    const size_t room = kRoom;
     if (small + 3 * piece > room) return 6;
     const int np = 2 * p.heads_per_cta;
     p.stages = p.b * cluster <= sms ? (int)std::min<size_t>(std::min(np, kMaxStages), (room - small) / piece) : std::min(np, 3);
@@ -285,6 +308,14 @@ int launch_slot_decode(SlotDecodeParams p, int dtype, int sms, cudaStream_t st)
     if ((2 * p.G * p.N + cluster - 1) / cluster > 4 * kSlotThreads) return 6;
     if ((int64_t)p.b * cluster > 0x7fffffffLL) return 6;
     return dtype == 1 ? launch_slots_t<__nv_bfloat16>(p, cluster, smem, st) : launch_slots_t<float>(p, cluster, smem, st);
+}
+
+int launch_slot_decode(const SlotDecodeParams &p, int dtype, int sms, cudaStream_t st)
+{
+    // 16 CTAs to a stream while the device runs so many clusters of 16 at a time: a CTA takes its heads one after the
+    // other (64 heads, 5 streams: 23 us with 8 CTAs each, 12 with 16; 32 heads, 2 streams: 12 and 8)
+    const int rc = 16 * (int64_t)p.b <= sms && p.H >= 16 ? launch_slots(p, 16, dtype, sms, st) : kNotWide;
+    return rc == kNotWide ? launch_slots(p, 8, dtype, sms, st) : rc;
 }
 
 }  // namespace ssd

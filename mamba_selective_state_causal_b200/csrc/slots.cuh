@@ -27,6 +27,6 @@ struct SlotDecodeParams {
     uint64_t wait_limit_ns;
 };
 
-int launch_slot_decode(SlotDecodeParams p, int dtype, int sms, cudaStream_t st);
+int launch_slot_decode(const SlotDecodeParams &p, int dtype, int sms, cudaStream_t st);
 
 }  // namespace ssd
