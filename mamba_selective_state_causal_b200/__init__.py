@@ -638,6 +638,17 @@ def _rows3(t, rows, H, P, dtype, dev, name):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
+def _on_stream(f, args):
+    """f(**args) with args' stream current, so that what f allocates or clears is ordered on that stream too, not on the
+    one that was current (whose next tensors would take a freed workspace's place while the call still runs)."""
+    stream = args.pop("stream")
+    t = next(iter(args.values()))
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    with torch.cuda.stream(stream):
+        return f(**args)
+
+
 def _launch(fn, a, dev, stream):
     """Call a C entry point with `dev` current, on `stream` or the device's current stream."""
     if dev.index is not None and dev.index != torch.cuda.current_device():
@@ -684,6 +695,8 @@ def packed_plan(cu_seqlens, total, *, slots=None, resume=None, n_slots=0, max_se
     bound of the lengths (0: total).  buf: the plan's memory (uint8, lib().ssd_packed_plan_size(n, total)
     bytes), to make it again in the same place (under a captured graph).
     """
+    if stream is not None:
+        return _on_stream(packed_plan, locals())
     dev = _device(cu_seqlens)
     n = cu_seqlens.numel() - 1
     if n < 0:
@@ -718,6 +731,8 @@ def packed_conv_forward(u, w, plan, bias=None, tail_in=None, tail_out=None, v=No
     u: [total, C_ch] (a view with any row stride of whole 16 bytes); tail_in, tail_out: [n_slots, 3, C_ch] or
     None, tail_out may be tail_in.  Rows of v that belong to no sequence stay as they were.
     """
+    if stream is not None:
+        return _on_stream(packed_conv_forward, locals())
     dev = _device(u)
     total, cch = u.shape
     dt = u.dtype
@@ -748,6 +763,8 @@ def packed_conv_backward(u, w, plan, dx, dB, dC, *, bias=None, tail_in=None, dta
     them; dtail_out: [n, 3, C_ch] float32 or None, by sequence.  ``out`` may hold outputs under the same keys;
     rows of no sequence stay as they were in them, and are zero in those allocated here.
     """
+    if stream is not None:
+        return _on_stream(packed_conv_backward, locals())
     dev = _device(u)
     total, cch = u.shape
     hp, gn = math.prod(dx.shape[1:]), math.prod(dB.shape[1:])
@@ -818,6 +835,8 @@ def packed_scan_forward(x, B, C, dt, A, D=None, *, plan, H, G=1, h_in=None, h_ou
     slots that the batch does not name stay as they were.  dt_bias / dt_softplus / dt_limit as in scan_forward.
     Rows of y that belong to no sequence stay as they were.
     """
+    if stream is not None:
+        return _on_stream(packed_scan_forward, locals())
     dev = _device(x)
     a = PackedScanArgs()
     total, P, N = _scan_inputs(a, x, B, C, dt, A, D, h_in, plan, H, G, dev)
@@ -846,6 +865,8 @@ def packed_scan_backward(x, B, C, dt, A, D, dy, *, plan, H, G=1, h_in=None, dh_o
     ``out`` may hold outputs under the same keys; rows of no sequence stay as they were in them, and are
     zero in those allocated here.
     """
+    if stream is not None:
+        return _on_stream(packed_scan_backward, locals())
     dev = _device(x)
     a = PackedScanBwdArgs()
     total, P, N = _scan_inputs(a, x, B, C, dt, A, D, h_in, plan, H, G, dev)
@@ -866,6 +887,8 @@ def decode_slots(u, conv_w, dt, A, D=None, *, slots, tail_in, h_in, H, P, N, G=1
     """One token of b streams of a pool: u [b, C_ch], dt [b, H], slots [b] int32 (-1 = an empty row, whose y is
     zero).  tail_in, tail_out: [n_slots, 3, C_ch], h_in, h_out: [n_slots, H, P, N] float32; without tail_out /
     h_out they are updated in place.  Returns {"y": [b, H, P], "h_out", "tail_out"}."""
+    if stream is not None:
+        return _on_stream(decode_slots, locals())
     dev = _device(u)
     b, cch = u.shape
     io, f32 = u.dtype, torch.float32
@@ -921,6 +944,8 @@ def gated_rmsnorm_backward(dout, y, z, weight, eps=1e-5, group_size=0, out=None,
     dout, y, z: [..., d] with the same leading shape, rows of d contiguous channels.  ``out`` may hold outputs
     under the same keys; dy may be dout or y, dz may be z (a row is read before it is written).
     """
+    if stream is not None:
+        return _on_stream(gated_rmsnorm_backward, locals())
     dev = _device(y)
     shape, io = y.shape, y.dtype
     d = shape[-1]

@@ -147,6 +147,43 @@ def test_two_streams_at_once(dtype, P, N):
     ssd.sync_status()
 
 
+@pytest.mark.parametrize("dtype,P,N", [(torch.bfloat16, 64, 128), (torch.float32, 32, 16)])
+def test_on_a_stream_that_is_behind(dtype, P, N):
+    """A call on a stream of its own allocates and clears there: tensors that the current stream makes meanwhile do not
+    take the place of its workspace and outputs."""
+    d = _data([700, 40, 128], 4, P, N, 1, dtype, 63)
+    dy, dh = _grad_inputs(d, 64)
+    x, B, C = _parts(d, d["v"].to(DEV))
+    dt, A, D, h0, dy, dh = (t.to(DEV) for t in (d["dt"], d["A"], d["D"], d["h"], dy, dh))
+    u, w = torch.randn(d["total"], x.shape[1] + 2 * N, device=DEV).to(dtype), torch.randn(x.shape[1] + 2 * N, 4, device=DEV)
+    z, nw = torch.randn_like(dy), torch.randn(4 * P, device=DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    cu, slots, resume = torch.tensor(d["cu"], **i32), torch.tensor(d["slots"], **i32), torch.tensor(d["resume"], **i32)
+
+    def calls(stream):
+        plan = ssd.packed_plan(cu, d["total"], slots=slots, resume=resume, n_slots=d["n_slots"], stream=stream)
+        v = ssd.packed_conv_forward(u, w, plan, stream=stream)[0]
+        y, _ = ssd.packed_scan_forward(x, B, C, dt, A, D, plan=plan, H=4, h_in=h0, stream=stream)
+        o = ssd.packed_scan_backward(x, B, C, dt, A, D, dy, plan=plan, H=4, h_in=h0, dh_out=dh, stream=stream)
+        c = ssd.packed_conv_backward(u, w, plan, o["dx"], o["dB"], o["dC"], stream=stream)
+        n = ssd.gated_rmsnorm_backward(dy, x.contiguous(), z, nw, stream=stream)
+        return {"v": v, "y": y, **{"s" + k: t for k, t in o.items()}, **{"c" + k: t for k, t in c.items()}, **{"n" + k: t for k, t in n.items()}}
+
+    want = calls(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+    got = calls(s)
+    junk = [torch.full((1 << 22,), float("nan"), device=DEV) for _ in range(64)]
+    torch.cuda.synchronize()
+    ssd.sync_status()
+    del junk
+    for k, t in want.items():
+        assert t is None or torch.equal(got[k], t), k
+
+
 def test_captured_batch_replayed_with_other_offsets():
     """Plan, convolution, scan and their gradients in one graph, replayed for batches of other lengths in the same buffers."""
     H, P, N, G, total, nseq = 4, 64, 128, 1, 512, 4

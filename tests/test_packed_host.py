@@ -186,3 +186,11 @@ def test_rows_of_a_view(ssd):
     assert ssd._rows3(wide[:, 1:3], 4, 2, 8, f32, cpu, "y") == (wide.data_ptr() + 32, 40)
     with pytest.raises(ValueError):
         ssd._rows3(y.transpose(1, 2), 4, 8, 2, f32, cpu, "y")
+
+
+def test_binding_refuses_another_devices_stream(ssd):
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="stream"):
+        ssd.decode_slots(torch.zeros(1, 48), None, None, None, slots=None, tail_in=None, h_in=None, H=1, P=16, N=16, stream=Stream())
