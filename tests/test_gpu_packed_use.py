@@ -238,6 +238,48 @@ def test_captured_batch_replayed_with_other_offsets():
             assert torch.equal(got[n][a:b], t[a:b]), n
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("total", [130, 2400, 5000, 12000])
+def test_convolution_in_pieces_is_the_layers(total, dtype):
+    """Whatever pieces of a chunk a thread takes (8, 4, 2 and 1 at these sizes), each sequence gets the layer's
+    convolution bit for bit, and hands on its last rows."""
+    cch = 2304
+    lens = [total - total // 3 - 66, 1, 65, total // 3]
+    g = torch.Generator().manual_seed(65)
+    u = torch.randn(total, cch, generator=g).to(DEV, dtype)
+    w, bias = (torch.rand(cch, 4, generator=g) - 0.5).to(DEV), torch.randn(cch, generator=g).to(DEV)
+    tails = torch.randn(4, 3, cch, generator=g).to(DEV, dtype)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    cu = [0, lens[0], lens[0] + 1, lens[0] + 66, total]
+    plan = ssd.packed_plan(torch.tensor(cu, **i32), total, slots=torch.tensor([2, 0, 1, 3], **i32), resume=torch.tensor([1, 1, 0, 1], **i32), n_slots=4)
+    t = tails.clone()
+    v = ssd.packed_conv_forward(u, w, plan, bias, tail_in=t, tail_out=t)[0]
+    ssd.sync_status()
+    for i, (k, r) in enumerate(zip([2, 0, 1, 3], [1, 1, 0, 1])):
+        rows = u[None, cu[i]:cu[i + 1]]
+        tail = tails[k][None] if r else torch.zeros_like(tails[k])[None]
+        one = ssd.conv_forward(rows, w, bias, tail_in=tail)
+        one = one[0] if isinstance(one, tuple) else one
+        assert torch.equal(v[cu[i]:cu[i + 1]], one[0]), i
+        assert torch.equal(t[k], torch.cat((tail[0], rows[0]))[-3:]), i
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,d,group", [(700, 4096, 0), (601, 4096, 1024), (450, 5120, 0), (460, 5120, 1280), (301, 6144, 0), (310, 8192, 2048)])
+def test_norm_gradient_of_wide_rows(rows, d, group, dtype):
+    """Several rows per CTA at every number of threads a row can take."""
+    g = torch.Generator().manual_seed(66)
+    dout, y, z = (torch.randn(rows, d, generator=g).to(DEV, dtype) for _ in range(3))
+    w = (1 + 0.2 * torch.randn(d, generator=g)).to(DEV)
+    dy, dz, dw = ref.norm_grad(dout, y, z, w, 1e-5, group or d)
+    o = ssd.gated_rmsnorm_backward(dout, y, z, w, eps=1e-5, group_size=group)
+    ssd.sync_status()
+    assert ref.rel(o["dweight"], dw) <= 1e-5
+    for k, r in (("dy", dy), ("dz", dz)):
+        # one rounding of half a step of bf16 per element, in the 2-norm below its largest 2^-8
+        assert ref.rel(o[k], r) <= (1e-5 if dtype == torch.float32 else 2.0 ** -8), k
+
+
 def _child(backward):
     d = _data([700, 300], 4, 64, 128, 1, torch.bfloat16, 61)
     dy, dh = _grad_inputs(d, 62)
