@@ -590,21 +590,25 @@ packed_output_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParam
                     const float b_own = dvb[lane & 15] * ex2(cvb[lane & 15] - m16);     // <= dt for lane < 16
                     const int xo = lo ? 0 : 16;
 #pragma unroll
-                    for (int k2 = 0; k2 < 8; ++k2) {
-                        float vl[2], vh[2];
+                    for (int k4 = 0; k4 < 4; ++k4) {
+                        const float4 c4 = *reinterpret_cast<const float4 *>(cvb + xo + 4 * k4), d4 = *reinterpret_cast<const float4 *>(dvb + xo + 4 * k4);
+                        const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, dd[4] = {d4.x, d4.y, d4.z, d4.w};
+                        float vl[4], vh[4];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int kc = 2 * k2 + e;
+                        for (int e = 0; e < 4; ++e) {
+                            const int kc = 4 * k4 + e;
                             const int x = xo + kc;
                             const float g_x = __uint_as_float(lo ? gv[kc] : gv[16 + kc]);
-                            float t = g_x * ex2(cvb[x] - csr) * dvb[x];
+                            float t = g_x * ex2(cc[e] - csr) * dd[e];
                             t = x > lane ? 0.0f : t;
                             const float bk = __shfl_sync(0xffffffffu, b_own, kc);
                             vl[e] = lo ? t : __uint_as_float(gv[kc]) * (a_r * bk);
                             vh[e] = lo ? 0.0f : t;
                         }
-                        pk[k2] = pack_bf16x2(vl[0], vl[1]);
-                        pk[8 + k2] = pack_bf16x2(vh[0], vh[1]);
+                        pk[2 * k4] = pack_bf16x2(vl[0], vl[1]);
+                        pk[2 * k4 + 1] = pack_bf16x2(vl[2], vl[3]);
+                        pk[8 + 2 * k4] = pack_bf16x2(vh[0], vh[1]);
+                        pk[9 + 2 * k4] = pack_bf16x2(vh[2], vh[3]);
                     }
                 } else {
 #pragma unroll
