@@ -95,11 +95,13 @@ ScanPlan scan_plan(int nseq, int64_t total, int64_t longest, int H, int P, int N
     // a sequence is handed on between windows only if it has more than one chunk
     s.carry = std::min<int64_t>(longest, total) > (s.tc ? 128 : 64);
     int64_t best = -1;
-    // (beyond four waves a window more changes nothing)
-    const int64_t most = std::min<int64_t>(chunks, std::max<int64_t>(4, 4 * slots / units));
-    for (int64_t nw = 1; nw <= most; ++nw) {
-        const int64_t per = (chunks + nw - 1) / nw, waves = (nw * units + slots - 1) / slots;
-        const int64_t cost = waves * (per + 2);
+    // (beyond four waves a window more changes nothing; chunks and windows x units fit 32 bits, whose quotients are the
+    // cheaper ones: this runs in every call)
+    const uint32_t nc = (uint32_t)chunks, un = (uint32_t)units, sl = (uint32_t)slots;
+    const uint32_t most = (uint32_t)std::min<int64_t>(chunks, std::max<int64_t>(4, 4 * slots / units));
+    for (uint32_t nw = 1; nw <= most; ++nw) {
+        const uint32_t per = (nc + nw - 1) / nw, waves = (nw * un + sl - 1) / sl;
+        const int64_t cost = (int64_t)waves * (per + 2);
         if (best < 0 || cost < best) { best = cost; s.nw = (int)nw; }
     }
     if (s.carry) {

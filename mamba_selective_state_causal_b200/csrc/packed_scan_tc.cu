@@ -1047,15 +1047,16 @@ int launch_packed_scan_tc(const PackedScanParams &p, bool carry, cudaStream_t st
     if (!enc) return 7;
     Maps maps{};
     const int64_t gn = (int64_t)p.G * p.N, hp = (int64_t)p.H * p.P, rows = p.plan.total > 0 ? p.plan.total : 1;
+    const bool hand_on = carry && p.nw > 1;
     if (p.plan.total > 0 &&
         (!encode_bf16(enc, &maps.x, p.x, hp, rows, 1, p.xrs, 0) || !encode_bf16(enc, &maps.B, p.B, gn, rows, 1, p.Brs, 0) ||
-         !encode_bf16(enc, &maps.x64, p.x, hp, rows, 1, p.xrs, 0, kQA) || !encode_bf16(enc, &maps.B64, p.B, gn, rows, 1, p.Brs, 0, kQA) ||
+         (hand_on && (!encode_bf16(enc, &maps.x64, p.x, hp, rows, 1, p.xrs, 0, kQA) || !encode_bf16(enc, &maps.B64, p.B, gn, rows, 1, p.Brs, 0, kQA))) ||
          !encode_bf16(enc, &maps.C, p.C, gn, rows, 1, p.Crs, 0) || !encode_bf16(enc, &maps.y, p.y, hp, rows, 1, p.yrs, 0)))
         return 6;
     static std::atomic<int> done_a[64], done_c[64];
     if (!allow_smem(packed_state_tc_kernel, (int)kSmemA, done_a) || !allow_smem(packed_output_tc_kernel, (int)kSmemC, done_c)) return 7;
     const unsigned units = (unsigned)p.nw * (unsigned)(p.H / 2);
-    if (carry && p.nw > 1) {
+    if (hand_on) {
         prof_begin(st, kKPackedState);
         packed_state_tc_kernel<<<units, kThreadsA, kSmemA, st>>>(maps, p);
         prof_end(st, kKPackedState);
