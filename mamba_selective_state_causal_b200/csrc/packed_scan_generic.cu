@@ -53,14 +53,17 @@ __device__ __forceinline__ void zero(float (&acc)[4][4])
         for (int c = 0; c < 4; ++c) acc[r][c] = 0.0f;
 }
 
-// rows of cols elements into shared memory (row stride cols + 1), zeros past the chunk's rows; cols is a
-// multiple of 16 and rows are 16-byte aligned
+// rows in use of a chunk's tiles: the products take rows four at a time
+__device__ __forceinline__ int tile_rows(int rows) { return (rows + 3) & ~3; }
+
+// rows of cols elements into shared memory (row stride cols + 1), zeros past the chunk's rows up to tile_rows; cols is
+// a multiple of 16 and rows are 16-byte aligned
 template <typename T>
 __device__ __forceinline__ void load_tile(float *dst, const T *src, int64_t rs, int rows, int cols)
 {
     constexpr int V = 16 / (int)sizeof(T);
     const int nv = cols / V;
-    for (int i = threadIdx.x; i < kQ * nv; i += kThr) {
+    for (int i = threadIdx.x; i < tile_rows(rows) * nv; i += kThr) {
         const int r = i / nv, c = i % nv * V;
         float *d = dst + r * (cols + 1) + c;
         if (r < rows) {
@@ -107,15 +110,15 @@ __device__ __forceinline__ void load_dt(const PackedScanParams &p, int row0, int
     for (int k = 0; k < 2; ++k) { dts[2 * lane + k] = d[k]; cs[2 * lane + k] = ex + s[k]; }
 }
 
-// h = e^{cs_last} h + sum_j (w o x)_j B_j^T for the chunk in xs (already weighted) and bs
-__device__ __forceinline__ void add_state(float *hs, const float *xw, const float *bs, int P, int N, float dec)
+// h = e^{cs_last} h + sum_j (w o x)_j B_j^T for the chunk's rows in xs (already weighted) and bs
+__device__ __forceinline__ void add_state(float *hs, const float *xw, const float *bs, int rows, int P, int N, float dec)
 {
     const int ct = N / 4;
     for (int tile = threadIdx.x; tile < (P / 4) * ct; tile += kThr) {
         const int p0 = (tile / ct) * 4, n0 = tile % ct;
         float acc[4][4];
         zero(acc);
-        mm(acc, xw, 1, P + 1, bs, N + 1, 1, kQ, p0, 1, n0, ct);
+        mm(acc, xw, 1, P + 1, bs, N + 1, 1, rows, p0, 1, n0, ct);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -158,12 +161,12 @@ __global__ void __launch_bounds__(kThr, 2) packed_state_kernel(PackedScanParams 
         __syncthreads();
         const float tot = cs[kQ - 1];
         dA += tot;
-        for (int i = threadIdx.x; i < kQ * P; i += kThr) {
+        for (int i = threadIdx.x; i < rows * P; i += kThr) {
             const int j = i / P;
             xs[j * (P + 1) + i % P] *= dts[j] * expf(tot - cs[j]);
         }
         __syncthreads();
-        add_state(hs, xs, bs, P, N, expf(tot));
+        add_state(hs, xs, bs, rows, P, N, expf(tot));
     }
     __syncthreads();
     float *dst = p.ws_S + ((int64_t)k * p.H + h) * P * N;
@@ -205,8 +208,8 @@ __global__ void __launch_bounds__(kThr) packed_output_kernel(PackedScanParams p)
             }
         }
         __syncthreads();
-        // M[i][j] = e^{cs_i - cs_j} dt_j (C_i . B_j), j <= i
-        for (int tile = threadIdx.x; tile < (kQ / 4) * ctn; tile += kThr) {
+        // M[i][j] = e^{cs_i - cs_j} dt_j (C_i . B_j), j <= i  (columns past the rows in use hold whatever lay there: masked)
+        for (int tile = threadIdx.x; tile < (tile_rows(rows) / 4) * ctn; tile += kThr) {
             const int i0 = (tile / ctn) * 4, j0 = tile % ctn;
             float acc[4][4];
             zero(acc);
@@ -222,7 +225,7 @@ __global__ void __launch_bounds__(kThr) packed_output_kernel(PackedScanParams p)
         __syncthreads();
         const float tot = cs[kQ - 1];
         T *yb = reinterpret_cast<T *>(p.y) + (int64_t)d.x * p.yrs + (int64_t)h * P;
-        for (int tile = threadIdx.x; tile < (kQ / 4) * ctp; tile += kThr) {
+        for (int tile = threadIdx.x; tile < (tile_rows(rows) / 4) * ctp; tile += kThr) {
             const int i0 = (tile / ctp) * 4, p0 = tile % ctp;
             float a1[4][4], a2[4][4];
             zero(a1);
@@ -244,12 +247,12 @@ __global__ void __launch_bounds__(kThr) packed_output_kernel(PackedScanParams p)
             }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < kQ * P; i += kThr) {
+        for (int i = threadIdx.x; i < rows * P; i += kThr) {
             const int j = i / P;
             xs[j * (P + 1) + i % P] *= dts[j] * expf(tot - cs[j]);
         }
         __syncthreads();
-        add_state(hs, xs, bs, P, N, expf(tot));
+        add_state(hs, xs, bs, rows, P, N, expf(tot));
         if ((d.y & kChunkLast) && p.h_out && d.w >= 0) {
             __syncthreads();
             float *dst = p.h_out + ((int64_t)d.w * p.H + h) * PN;
