@@ -114,12 +114,13 @@ __device__ __forceinline__ void zero4x4(float (&acc)[4][4])
         for (int c = 0; c < 4; ++c) acc[r][c] = 0.0f;
 }
 
-// chunk-local inclusive cumsum of dt*A (serial, deterministic)
-__device__ __forceinline__ void chunk_cumsum(const float *dts, float *cum, float A)
+// chunk-local inclusive cumsum of dt*A (serial, deterministic); the rows from n on have no dt
+__device__ __forceinline__ void chunk_cumsum(const float *dts, float *cum, float A, int n = kQb)
 {
     if (threadIdx.x == 0) {
         float acc = 0.0f;
-        for (int i = 0; i < kQb; ++i) { acc = fmaf(dts[i], A, acc); cum[i] = acc; }
+        for (int i = 0; i < n; ++i) { acc = fmaf(dts[i], A, acc); cum[i] = acc; }
+        for (int i = n; i < kQb; ++i) cum[i] = acc;
     }
 }
 
@@ -296,6 +297,7 @@ __global__ void __launch_bounds__(kBwdThreads) bwd_chunk_summary_kernel(BwdParam
     int64_t t0;
     int rows;
     if (!bwd_chunk<kPacked>(p, c, t0, rows)) return;
+    const int kr = kPacked ? rows : kQb;      // rows that the sums take (packed: many chunks are short)
     float *xs = sm;                 // [Qb][P1]  dt_j e^{lam-cs_j} x_j
     float *gs = xs + kQb * P1;      // [Qb][P1]  e^{cs_t} dy_t
     float *bs = gs + kQb * P1;      // [Qb][N1]
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__(kBwdThreads) bwd_chunk_summary_kernel(BwdParam
     for (int i = threadIdx.x; i < kQb; i += blockDim.x)
         dts[i] = i < rows ? p.dt[((int64_t)bi * p.L + t0 + i) * p.H + h] : 0.0f;
     __syncthreads();
-    chunk_cumsum(dts, cum, p.A[h]);
+    chunk_cumsum(dts, cum, p.A[h], kr);
     __syncthreads();
     const float lam = cum[kQb - 1];
     for (int i = threadIdx.x; i < kQb; i += blockDim.x) {
@@ -337,13 +339,13 @@ __global__ void __launch_bounds__(kBwdThreads) bwd_chunk_summary_kernel(BwdParam
         const int p0 = (tile / ct) * 4, n0 = tile % ct;
         float acc[4][4];
         zero4x4(acc);
-        mm4x4(acc, xs, 1, P1, bs, N1, 1, kQb, p0, 1, n0, ct);
+        mm4x4(acc, xs, 1, P1, bs, N1, 1, kr, p0, 1, n0, ct);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int c = 0; c < 4; ++c) S[(int64_t)(p0 + r) * N + n0 + c * ct] = acc[r][c];
         zero4x4(acc);
-        mm4x4(acc, gs, 1, P1, cs, N1, 1, kQb, p0, 1, n0, ct);
+        mm4x4(acc, gs, 1, P1, cs, N1, 1, kr, p0, 1, n0, ct);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -498,6 +500,7 @@ __global__ void __launch_bounds__(kGradThreads) bwd_chunk_grad_kernel(BwdParams 
     int64_t t0;
     int rows;
     if (!bwd_chunk<kPacked>(p, c, t0, rows)) return;
+    const int kr = kPacked ? rows : kQb;      // rows that are formed and summed
     const int tid = threadIdx.x;
     float *xs = sm;                  // [Qb][P1]
     float *gs = xs + kQb * P1;       // [Qb][P1] dy
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(kGradThreads) bwd_chunk_grad_kernel(BwdParams 
         }
     }
     __syncthreads();
-    chunk_cumsum(dts, cum, Ah);
+    chunk_cumsum(dts, cum, Ah, kr);
     // <Gam, h_prev>, reduced in a fixed order
     float part = 0.0f;
     for (int64_t i = tid; i < (int64_t)P * N; i += blockDim.x) part = fmaf(Gam[i], hprev[i], part);
@@ -564,6 +567,7 @@ __global__ void __launch_bounds__(kGradThreads) bwd_chunk_grad_kernel(BwdParams 
         const int tile = half ? w % half : w;
         if (tile >= kQt * kQt) continue;
         const int r0 = (tile / kQt) * 4, c0 = tile % kQt;
+        if (kPacked && r0 >= kr) continue;
         float acc[4][4];
         if (do_cb) {
             zero4x4(acc);
@@ -587,7 +591,7 @@ __global__ void __launch_bounds__(kGradThreads) bwd_chunk_grad_kernel(BwdParams 
     for (int w = 0; w < (int)(blockDim.x >> 5); ++w) gam_h += misc[w];
     const float term3 = expf(lam) * gam_h;
     // K (strictly below the diagonal), then CB and GX masked and decayed in place
-    for (int i = tid; i < kQb * kQb; i += blockDim.x) {
+    for (int i = tid; i < kr * kQb; i += blockDim.x) {
         const int t = i / kQb, j = i % kQb;
         float kv = 0.0f, cb = 0.0f, gx = 0.0f;
         if (j <= t) {
@@ -604,13 +608,13 @@ __global__ void __launch_bounds__(kGradThreads) bwd_chunk_grad_kernel(BwdParams 
     // dD of this chunk: the diagonal of GX (decay 1 there)
     if (tid == kQb) {
         float sD = 0.0f;
-        for (int t = 0; t < kQb; ++t) sD += GX[t * kQ1 + t];
+        for (int t = 0; t < kr; ++t) sD += GX[t * kQ1 + t];
         p.ws_pD[unit] = sD;
     }
     // row-exclusive prefix sums of K: KK[t][u] := sum_{j<u} K[t][j]
     if (tid < kQb) {
         float run = 0.0f;
-        for (int u = 0; u < kQb; ++u) {
+        for (int u = 0; u < kr; ++u) {
             const float v = KK[tid * kQ1 + u];
             KK[tid * kQ1 + u] = run;
             run += v;
@@ -619,12 +623,12 @@ __global__ void __launch_bounds__(kGradThreads) bwd_chunk_grad_kernel(BwdParams 
     __syncthreads();
     if (tid < kQb) {
         float s = 0.0f;
-        for (int t = tid; t < kQb; ++t) s += KK[t * kQ1 + tid];
+        for (int t = tid; t < kr; ++t) s += KK[t * kQ1 + tid];
         rr[tid] = s;
     }
     __syncthreads();
     // KK := GX * dt_j, the weights of dC's intra-chunk term
-    for (int i = tid; i < kQb * kQb; i += blockDim.x) {
+    for (int i = tid; i < kr * kQb; i += blockDim.x) {
         const int t = i / kQb, j = i % kQb;
         KK[t * kQ1 + j] = GX[t * kQ1 + j] * dts[j];
     }
@@ -639,7 +643,7 @@ __global__ void __launch_bounds__(kGradThreads) bwd_chunk_grad_kernel(BwdParams 
             float a1[4][4], a2[4][4];
             zero4x4(a1);
             zero4x4(a2);
-            mm4x4(a1, CB, 1, kQ1, gs, P1, 1, kQb, j0, kQt, p0, 1);
+            mm4x4(a1, CB, 1, kQ1, gs, P1, 1, kr, j0, kQt, p0, 1);
             mm4x4(a2, bs, N1, 1, Gam, 1, N, N, j0, kQt, p0, 1);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -662,10 +666,11 @@ __global__ void __launch_bounds__(kGradThreads) bwd_chunk_grad_kernel(BwdParams 
     const int ctn = N / 4;
     for (int tile = tid; tile < (kQb / 4) * ctn; tile += blockDim.x) {
         const int j0 = (tile / ctn) * 4, nt = tile % ctn;    // columns nt + q * ctn
+        if (kPacked && j0 >= kr) break;
         float a1[4][4], a2[4][4];
         zero4x4(a1);
         zero4x4(a2);
-        mm4x4(a1, GX, 1, kQ1, cs, N1, 1, kQb, j0, 1, nt, ctn);
+        mm4x4(a1, GX, 1, kQ1, cs, N1, 1, kr, j0, 1, nt, ctn);
         mm4x4(a2, xs, P1, 1, Gam, N, 1, P, j0, 1, nt, ctn);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -699,11 +704,12 @@ __global__ void __launch_bounds__(kGradThreads) bwd_chunk_grad_kernel(BwdParams 
     // dC[t][n] = ecs_t sum_p dy_t[p] h_prev[p][n] + sum_j GX[t][j] dt_j B_j[n]
     for (int tile = tid; tile < (kQb / 4) * ctn; tile += blockDim.x) {
         const int r0 = (tile / ctn) * 4, nt = tile % ctn;    // columns nt + q * ctn
+        if (kPacked && r0 >= kr) break;
         float a1[4][4], a2[4][4];
         zero4x4(a1);
         zero4x4(a2);
         mm4x4(a1, gs, P1, 1, hprev, N, 1, P, r0, 1, nt, ctn);
-        mm4x4(a2, KK, kQ1, 1, bs, N1, 1, kQb, r0, 1, nt, ctn);
+        mm4x4(a2, KK, kQ1, 1, bs, N1, 1, kr, r0, 1, nt, ctn);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int t = r0 + r;
@@ -729,7 +735,7 @@ __global__ void __launch_bounds__(kGradThreads) bwd_chunk_grad_kernel(BwdParams 
     if (tid < kQb) {
         const int t = tid;
         float suf = 0.0f, pre = 0.0f;
-        for (int u = t; u < kQb; ++u) suf += al[u];
+        for (int u = t; u < kr; ++u) suf += al[u];
         for (int j = 0; j < t; ++j) pre += be[j];
         const float dl = suf + rr[t] + term3 + pre;
         if (t < rows) p.ddt[((int64_t)bi * p.L + t0 + t) * p.H + h] = fmaf(Ah, dl, din[t]);
@@ -738,7 +744,7 @@ __global__ void __launch_bounds__(kGradThreads) bwd_chunk_grad_kernel(BwdParams 
     __syncthreads();
     if (tid == 0) {
         float sA = 0.0f;
-        for (int t = 0; t < kQb; ++t) sA += misc[t];
+        for (int t = 0; t < kr; ++t) sA += misc[t];
         p.ws_pA[unit] = sA;
     }
 }
