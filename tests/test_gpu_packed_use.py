@@ -238,6 +238,61 @@ def test_captured_batch_replayed_with_other_offsets():
             assert torch.equal(got[n][a:b], t[a:b]), n
 
 
+@pytest.mark.parametrize("dtype,P,N", [(torch.bfloat16, 64, 128), (torch.float32, 32, 16)])
+def test_rows_far_apart(dtype, P, N):
+    """Rows whose offsets pass 32 bits (views of a buffer of 2.2e9 elements) give what rows side by side give."""
+    d = _data([200, 31, 65], 2, P, N, 1, dtype, 67)
+    total, cch, far = d["total"], 2 * P + 2 * N, 7_400_000
+    assert (total - 1) * far > 1 << 31
+    dy, dh = _grad_inputs(d, 68)
+    wide = torch.empty(total, far, dtype=dtype, device=DEV)
+    v, dyw, yw = wide[:, :cch], wide[:, 4096:4096 + 2 * P], wide[:, 8192:8192 + 2 * P].unflatten(1, (2, P))
+    v.copy_(d["v"])
+    dyw.copy_(dy)
+    plan = _plan(d)
+    dt, A, D, h0, dh = (t.to(DEV) for t in (d["dt"], d["A"], d["D"], d["h"], dh))
+    got = []
+    for src, g, y in ((d["v"].to(DEV), dy.to(DEV), None), (v, dyw, yw)):
+        x, B, C = _parts(d, src)
+        y, h = ssd.packed_scan_forward(x, B, C, dt, A, D, plan=plan, H=2, h_in=h0, h_out=h0.clone(), y=y)
+        o = ssd.packed_scan_backward(x, B, C, dt, A, D, g, plan=plan, H=2, h_in=h0, dh_out=dh)
+        w = torch.linspace(-0.5, 0.5, cch * 4, device=DEV).view(cch, 4)
+        c = ssd.packed_conv_forward(src, w, plan)[0]
+        e = ssd.packed_conv_backward(src, w, plan, o["dx"], o["dB"], o["dC"])
+        got.append({"y": y, "h": h, "v": c, **{"s" + k: t for k, t in o.items()}, **{"c" + k: t for k, t in e.items()}})
+    ssd.sync_status()
+    for k, t in got[0].items():
+        assert t is None or torch.equal(got[1][k], t), k
+
+
+def test_slots_far_into_a_large_pool():
+    """States past 2^31 elements of their pool (8.8 GB): prompts, their gradients and a token give what a small pool gives."""
+    H, P, N, many = 64, 64, 128, 4200
+    assert (many - 1) * H * P * N > 1 << 31
+    d = _data([130, 20], H, P, N, 1, torch.bfloat16, 69, slots=[0, 1], n_slots=2)
+    cch, g = H * P + 2 * N, torch.Generator().manual_seed(70)
+    dy, dh = _grad_inputs(d, 71)
+    x, B, C = _parts(d, d["v"].to(DEV))
+    dt, A, D, h0, dy, dh = (t.to(DEV) for t in (d["dt"], d["A"], d["D"], d["h"], dy, dh))
+    u, w = torch.randn(2, cch, generator=g).to(DEV, torch.bfloat16), (torch.rand(cch, 4, generator=g) - 0.5).to(DEV)
+    tails = torch.randn(2, 3, cch, generator=g).to(DEV, torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    cu, got = torch.tensor(d["cu"], **i32), []
+    for n, ks in ((2, [0, 1]), (many, [many - 1, many - 2])):
+        slots = torch.tensor(ks, **i32)
+        pool, tp = torch.empty(n, H, P, N, device=DEV), torch.empty(n, 3, cch, dtype=torch.bfloat16, device=DEV)
+        pool[slots.long()], tp[slots.long()] = h0, tails
+        plan = ssd.packed_plan(cu, d["total"], slots=slots, n_slots=n)
+        o = ssd.packed_scan_backward(x, B, C, dt, A, D, dy, plan=plan, H=H, h_in=pool, dh_out=dh)
+        y, _ = ssd.packed_scan_forward(x, B, C, dt, A, D, plan=plan, H=H, h_in=pool, h_out=pool)
+        s = ssd.decode_slots(u, w, dt[:2].contiguous(), A, D, slots=slots, H=H, P=P, N=N, tail_in=tp, h_in=pool)
+        got.append({"y": y, "t": s["y"], "h": pool[slots.long()], "tail": tp[slots.long()], **o})
+        del pool
+    ssd.sync_status()
+    for k, t in got[0].items():
+        assert torch.equal(got[1][k], t), k
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("total", [130, 2400, 5000, 12000])
 def test_convolution_in_pieces_is_the_layers(total, dtype):
