@@ -265,6 +265,28 @@ def test_rows_far_apart(dtype, P, N):
         assert t is None or torch.equal(got[1][k], t), k
 
 
+@pytest.mark.parametrize("dtype,P,N,H", [(torch.bfloat16, 64, 128, 4), (torch.bfloat16, 64, 128, 16), (torch.float32, 32, 16, 2)])
+def test_what_may_be_left_out(dtype, P, N, H):
+    """Without D, start states and the states' gradients: as with zeros.  A slot that a sequence does not resume from is not
+    read, whatever it holds."""
+    lens = [1100, 70]
+    d = _data(lens, H, P, N, 1, dtype, 72, resume=[0, 0], n_slots=2)
+    dy, dh = _grad_inputs(d, 73)
+    plan = _plan(d)
+    x, B, C = _parts(d, d["v"].to(DEV))
+    dt, A, dy = d["dt"].to(DEV), d["A"].to(DEV), dy.to(DEV)
+    none = ssd.packed_scan_backward(x, B, C, dt, A, None, dy, plan=plan, H=H)
+    y0, _ = ssd.packed_scan_forward(x, B, C, dt, A, None, plan=plan, H=H)
+    bad = torch.full((2, H, P, N), float("nan"), device=DEV)
+    zero = ssd.packed_scan_backward(x, B, C, dt, A, torch.zeros(H, device=DEV), dy, plan=plan, H=H, h_in=bad, dh_out=torch.zeros_like(bad))
+    y1, h = ssd.packed_scan_forward(x, B, C, dt, A, torch.zeros(H, device=DEV), plan=plan, H=H, h_in=bad, h_out=bad)
+    ssd.sync_status()
+    assert torch.equal(y0, y1) and torch.isfinite(h).all()
+    for k in ("dx", "dB", "dC", "ddt", "dA"):
+        assert torch.equal(none[k], zero[k]), k
+    assert (zero["dh_in"] == 0).all()
+
+
 def test_slots_far_into_a_large_pool():
     """States past 2^31 elements of their pool (8.8 GB): prompts, their gradients and a token give what a small pool gives."""
     H, P, N, many = 64, 64, 128, 4200
