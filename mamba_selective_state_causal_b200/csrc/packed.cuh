@@ -5,8 +5,9 @@
 // and layer that works on the same batch: a header, one PackedSeq per sequence, and the
 // sequences cut into chunks of 64 and of 128 rows.  A chunk never crosses a sequence, its rows are
 // consecutive, and the chunks of a sequence follow one another, so that a kernel which takes
-// chunks in order takes the sequences one after the other.  An empty sequence has one chunk of
-// no rows (its state still moves from h_in to h_out); one whose offsets are refused has none.
+// chunks in order takes the sequences one after the other.  An empty sequence with a slot has one chunk
+// of no rows (its state still moves from h_in to h_out); one without (a batch padded to a number of
+// sequences) has none, nor has one whose offsets are refused.
 #pragma once
 
 #include <atomic>

@@ -435,6 +435,12 @@ __global__ void __launch_bounds__(32 * kRedWarps) packed_conv_reduce_kernel(Pack
     sw[sl][cl] = acc;
     sb[sl][cl] = ab;
     __syncthreads();
+    if (p.dtail_in && c < p.C_ch && packed_ok(p.plan, p.status)) {
+        // sequences without chunks start from no buffer
+        for (int q = sl; q < p.plan.nseq; q += kRedWarps)
+            if (p.plan.seqs[q].n64 == 0)
+                for (int r = 0; r < 3; ++r) p.dtail_in[((int64_t)q * 3 + r) * p.C_ch + c] = 0.0f;
+    }
     if (sl == 0 && c < p.C_ch) {
         for (int k = 1; k < kRedWarps; ++k) {
             const float4 v = sw[k][cl];

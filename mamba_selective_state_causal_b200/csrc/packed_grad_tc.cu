@@ -1161,7 +1161,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
 
 // =============================================================== sums
 // The first kSumParts x units blocks: dB and dC of a (chunk, group) whose heads make several blocks, in their order; the H blocks
-// behind them: dA and dD of a head, in a fixed order.
+// behind them: dA and dD of a head, in a fixed order; the blocks behind those: dh_in of a sequence without chunks.
 constexpr int kSumParts = 4;        // blocks to a unit
 
 __global__ void __launch_bounds__(256) packed_grad_sum_kernel(const PackedGradParams p, int ctas)
@@ -1189,6 +1189,14 @@ __global__ void __launch_bounds__(256) packed_grad_sum_kernel(const PackedGradPa
             reinterpret_cast<float4 *>(p.dB + o)[n4] = sb;
             reinterpret_cast<float4 *>(p.dC + o)[n4] = sc;
         }
+        return;
+    }
+    if (blockIdx.x >= kSumParts * units + p.H) {
+        // a sequence without chunks starts from no state
+        const int64_t q = blockIdx.x - kSumParts * units - p.H;
+        if (!p.dh_in || !packed_ok(p.plan, p.status) || p.plan.seqs[q].n64 != 0) return;
+        float4 *dst = reinterpret_cast<float4 *>(p.dh_in + q * p.H * kPN);
+        for (int64_t i = threadIdx.x; i < (int64_t)p.H * (kPN / 4); i += blockDim.x) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         return;
     }
     __shared__ float sa[256], sd[256];
@@ -1242,7 +1250,7 @@ static int launch_parts(const PackedGradParams &p, int ctas, cudaStream_t st)
     // parts of the chunk list: two waves of one CTA per SM, no more parts than sequences (they begin between sequences)
     const int64_t wide = 2 * (int64_t)p.H;
     const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(p.plan.nseq, (2 * (int64_t)ctas + wide - 1) / wide));
-    const int64_t units = kSumParts * p.plan.m64 * p.G + p.H;
+    const int64_t units = kSumParts * p.plan.m64 * p.G + p.H + p.plan.nseq;
     if (units > 0x7fffffff) return 2;
     prof_begin(st, kKBwdChain);
     packed_grad_walk_kernel<kParts><<<dim3((unsigned)wide, (unsigned)parts), kWalkThreads, sizeof(SmemWalk<kParts>), st>>>(p);

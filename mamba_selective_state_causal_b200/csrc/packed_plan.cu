@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_seq_kernel(PackedPlanPara
             }
             s.resume = p.resume ? (p.resume[i] != 0) : 1;
             if (s.slot < 0) s.resume = 0;
-            if (fits) {
+            if (fits && (s.len > 0 || s.slot >= 0)) {       // (nothing to do for one of no rows that is kept nowhere)
                 s.n64 = max(1, (s.len + 63) / 64);
                 s.n128 = max(1, (s.len + 127) / 128);
             }
@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(kPlanThreads) packed_seq_kernel(PackedPlanPara
     }
 }
 
-// chunk k of Q rows: its sequence is the last one whose first chunk is at or before k (a refused
-// sequence has no chunks and shares its first with the next, so it is never the last one)
+// chunk k of Q rows: its sequence is the last one whose first chunk is at or before k (a sequence
+// without chunks shares its first with the next, so it is never the last one)
 template <int Q>
 __device__ __forceinline__ void write_chunk(const PackedPlan &p, int k, int n, int4 *out)
 {

@@ -448,7 +448,10 @@ __global__ void __launch_bounds__(kBwdThreads) bwd_adjoint_chain_kernel(BwdParam
     const int64_t k = blockIdx.x / slices;
     const int64_t lo = kPacked ? p.seqs[k].c64 : 0;
     const int64_t hi = kPacked ? lo + p.seqs[k].n64 : p.nch;
-    if (kPacked && hi == lo) return;      // a refused sequence
+    if (kPacked && hi == lo) {            // a sequence without chunks starts from no state
+        if (p.dh0) *reinterpret_cast<float4 *>(p.dh0 + (k * p.H + h) * PN + e) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        return;
+    }
     const int64_t su = kPacked ? k * p.H + h : hu;
     float4 gv = p.dh_final ? *reinterpret_cast<const float4 *>(p.dh_final + su * PN + e)
                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);

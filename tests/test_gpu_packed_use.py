@@ -287,6 +287,43 @@ def test_what_may_be_left_out(dtype, P, N, H):
     assert (zero["dh_in"] == 0).all()
 
 
+@pytest.mark.parametrize("dtype,P,N,H", [(torch.bfloat16, 64, 128, 4), (torch.float32, 32, 16, 2)])
+def test_batch_padded_with_empty_sequences(dtype, P, N, H):
+    """Empty sequences without a slot change nothing of the others, and their states' and buffers' gradients are zero."""
+    lens, cch = [100, 0, 0, 300, 0, 30, 0, 0, 0], H * P + 2 * N
+    slots, resume = [2, -1, -1, 0, 3, 1, -1, -1, -1], [1, 1, 0, 1, 1, 0, 1, 1, 1]
+    on = [i for i, m in enumerate(lens) if m]
+    d = _data(lens, H, P, N, 1, dtype, 74, slots=slots, resume=resume, n_slots=4)
+    dy, dh = _grad_inputs(d, 75)
+    bare = dict(d, cu=[0, 100, 400, 430], slots=[2, 0, 1], resume=[1, 1, 0])
+    g = torch.Generator().manual_seed(76)
+    w, bias = (torch.rand(cch, 4, generator=g) - 0.5).to(DEV), torch.randn(cch, generator=g).to(DEV)
+    tails = torch.randn(4, 3, cch, generator=g).to(DEV, dtype)
+    got = []
+    for e, dhe in ((d, dh), (bare, dh[on])):
+        plan, n = _plan(e), len(e["slots"])
+        y, h = _run(e, plan=plan, h_in=d["h"].to(DEV), h_out=d["h"].to(DEV))
+        out = {"dh_in": torch.full((n, H, P, N), float("nan"), device=DEV)}
+        o = _grads(e, dy, dhe, plan, out=out)
+        u = d["v"].to(DEV)
+        v, t = ssd.packed_conv_forward(u, w, plan, bias, tail_in=tails, tail_out=tails.clone())
+        c = ssd.packed_conv_backward(u, w, plan, o["dx"], o["dB"], o["dC"], bias=bias, tail_in=tails,
+                                     out={"dtail_in": torch.full((n, 3, cch), float("nan"), device=DEV)})
+        got.append({"y": y, "h": h, "v": v, "t": t, **{"s" + k: x for k, x in o.items()}, **{"c" + k: x for k, x in c.items() if x is not None}})
+    ssd.sync_status()
+    for k, x in got[1].items():
+        z = got[0][k]
+        if k in ("sdh_in", "cdtail_in"):
+            rest = [i for i in range(len(lens)) if i not in on and slots[i] < 0]
+            assert (z[rest] == 0).all() and torch.isfinite(z).all(), k
+            z = z[on]
+        if k in ("y", "h", "sdA", "sdD", "cdconv_w", "cdconv_bias"):
+            # (windows and partial sums are cut elsewhere)
+            assert ref.rel(z.float(), x.float()) <= (1e-5 if z.dtype == torch.float32 else 2.0 ** -8), k
+        else:
+            assert ref.rel(z.float(), x.float()) <= 1e-5, k
+
+
 def test_slots_far_into_a_large_pool():
     """States past 2^31 elements of their pool (8.8 GB): prompts, their gradients and a token give what a small pool gives."""
     H, P, N, many = 64, 64, 128, 4200
