@@ -442,8 +442,9 @@ SSD_API int ssd_gated_rmsnorm_forward(const void *y, int64_t y_row_stride, const
  * back to the host, so the call can be captured, and replayed with other contents of the
  * same buffers.
  *   cu_seqlens [nseq + 1] int32, not decreasing, within 0 .. total; rows outside
- *              [cu_seqlens[0], cu_seqlens[nseq]) belong to no sequence and are neither read
- *              nor written by any packed call.  A sequence may be empty.
+ *              [cu_seqlens[0], cu_seqlens[nseq]) belong to no sequence: whatever they hold
+ *              changes nothing, and no packed call writes them.  A sequence may be empty (one
+ *              with slot -1, as in a batch padded to a number of sequences, costs nothing).
  *   slots      [nseq] int32 or NULL (sequence i has slot i): 0 .. n_slots-1, or -1: the
  *              sequence starts from zero and its state is not kept.  At most 16384
  *              sequences when given.
@@ -587,7 +588,8 @@ SSD_API size_t ssd_packed_scan_workspace_size(int nseq, int64_t total, int64_t m
  *   dh_out [nseq][H][P][N] float or NULL: dLoss/d(h_out), by SEQUENCE, not by slot
  * Outputs, float, contiguous: dx [total][H][P]; dB, dC [total][G][N]; ddt [total][H] (rows of
  * no sequence stay as they were); dA [H]; dD [H] or NULL; dh_in [nseq][H][P][N] or NULL
- * (zero for a sequence that does not resume).  Sums are in a fixed order.
+ * (zero for a sequence that does not resume, or that the plan left out).  Sums are in a fixed
+ * order.
  */
 typedef struct ssd_packed_scan_bwd_args {
     int dtype;
