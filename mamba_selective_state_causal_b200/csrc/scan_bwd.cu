@@ -51,13 +51,16 @@ constexpr int kBwdThreads = 256;
 constexpr int kGradThreads = 512; // the gradient kernel: 16 warps per SM hide its load latency
 constexpr int kQ1 = kQb + 1;      // padded row of the chunk x chunk matrices
 
-// Chunks in use of a packed batch (0 when the plan is not of the call's sizes: nothing is done)
-__device__ __forceinline__ int bwd_packed_chunks(const BwdParams &p)
+// The plan of a packed batch, as far as packed_ok and packed_n64 look at it
+__device__ __forceinline__ PackedPlan bwd_packed_view(const BwdParams &p)
 {
     PackedPlan v{};
     v.hdr = p.hdr; v.nseq = p.nseq; v.total = p.L; v.max_len = -1;
-    return packed_n64(v, p.status);
+    return v;
 }
+
+// Chunks in use of a packed batch (0 when the plan is not of the call's sizes: nothing is done)
+__device__ __forceinline__ int bwd_packed_chunks(const BwdParams &p) { return packed_n64(bwd_packed_view(p), p.status); }
 
 // Rows t0 .. t0 + rows - 1 of chunk c; false for a chunk that a packed batch (kPacked) does not use
 template <bool kPacked>
@@ -441,7 +444,8 @@ __global__ void __launch_bounds__(kBwdThreads) bwd_adjoint_chain_kernel(BwdParam
     const int slices = (int)((PN + 4 * kBwdThreads - 1) / (4 * kBwdThreads));
     const int sl = kPacked ? blockIdx.x % slices : blockIdx.x, h = blockIdx.y, bi = blockIdx.z;
     const int64_t e = (int64_t)sl * 4 * kBwdThreads + 4 * threadIdx.x;
-    if (kPacked && bwd_packed_chunks(p) == 0) return;
+    // (a batch without a chunk goes on: dh0 of its sequences is zero)
+    if (kPacked && !packed_ok(bwd_packed_view(p), p.status)) return;
     if (e >= PN) return;
     const int64_t hu = (int64_t)bi * p.H + h;
     // the chunks lo .. hi - 1 of the whole sequence, or of packed sequence k, whose states go by sequence
