@@ -23,7 +23,8 @@ struct PackedHeader {
     int64_t total;
     int64_t max_len;        // no sequence is longer
     int n64, n128;          // chunks in use of each length
-    int pad[8];
+    int rows;               // rows of the sequences
+    int pad[7];
 };
 static_assert(sizeof(PackedHeader) == 64, "packed header");
 

@@ -42,8 +42,15 @@ template <int kParts> constexpr uint32_t kImage = kParts * kPiece;
 // Two parts where dA, one number per head, is made of many rows of many heads, three elsewhere: among random batches of
 // few rows or few heads two parts left dA off by up to 1.3e-5 of 64 bits, three by 2.4e-6 (worst of 120); from 1024
 // rows of 16 heads on two are off by 2e-6 as well (16384 rows of 32 heads: 1.9e-6), and three take 553 us instead
-// of 453 there.
-inline bool two_parts(int64_t total, int H) { return total >= 1024 && H >= 16; }
+// of 453 there.  The rows are those of the sequences, which the device knows (the buffers of a captured batch may hold
+// many more), so where the tensors have the rows for it the kernels hold both forms and the plan decides.
+constexpr int kManyRows = 1024, kManyHeads = 16;
+inline bool either_form(int64_t total, int H) { return total >= kManyRows && H >= kManyHeads; }
+template <bool kEither>
+__device__ __forceinline__ bool two_parts(const PackedGradParams &p)
+{
+    return kEither && packed_ok(p.plan, p.status) && p.plan.hdr->rows >= kManyRows;
+}
 
 __device__ __forceinline__ void raise_timeout(const PackedGradParams &p, volatile int *abort)
 {
@@ -155,10 +162,9 @@ __device__ __forceinline__ int sequence_begin(const PackedPlan &p, int n, int64_
 static_assert(sizeof(SmemWalk<2>) <= 232448 && sizeof(SmemWalk<3>) <= 232448, "the walk's shared memory");
 
 template <int kParts>
-__global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const PackedGradParams p)
+__device__ __forceinline__ void grad_walk(const PackedGradParams &p, uint8_t *raw)
 {
-    extern __shared__ __align__(1024) uint8_t sw_raw[];
-    SmemWalk<kParts> &s = *reinterpret_cast<SmemWalk<kParts> *>(sw_raw);
+    SmemWalk<kParts> &s = *reinterpret_cast<SmemWalk<kParts> *>(raw);
     constexpr int kStages = kWalkStages<kParts>;
     constexpr uint32_t kImg = kImage<kParts>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -437,6 +443,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
     if (warp == 0) tmem_dealloc(tS, 256);
 }
 
+template <bool kEither>
+__global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const __grid_constant__ PackedGradParams p)
+{
+    extern __shared__ __align__(1024) uint8_t sw_raw[];
+    if (two_parts<kEither>(p)) grad_walk<2>(p, sw_raw);
+    else grad_walk<3>(p, sw_raw);
+}
+
 // =============================================================== gradients
 // The items (chunk, head), chunk after chunk, are dealt out in equal runs of blocks of heads, one CTA per SM: a CTA meets
 // few chunks, loads C and B of a group once, and keeps dB and dC in TMEM through a block.
@@ -547,10 +561,9 @@ struct Items {
 };
 
 template <int kParts>
-__global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const PackedGradParams p)
+__device__ __forceinline__ void grad_items(const PackedGradParams &p, uint8_t *raw)
 {
-    extern __shared__ __align__(1024) uint8_t sg_raw[];
-    SmemGrad<kParts> &s = *reinterpret_cast<SmemGrad<kParts> *>(sg_raw);
+    SmemGrad<kParts> &s = *reinterpret_cast<SmemGrad<kParts> *>(raw);
     constexpr int kSlots = kGradSlots<kParts>;
     constexpr uint32_t kImg = kImage<kParts>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1159,6 +1172,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const P
     if (warp == 0) tmem_dealloc(tm, 512);
 }
 
+template <bool kEither>
+__global__ void __launch_bounds__(kGradThreads, 1) packed_grad_tc_kernel(const __grid_constant__ PackedGradParams p)
+{
+    extern __shared__ __align__(1024) uint8_t sg_raw[];
+    if (two_parts<kEither>(p)) grad_items<2>(p, sg_raw);
+    else grad_items<3>(p, sg_raw);
+}
+
 // =============================================================== sums
 // The first kSumParts x units blocks: dB and dC of a (chunk, group) whose heads make several blocks, in their order; the H blocks
 // behind them: dA and dD of a head, in a fixed order; the blocks behind those: dh_in of a sequence without chunks.
@@ -1232,7 +1253,10 @@ PackedGradLayout packed_grad_layout(int64_t nseq, int64_t total, int H, int ctas
     const int64_t m64 = packed_layout(nseq, total).m64, blocks = std::max<int64_t>(4 * ctas, 2 * m64 * H / kMaxBlock);
     auto round = [](size_t b) { return (b + 255) & ~size_t(255); };
     PackedGradLayout l;
-    l.off_part = (size_t)m64 * H * 2 * (two_parts(total, H) ? kImage<2> : kImage<3>);
+    // The states' images: in two parts for all chunks, in three for those of fewer than kManyRows rows
+    size_t images = (size_t)m64 * kImage<3>;
+    if (either_form(total, H)) images = std::max((size_t)m64 * kImage<2>, (size_t)((kManyRows - 1) / kQ + nseq) * kImage<3>);
+    l.off_part = images * H * 2;
     l.off_sums = l.off_part + (size_t)blocks * (2 * kQ * kN) * sizeof(float);
     l.off_pA = l.off_sums + round((size_t)ctas * 2 * kSumFloats * sizeof(float));
     l.off_pD = l.off_pA + round((size_t)m64 * H * sizeof(float));
@@ -1240,12 +1264,13 @@ PackedGradLayout packed_grad_layout(int64_t nseq, int64_t total, int H, int ctas
     return l;
 }
 
-template <int kParts>
-static int launch_parts(const PackedGradParams &p, int ctas, cudaStream_t st)
+template <bool kEither>
+static int launch_forms(const PackedGradParams &p, int ctas, cudaStream_t st)
 {
     static std::atomic<int> walk_done[64], grad_done[64];
-    if (!allow_smem(packed_grad_walk_kernel<kParts>, (int)sizeof(SmemWalk<kParts>), walk_done) ||
-        !allow_smem(packed_grad_tc_kernel<kParts>, (int)sizeof(SmemGrad<kParts>), grad_done))
+    constexpr size_t walk = kEither ? std::max(sizeof(SmemWalk<2>), sizeof(SmemWalk<3>)) : sizeof(SmemWalk<3>);
+    constexpr size_t grad = kEither ? std::max(sizeof(SmemGrad<2>), sizeof(SmemGrad<3>)) : sizeof(SmemGrad<3>);
+    if (!allow_smem(packed_grad_walk_kernel<kEither>, (int)walk, walk_done) || !allow_smem(packed_grad_tc_kernel<kEither>, (int)grad, grad_done))
         return 7;
     // parts of the chunk list: two waves of one CTA per SM, no more parts than sequences (they begin between sequences)
     const int64_t wide = 2 * (int64_t)p.H;
@@ -1253,10 +1278,10 @@ static int launch_parts(const PackedGradParams &p, int ctas, cudaStream_t st)
     const int64_t units = kSumParts * p.plan.m64 * p.G + p.H + p.plan.nseq;
     if (units > 0x7fffffff) return 2;
     prof_begin(st, kKBwdChain);
-    packed_grad_walk_kernel<kParts><<<dim3((unsigned)wide, (unsigned)parts), kWalkThreads, sizeof(SmemWalk<kParts>), st>>>(p);
+    packed_grad_walk_kernel<kEither><<<dim3((unsigned)wide, (unsigned)parts), kWalkThreads, walk, st>>>(p);
     prof_end(st, kKBwdChain);
     prof_begin(st, kKBwdGrad);
-    packed_grad_tc_kernel<kParts><<<(unsigned)ctas, kGradThreads, sizeof(SmemGrad<kParts>), st>>>(p);
+    packed_grad_tc_kernel<kEither><<<(unsigned)ctas, kGradThreads, grad, st>>>(p);
     prof_end(st, kKBwdGrad);
     prof_begin(st, kKBwdReduce);
     packed_grad_sum_kernel<<<(unsigned)units, 256, 0, st>>>(p, ctas);
@@ -1266,7 +1291,7 @@ static int launch_parts(const PackedGradParams &p, int ctas, cudaStream_t st)
 
 int launch_packed_grad_tc(const PackedGradParams &p, int ctas, cudaStream_t st)
 {
-    return two_parts(p.plan.total, p.H) ? launch_parts<2>(p, ctas, st) : launch_parts<3>(p, ctas, st);
+    return either_form(p.plan.total, p.H) ? launch_forms<true>(p, ctas, st) : launch_forms<false>(p, ctas, st);
 }
 
 }  // namespace ssd

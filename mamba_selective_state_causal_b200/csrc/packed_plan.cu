@@ -77,8 +77,10 @@ __global__ void __launch_bounds__(kPlanThreads) packed_seq_kernel(PackedPlanPara
     extern __shared__ int table[];         // [hash_size] lowest sequence + 1 of a slot, 0 = free
     __shared__ int2 part[32];
     __shared__ int most[32];
+    __shared__ int live;                   // rows of the sequences so far
     const int tid = threadIdx.x, mask = hash_size - 1;
     bool bad = false;
+    if (tid == 0) live = 0;                // (a barrier of block_max lies before the first addition)
     if (p.slots) {
         for (int i = tid; i < hash_size; i += kPlanThreads) table[i] = 0;
         __syncthreads();
@@ -128,6 +130,8 @@ __global__ void __launch_bounds__(kPlanThreads) packed_seq_kernel(PackedPlanPara
             }
             c = make_int2(s.n64, s.n128);
         }
+        const int rows = __reduce_add_sync(0xffffffffu, s.len);
+        if ((tid & 31) == 0 && rows > 0) atomicAdd(&live, rows);
         const int2 sum = block_sum(c, part);
         if (i < p.nseq) {
             s.c64 = base.x + sum.x - c.x;
@@ -143,6 +147,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_seq_kernel(PackedPlanPara
         PackedHeader h{};
         h.magic = kPackedMagic; h.nseq = p.nseq; h.total = p.total; h.max_len = p.max_seqlen;
         h.n64 = base.x; h.n128 = base.y;
+        h.rows = live;
         *static_cast<PackedHeader *>(p.plan) = h;
     }
 }

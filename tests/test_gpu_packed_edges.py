@@ -43,3 +43,31 @@ def test_gradients_of_a_batch_without_chunks(refused, total, dtype, P, N):
         assert (o[k] == 0).all(), k
     for k in ("dtail_in", "dconv_w", "dconv_bias"):
         assert (c[k] == 0).all(), k
+
+
+@pytest.mark.parametrize("lens", [[1] * 5, [3, 0, 70], [1, 500, 2]])
+@pytest.mark.parametrize("H,dtype,P,N", [(16, torch.bfloat16, 64, 128), (32, torch.bfloat16, 64, 128), (4, torch.float32, 32, 16)])
+def test_gradient_of_few_rows_in_large_buffers(H, dtype, P, N, lens):
+    """Rows of no sequence behind a few live ones change no bit of their gradients (a captured batch in buffers of a fixed
+    size), and those are as near to 64 bits as in buffers of their own."""
+    n = len(lens)
+    for seed in range(4):
+        got = []
+        for behind in (0, 8192):
+            d = _data(lens, H, P, N, 1, dtype, 80 + seed)
+            g = torch.Generator().manual_seed(90 + seed)
+            live = d["total"]
+            dy, dh = torch.randn(live, H * P, generator=g).to(dtype), torch.randn(n, H, P, N, generator=g)
+            more = lambda t: torch.cat((t, torch.full((behind, t.shape[1]), float("nan")).to(t.dtype))).to(DEV)  # noqa: E731
+            x, B, C = _parts(d, more(d["v"]))
+            plan = _plan(dict(d, total=live + behind))
+            o = ssd.packed_scan_backward(x, B, C, more(d["dt"]), d["A"].to(DEV), d["D"].to(DEV), more(dy), plan=plan, H=H,
+                                         h_in=d["h"].to(DEV), dh_out=dh.to(DEV))
+            got.append({k: t if k in ("dA", "dD", "dh_in") else t[:live] for k, t in o.items()})
+        ssd.sync_status()
+        for k, t in got[0].items():
+            assert torch.equal(got[1][k], t), k
+        x, B, C = _ref_in(d)
+        r = ref.scan_grad(x, B, C, d["dt"], d["A"], d["D"], d["cu"], d["slots"], d["resume"], d["h"], dy.view(-1, H, P), dh, 1)
+        for k, t in got[1].items():
+            assert ref.rel(t, r[k]) <= 1e-5, (k, ref.rel(t, r[k]))
