@@ -509,7 +509,8 @@ SSD_API int ssd_packed_conv_forward(const ssd_packed_conv_args *args, ssd_stream
  * [nseq][3][C_ch] float or NULL (dLoss/d(tail_out), by SEQUENCE, not by slot).
  * C_ch = d_inner + 2*d_bc.  Outputs, float, contiguous: du [total][C_ch]
  * (rows of no sequence stay as they were); dtail_in [nseq][3][C_ch] or NULL (zero for a sequence
- * that does not resume); dconv_w [C_ch][4]; dconv_bias [C_ch] or NULL.  The rounding of v to the
+ * that does not resume, and for every one when tail_in is NULL: no sequence has a buffer then that
+ * the gradient could be handed to, unlike in ssd_layer_backward); dconv_w [C_ch][4]; dconv_bias [C_ch] or NULL.  The rounding of v to the
  * I/O dtype is taken as the identity.  Sums are in a fixed order: the same result every time.
  */
 typedef struct ssd_packed_conv_bwd_args {
@@ -588,8 +589,10 @@ SSD_API size_t ssd_packed_scan_workspace_size(int nseq, int64_t total, int64_t m
  *   dh_out [nseq][H][P][N] float or NULL: dLoss/d(h_out), by SEQUENCE, not by slot
  * Outputs, float, contiguous: dx [total][H][P]; dB, dC [total][G][N]; ddt [total][H] (rows of
  * no sequence stay as they were); dA [H]; dD [H] or NULL; dh_in [nseq][H][P][N] or NULL
- * (zero for a sequence that does not resume, or that the plan left out).  Sums are in a fixed
- * order.
+ * (zero for a sequence that does not resume, or that the plan left out, and for every one when h_in
+ * is NULL: no sequence has a state then that the gradient could be handed to, unlike in
+ * ssd_scan_backward.  A caller who wants the gradient of a start from zeros gives a pool of zeros).
+ * Sums are in a fixed order.
  */
 typedef struct ssd_packed_scan_bwd_args {
     int dtype;

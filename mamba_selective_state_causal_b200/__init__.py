@@ -760,7 +760,8 @@ def packed_conv_backward(u, w, plan, dx, dB, dC, *, bias=None, tail_in=None, dta
     """Gradients through packed_conv_forward: dict du [total, C_ch], dtail_in [n, 3, C_ch], dconv_w, dconv_bias (float32).
 
     dx [total, (H, P)], dB, dC [total, (G, N)]: float32 gradients of v's columns, as packed_scan_backward returns
-    them; dtail_out: [n, 3, C_ch] float32 or None, by sequence.  ``out`` may hold outputs under the same keys;
+    them; dtail_out: [n, 3, C_ch] float32 or None, by sequence.  Without tail_in no sequence resumes: dtail_in is
+    zero (a pool of zeros gives the gradient of a start from zeros).  ``out`` may hold outputs under the same keys;
     rows of no sequence stay as they were in them, and are zero in those allocated here.
     """
     if stream is not None:
@@ -862,6 +863,7 @@ def packed_scan_backward(x, B, C, dt, A, D, dy, *, plan, H, G=1, h_in=None, dh_o
 
     x, B, C, dt, A, D, h_in as in the forward (dt the step that the scan used); dy: [total, H*P] or
     [total, H, P]; dh_out: [n, H, P, N] float32 or None.  dh_out and dh_in go by sequence, h_in by slot.
+    Without h_in no sequence resumes: dh_in is zero (a pool of zeros gives the gradient of a start from zeros).
     ``out`` may hold outputs under the same keys; rows of no sequence stay as they were in them, and are
     zero in those allocated here.
     """

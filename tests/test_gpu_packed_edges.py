@@ -71,3 +71,30 @@ def test_gradient_of_few_rows_in_large_buffers(H, dtype, P, N, lens):
         r = ref.scan_grad(x, B, C, d["dt"], d["A"], d["D"], d["cu"], d["slots"], d["resume"], d["h"], dy.view(-1, H, P), dh, 1)
         for k, t in got[1].items():
             assert ref.rel(t, r[k]) <= 1e-5, (k, ref.rel(t, r[k]))
+
+
+@pytest.mark.parametrize("dtype,P,N,H", [(torch.bfloat16, 64, 128, 4), (torch.float32, 32, 16, 2)])
+def test_start_states_left_out_are_zeros(dtype, P, N, H):
+    """Without h_in and tail_in every sequence starts from zeros: as with pools of zeros, only that no sequence has a state or a
+    buffer whose gradient could be asked for."""
+    lens, cch = [100, 0, 2, 65], H * P + 2 * N
+    d = _data(lens, H, P, N, 1, dtype, 85, resume=[1, 1, 1, 0])
+    g = torch.Generator().manual_seed(86)
+    dy, dh = torch.randn(d["total"], H * P, generator=g).to(DEV, dtype), torch.randn(4, H, P, N, generator=g).to(DEV)
+    w, dtail = (torch.rand(cch, 4, generator=g) - 0.5).to(DEV), torch.randn(4, 3, cch, generator=g).to(DEV)
+    u, plan = d["v"].to(DEV), _plan(d)
+    x, B, C = _parts(d, u)
+    got = []
+    for h0, t0 in ((None, None), (torch.zeros_like(d["h"]).to(DEV), torch.zeros(d["n_slots"], 3, cch, device=DEV, dtype=dtype))):
+        out = {"dh_in": torch.full_like(dh, float("nan"))}
+        o = ssd.packed_scan_backward(x, B, C, d["dt"].to(DEV), d["A"].to(DEV), d["D"].to(DEV), dy, plan=plan, H=H, h_in=h0, dh_out=dh, out=out)
+        c = ssd.packed_conv_backward(u, w, plan, o["dx"], o["dB"], o["dC"], tail_in=t0, dtail_out=dtail,
+                                     out={"dtail_in": torch.full_like(dtail, float("nan"))})
+        got.append({**o, **c})
+    ssd.sync_status()
+    for k, t in got[0].items():
+        if k in ("dh_in", "dtail_in"):
+            norms = got[1][k].flatten(1).norm(dim=1)
+            assert (t == 0).all() and (norms[:3] > 0).all() and norms[3] == 0, k
+        else:
+            assert torch.equal(got[1][k], t), k
