@@ -237,7 +237,7 @@ constexpr int kRoom = 200 * 1024;         // shared memory of a CTA, at most
 template <typename T, int nq>
 int launch_slots_n(const SlotDecodeParams &p, int cluster, size_t smem, cudaStream_t st)
 {
-    static std::atomic<int> done[64];
+    static SmemLimit done;
     if (!allow_smem(decode_slots_kernel<T, nq>, cluster > 8 ? kRoom : (int)smem, done)) return 7;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)p.b * (unsigned)cluster);

@@ -232,7 +232,7 @@ int launch_mode(const NormBwdParams &p, const NormBwdPlan &pl, cudaStream_t st)
 {
     const size_t smem = sizeof(Vec8<T>) * 3 * kDepth<T> * pl.threads +
                         sizeof(float2) * 2 * (kMode == 0 ? 0 : kMode == 1 ? pl.threads / 32 : pl.threads);
-    static std::atomic<int> done[64];
+    static SmemLimit done;
     if (!allow_smem(gated_norm_bwd_kernel<T, kMode, kMost>, (int)smem, done)) return 7;
     prof_begin(st, kKGatedNormBwd);
     gated_norm_bwd_kernel<T, kMode, kMost><<<(unsigned)pl.grid, pl.threads, smem, st>>>(p, pl.teams);

@@ -10,8 +10,7 @@
 // sequences) has none, nor has one whose offsets are refused.
 #pragma once
 
-#include <atomic>
-
+#include "smem.cuh"
 #include "ssd_common.cuh"
 
 namespace ssd {
@@ -232,18 +231,6 @@ __device__ __forceinline__ const float *window_start(const PackedScanParams &p, 
         if ((k64 ? s.c64 + s.n64 : s.c128 + s.n128) > c1) return p.ws_start + ((int64_t)window * p.H + h) * PN;
     }
     return p.h_in + ((int64_t)d.w * p.H + h) * PN;
-}
-
-// Let a kernel take up to `bytes` of dynamic shared memory, once per device (`done` is the kernel's own)
-template <typename F>
-inline bool allow_smem(F *kernel, int bytes, std::atomic<int> (&done)[64])
-{
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-    if (done[dev].load(std::memory_order_relaxed) >= bytes) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-    done[dev].store(bytes, std::memory_order_relaxed);
-    return true;
 }
 
 // The state entering window k, whose first chunk d continues a sequence that began in window b, is

@@ -191,7 +191,7 @@ int launch_conv_t(const PackedConvParams &p, int sms, cudaStream_t st)
     const int64_t blocks = (pieces * threads + kPackedConvThreads - 1) / kPackedConvThreads;
     if (blocks > 0x7fffffffLL) return 2;
     constexpr int smem = kRing * kPackedConvThreads * (int)sizeof(Vec16p);
-    static std::atomic<int> done[64];
+    static SmemLimit done;
     if (!allow_smem(packed_conv_kernel<T>, smem, done)) return 7;
     prof_begin(st, kKPackedConv);
     packed_conv_kernel<T><<<(unsigned)blocks, kPackedConvThreads, smem, st>>>(p, pieces);
@@ -467,7 +467,7 @@ int launch_packed_conv_backward(const PackedConvBwdParams &p, int dtype, cudaStr
     if (blocks > 0x7fffffffLL) return 2;
     prof_begin(st, kKPackedConvBwd);
     if (blocks > 0) {
-        static std::atomic<int> done_b[64], done_f[64];
+        static SmemLimit done_b, done_f;
         const int smem_b = (16 + 8) * kBack * kConvBwdT, smem_f = (16 + 16) * kBack * kConvBwdT;
         if (!(dtype == 1 ? allow_smem(packed_conv_bwd_kernel<__nv_bfloat16>, smem_b, done_b) : allow_smem(packed_conv_bwd_kernel<float>, smem_f, done_f)))
             return 7;

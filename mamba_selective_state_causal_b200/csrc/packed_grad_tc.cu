@@ -24,7 +24,6 @@
 // All waits are bounded (tc::mbar_wait): on a timeout the CTA raises an abort flag, every thread
 // unwinds, copies and products in flight are drained, TMEM is freed and the status word reports it.
 #include <algorithm>
-#include <atomic>
 
 #include "packed.cuh"
 #include "scan_tc_util.cuh"
@@ -1267,7 +1266,7 @@ PackedGradLayout packed_grad_layout(int64_t nseq, int64_t total, int H, int ctas
 template <bool kEither>
 static int launch_forms(const PackedGradParams &p, int ctas, cudaStream_t st)
 {
-    static std::atomic<int> walk_done[64], grad_done[64];
+    static SmemLimit walk_done, grad_done;
     constexpr size_t walk = kEither ? std::max(sizeof(SmemWalk<2>), sizeof(SmemWalk<3>)) : sizeof(SmemWalk<3>);
     constexpr size_t grad = kEither ? std::max(sizeof(SmemGrad<2>), sizeof(SmemGrad<3>)) : sizeof(SmemGrad<3>);
     if (!allow_smem(packed_grad_walk_kernel<kEither>, (int)walk, walk_done) || !allow_smem(packed_grad_tc_kernel<kEither>, (int)grad, grad_done))

@@ -9,7 +9,6 @@
 // The second kernel writes the chunks, each found by a binary search over the sequences' first chunks.
 // Both are latency: at 256 sequences of 8191 rows the two take a few microseconds once per batch.
 #include <algorithm>
-#include <atomic>
 
 #include "packed.cuh"
 
@@ -189,7 +188,7 @@ int launch_packed_plan(const PackedPlanParams &p, cudaStream_t st)
     int hash = 64;
     if (p.slots) while (hash < 2 * p.nseq) hash *= 2;
     const int smem = p.slots ? hash * (int)sizeof(int) : 0;
-    static std::atomic<int> done[64];
+    static SmemLimit done;
     if (!allow_smem(packed_seq_kernel, 2 * kPackedMaxSlotted * (int)sizeof(int), done)) return 7;
     prof_begin(st, kKPackedPlan);
     packed_seq_kernel<<<1, kPlanThreads, smem, st>>>(p, reinterpret_cast<PackedSeq *>(b + l.off_seq), hash);

@@ -319,7 +319,7 @@ int launch_generic_t(const PackedScanParams &p, bool carry, cudaStream_t st)
     const int P = p.P, N = p.N;
     const size_t smA = sizeof(float) * ((size_t)kQ * (P + 1) + (size_t)kQ * (N + 1) + (size_t)P * (N + 1) + 2 * kQ);
     const size_t smC = smA + sizeof(float) * ((size_t)kQ * (N + 1) + (size_t)kQ * kM);
-    static std::atomic<int> done_a[64], done_c[64];
+    static SmemLimit done_a, done_c;
     if (!allow_smem(packed_state_kernel<T>, (int)smA, done_a) || !allow_smem(packed_output_kernel<T>, (int)smC, done_c)) return 7;
     const dim3 grid((unsigned)p.nw, (unsigned)p.H);
     if (carry && p.nw > 1) {

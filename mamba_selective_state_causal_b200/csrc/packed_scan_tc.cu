@@ -22,7 +22,6 @@
 //
 // All waits are bounded (tc::mbar_wait): on a timeout the CTA raises an abort flag, every thread
 // unwinds, outstanding MMAs and loads are drained, TMEM is freed and the status word reports it.
-#include <atomic>
 
 #include <cuda.h>
 
@@ -1053,7 +1052,7 @@ int launch_packed_scan_tc(const PackedScanParams &p, bool carry, cudaStream_t st
          (hand_on && (!encode_bf16(enc, &maps.x64, p.x, hp, rows, 1, p.xrs, 0, kQA) || !encode_bf16(enc, &maps.B64, p.B, gn, rows, 1, p.Brs, 0, kQA))) ||
          !encode_bf16(enc, &maps.C, p.C, gn, rows, 1, p.Crs, 0) || !encode_bf16(enc, &maps.y, p.y, hp, rows, 1, p.yrs, 0)))
         return 6;
-    static std::atomic<int> done_a[64], done_c[64];
+    static SmemLimit done_a, done_c;
     if (!allow_smem(packed_state_tc_kernel, (int)kSmemA, done_a) || !allow_smem(packed_output_tc_kernel, (int)kSmemC, done_c)) return 7;
     const unsigned units = (unsigned)p.nw * (unsigned)(p.H / 2);
     if (hand_on) {

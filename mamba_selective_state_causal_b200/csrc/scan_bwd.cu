@@ -1450,10 +1450,8 @@ int launch_bwd_t(BwdParams p, cudaStream_t st)
     const size_t s1 = summary_smem(p.P, p.N);
     p.stage_adjoint = grad_smem(p.P, p.N, true) <= (size_t)smem_optin() ? 1 : 0;
     const size_t s2 = grad_smem(p.P, p.N, p.stage_adjoint != 0);
-    if (cudaFuncSetAttribute(bwd_chunk_summary_kernel<T, kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(bwd_chunk_grad_kernel<T, kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2) !=
-            cudaSuccess)
+    static SmemLimit summary_limit, grad_limit;
+    if (!allow_smem(bwd_chunk_summary_kernel<T, kPacked>, (int)s1, summary_limit) || !allow_smem(bwd_chunk_grad_kernel<T, kPacked>, (int)s2, grad_limit))
         return 7;
     const dim3 grid((unsigned)p.nch, (unsigned)p.H, (unsigned)p.b);
     // bf16 inputs at P = 64, N = 128: the summaries and the gradients on the tensor cores

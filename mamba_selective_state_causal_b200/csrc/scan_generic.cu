@@ -22,6 +22,7 @@
 // This file is the general path: any supported P, N, Q and both dtypes.
 #include <algorithm>
 
+#include "smem.cuh"
 #include "ssd_common.cuh"
 
 namespace ssd {
@@ -236,8 +237,8 @@ int launch_t(const ScanParams &p, cudaStream_t st)
     const size_t smA = sizeof(float) * ((size_t)Q * (P + N) + 3 * Q);
     const size_t smC = sizeof(float) * ((size_t)Q * (P + 2 * N) + (size_t)P * N + kRowBlock * Q + 3 * Q);
     if (smC > 227 * 1024 || smA > 227 * 1024) return 6;
-    if (cudaFuncSetAttribute(stripe_state_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smA) != cudaSuccess) return 7;
-    if (cudaFuncSetAttribute(chunk_output_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smC) != cudaSuccess) return 7;
+    static SmemLimit state_limit, output_limit;
+    if (!allow_smem(stripe_state_kernel<T>, (int)smA, state_limit) || !allow_smem(chunk_output_kernel<T>, (int)smC, output_limit)) return 7;
     if (p.ns > 65535 || p.H > 65535 || p.b > 65535) return 6;
     const dim3 grid((unsigned)p.ns, (unsigned)p.H, (unsigned)p.b);
     if (p.ns > 1) {
