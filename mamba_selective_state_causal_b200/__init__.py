@@ -854,7 +854,9 @@ def packed_scan_forward(x, B, C, dt, A, D=None, *, plan, H, G=1, h_in=None, h_ou
 
 def packed_scan_backward_workspace(plan, H, P, N):
     """Workspace of packed_scan_backward for this plan and these heads."""
-    return _bytes_on(plan.device, lib().ssd_packed_scan_backward_workspace_size(plan.nseq, plan.total, H, P, N))
+    with torch.cuda.device(plan.device):
+        n = lib().ssd_packed_scan_backward_workspace_size(plan.nseq, plan.total, H, P, N)
+    return _bytes_on(plan.device, n)
 
 
 def packed_scan_backward(x, B, C, dt, A, D, dy, *, plan, H, G=1, h_in=None, dh_out=None, out=None, workspace=None, stream=None):
