@@ -34,9 +34,10 @@
  *                          (default 2000); a wait that runs out latches
  *                          SSD_ERR_TIMEOUT in the device status word.
  *      SSD_TEST_DROP_UNIT  index of one work unit (CTA) of the tensor-core
- *                          scan whose loads are never issued, so that its
- *                          waits run out (failure-detection test); it applies
- *                          to the first scan call of the process only.
+ *                          scan or of ssd_decode_slots whose loads are never
+ *                          issued, so that its waits run out (failure-detection
+ *                          test); it applies to the first such call of the
+ *                          process only.
  *      SSD_SCAN_PATH       "generic" forces the CUDA-core scan kernels.
  */
 #ifndef SSD_H_
@@ -723,7 +724,9 @@ SSD_API int ssd_scan_forward_static_scratch(const ssd_scan_args *args, ssd_strea
  * ssd_sync_status -- synchronise `stream`, then return SSD_ERR_LAUNCH if the
  * CUDA runtime reports an error, else the device status word latched by
  * this library's kernels on the current device (SSD_OK, SSD_ERR_TIMEOUT, or SSD_ERR_INDEX
- * from the packed calls), which it then clears.
+ * from the packed calls), which it then clears.  After SSD_ERR_TIMEOUT the outputs of the call
+ * whose wait ran out are undefined, and so are the slots that it updated in place: some of
+ * a stream's states may have taken the step, others and its conv buffer not.
  */
 SSD_API int ssd_sync_status(ssd_stream_t stream);
 

@@ -14,7 +14,7 @@ unsigned int *api_status_ptr();
 int api_sm_count();
 uint64_t api_wait_limit_ns();
 bool api_force_generic();
-int64_t api_take_drop_unit();   // SSD_TEST_DROP_UNIT on the first scan call of the process, else -1
+int64_t api_take_drop_unit();   // SSD_TEST_DROP_UNIT on the first scan or slot step of the process, else -1
 
 inline size_t api_elem_size(int dtype) { return dtype == 1 ? 2 : 4; }
 inline bool api_aligned(const void *p, size_t n = 16) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

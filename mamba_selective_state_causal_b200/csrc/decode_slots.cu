@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kSlotThreads) decode_slots_kernel(SlotDecodePa
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
         fence_mbar_init();
-        for (int i = 0; i < kStages && i < np; ++i) {
+        for (int i = 0; i < kStages && i < np && (int64_t)blockIdx.x != p.test_drop_unit; ++i) {
             mbar_arrive_expect_tx(&full[i], bytes);
             bulk_load(state + i * piece, hin + (int64_t)i * piece, bytes, &full[i]);
         }
@@ -198,13 +198,15 @@ __global__ void __launch_bounds__(kSlotThreads) decode_slots_kernel(SlotDecodePa
         }
         fence_proxy_async_smem();
         if (!__syncthreads_and(landed)) {
-            // a copy never came: nothing more is written, and what is on its way is waited for
+            // a copy never came: this CTA writes no more states and no buffer, and what is on its way is waited for
             if (tid == 0) {
                 atomicOr(p.status, kDevTimeout);
                 for (int q = k; q < np && q < k + kStages - (k > 0 ? 1 : 0); ++q)
                     mbar_wait(&full[q % kStages], (uint32_t)(q / kStages) & 1, nullptr, 100000000ull);
+                tma_store_wait<0>();
             }
-            break;
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            return;
         }
         if (tid == 0) {
             bulk_store(hout + (int64_t)k * piece, sm, bytes);

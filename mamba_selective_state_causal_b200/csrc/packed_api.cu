@@ -403,6 +403,7 @@ int ssd_decode_slots(const ssd_decode_slots_args *a, ssd_stream_t stream)
     p.h_in = a->h_in; p.h_out = a->h_out; p.y = a->y; p.ybs = a->y_batch_stride;
     p.dt_bias = a->dt_bias; p.dt_softplus = a->dt_softplus; p.dt_min = a->dt_min; p.dt_max = a->dt_max;
     p.wait_limit_ns = api_wait_limit_ns();
+    p.test_drop_unit = api_take_drop_unit();
     rc = launch_slot_decode(p, a->dtype, api_sm_count(), (cudaStream_t)stream);
     if (rc == 6) return api_fail(SSD_ERR_UNSUPPORTED, "no GPU kernel for this shape (b=%d H=%d P=%d N=%d G=%d)", a->b, a->H, a->P, a->N, a->G);
     return rc ? cuda_fail("slot decode") : api_ok();

@@ -25,6 +25,7 @@ struct SlotDecodeParams {
     int heads_per_cta, stages;  // set by the launcher
     unsigned int *status;
     uint64_t wait_limit_ns;
+    int64_t test_drop_unit;     // the CTA whose copies are never issued (test hook), or -1
 };
 
 int launch_slot_decode(const SlotDecodeParams &p, int dtype, int sms, cudaStream_t st);

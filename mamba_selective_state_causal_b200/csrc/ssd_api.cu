@@ -59,7 +59,7 @@ unsigned int *status_ptr()
 // Test and diagnostic hooks, read from the environment once per process (the
 // first scan call) and documented in include/ssd.h:
 //   SSD_WAIT_LIMIT_MS   bound of every device-side wait, in ms (default 2000)
-//   SSD_TEST_DROP_UNIT  index of one work unit of the first scan call of the process
+//   SSD_TEST_DROP_UNIT  index of one work unit of the first scan or slot step of the process
 //                       whose loads are never issued, so that its waits run out
 //                       (failure-detection test); later calls run normally
 //   SSD_SCAN_PATH       "generic" forces the CUDA-core scan kernels

@@ -3,8 +3,16 @@
 Tolerances as in test_gpu_packed_scan.py and test_gpu_slots.py (relL2 1e-5 against 64 bits for fp32 outputs); where two
 calls have the same arithmetic, their outputs are equal.
 """
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+if __name__ == "__main__":
+    sys.path[:0] = [HERE, os.path.dirname(HERE)]
 
 import mamba_selective_state_causal_b200 as ssd
 import packed_ref as ref
@@ -98,3 +106,40 @@ def test_start_states_left_out_are_zeros(dtype, P, N, H):
             assert (t == 0).all() and (norms[:3] > 0).all() and norms[3] == 0, k
         else:
             assert torch.equal(got[1][k], t), k
+
+
+def _child():
+    from test_gpu_slots import _pool, _step
+    H, P, N, slots, dtype = 32, 64, 128, [4, 0, 2], torch.bfloat16
+    d = _pool(3, 5, H, P, N, 1, dtype, slots, 88)
+    hp, tp = d["h"].to(DEV), d["tail"].to(DEV)
+    _step(d, tail_in=tp, h_in=hp)
+    try:
+        ssd.sync_status()
+    except ssd.SSDError as e:
+        assert e.code == 8, e
+    else:
+        raise AssertionError("the dropped unit did not time out")
+    h1, t1 = d["h"].to(DEV), d["tail"].to(DEV)
+    _step(d, tail_in=t1, h_in=h1)
+    ssd.sync_status()
+    for k in (4, 2, 1, 3):                  # the other streams, and the slots of none
+        assert torch.equal(hp[k], h1[k]) and torch.equal(tp[k], t1[k]), k
+    # 16 CTAs to a stream: the second one of the second stream has heads 2 and 3 and channels 16 .. 31 of B and C
+    old, new = d["tail"][0].to(DEV), tp[0]
+    for a, b in ((2 * P, 4 * P), (H * P + 16, H * P + 32)):
+        assert torch.equal(new[:, a:b], old[:, a:b])
+    assert torch.equal(hp[0, 2:4], d["h"][0, 2:4].to(DEV))
+    print("child ok")
+
+
+def test_step_whose_copies_never_come():
+    """A CTA of the slot step that gives up writes none of its states and nothing into the conv buffer; the other streams and the
+    next call are right."""
+    env = dict(os.environ, SSD_TEST_DROP_UNIT="17", SSD_WAIT_LIMIT_MS="200")
+    r = subprocess.run([sys.executable, os.path.abspath(__file__)], env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "child ok" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+
+
+if __name__ == "__main__":
+    _child()
