@@ -133,9 +133,10 @@ __global__ void __launch_bounds__(kSlotThreads) decode_slots_kernel(SlotDecodePa
         reinterpret_cast<float4 *>(hv)[i] = make_float4(expf(dt * p.A[h]), dt, p.D ? p.D[h] : 0.0f, 0.0f);
     }
     // this CTA has read the old buffer's B and C rows; it writes its share of the new ones at the end.
-    // Their values are read before the barrier, since any of them may change after it
+    // The values of the first kKeep turns are read here, ahead of their use; those of more (many groups) at the end: after the
+    // barrier no other CTA reads or writes them
     const int bcn = 2 * p.G * N, share = (bcn + ncta - 1) / ncta;
-    constexpr int kKeep = 4;                                      // share <= kKeep * kSlotThreads (checked by the launcher)
+    constexpr int kKeep = 4;
     T k1[kKeep], k2[kKeep], k3[kKeep];
 #pragma unroll
     for (int k = 0; k < kKeep; ++k) {
@@ -225,8 +226,10 @@ __global__ void __launch_bounds__(kSlotThreads) decode_slots_kernel(SlotDecodePa
         const int i = tid + k * kSlotThreads, c = din + rank * share + i;
         if (i < share && rank * share + i < bcn) { tout[c] = k1[k]; tout[C_ch + c] = k2[k]; tout[2 * C_ch + c] = k3[k]; }
     }
-    for (int i = tid; i < nx; i += kSlotThreads) {                // x's channels: no other CTA reads or writes them
-        const int c = h0 * P + i;
+    // x's channels, which no other CTA reads or writes, and what the share has beyond the values kept
+    const int more = min(share, bcn - rank * share) - kKeep * kSlotThreads;
+    for (int i = tid; i < nx + max(0, more); i += kSlotThreads) {
+        const int c = i < nx ? h0 * P + i : din + rank * share + kKeep * kSlotThreads + i - nx;
         const T a = tin[C_ch + c], b = tin[2 * C_ch + c], n = u[c];
         tout[c] = a; tout[C_ch + c] = b; tout[2 * C_ch + c] = n;
     }
@@ -307,7 +310,6 @@ static int launch_slots(SlotDecodeParams p, int cluster, int dtype, int sms, cud
     const int np = 2 * p.heads_per_cta;
     p.stages = p.b * cluster <= sms ? (int)std::min<size_t>(std::min(np, kMaxStages), (room - small) / piece) : std::min(np, 3);
     const size_t smem = p.stages * piece + small;
-    if ((2 * p.G * p.N + cluster - 1) / cluster > 4 * kSlotThreads) return 6;
     if ((int64_t)p.b * cluster > 0x7fffffffLL) return 6;
     return dtype == 1 ? launch_slots_t<__nv_bfloat16>(p, cluster, smem, st) : launch_slots_t<float>(p, cluster, smem, st);
 }

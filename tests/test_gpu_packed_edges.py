@@ -108,6 +108,23 @@ def test_start_states_left_out_are_zeros(dtype, P, N, H):
             assert torch.equal(got[1][k], t), k
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("b", [2, 12])
+def test_step_of_many_groups(b, dtype):
+    """A group to each of 40 heads: 10240 channels of B and C, more than the CTAs of a stream hold in registers."""
+    from test_gpu_slots import _pool, _ref_step, _step
+    slots = [(4 * i + 1) % (b + 3) for i in range(b)]
+    d = _pool(b, b + 3, 40, 16, 128, 40, dtype, slots, 87)
+    y, h, tail, ya = _ref_step(d, slots)
+    hp, tp = d["h"].to(DEV), d["tail"].to(DEV)
+    o = _step(d, tail_in=tp, h_in=hp)
+    ssd.sync_status()
+    assert ref.rel(hp, h) <= 1e-5
+    assert torch.equal(tp.cpu().double(), tail)
+    near = (2.0 ** -8 if dtype == torch.bfloat16 else 0.0) * y.abs() + 2.0 ** -14 * ya
+    assert ((o["y"].cpu().double() - y).abs() <= near).all()
+
+
 def _child():
     from test_gpu_slots import _pool, _step
     H, P, N, slots, dtype = 32, 64, 128, [4, 0, 2], torch.bfloat16
