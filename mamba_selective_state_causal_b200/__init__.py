@@ -661,11 +661,17 @@ def _bytes_on(dev, n):
     return torch.empty(max(int(n), 1), dtype=torch.uint8, device=dev)
 
 
+def _memory(t, dev, name):
+    """(data pointer, bytes behind it) of a buffer of any type: a view's elements need not all lie there."""
+    if t.device != dev:
+        raise ValueError(f"all tensors must be on {dev}, {name} is on {t.device}")
+    if not t.is_contiguous():
+        raise TypeError(f"{name} must be contiguous")
+    return t.data_ptr(), t.nbytes
+
+
 def _set_ws(a, workspace, dev):
-    if workspace.device != dev:
-        raise ValueError(f"all tensors must be on {dev}, workspace is on {workspace.device}")
-    a.workspace = workspace.data_ptr()
-    a.workspace_bytes = workspace.nbytes
+    a.workspace, a.workspace_bytes = _memory(workspace, dev, "workspace")
 
 
 def _outputs(out, shapes, dev):
@@ -710,9 +716,7 @@ def packed_plan(cu_seqlens, total, *, slots=None, resume=None, n_slots=0, max_se
     a.resume = _ptr_of(resume, (n,), torch.int32, dev, "resume")
     if buf is None:
         buf = _bytes_on(dev, lib().ssd_packed_plan_size(n, total))
-    if buf.device != dev:
-        raise ValueError(f"all tensors must be on {dev}, buf is on {buf.device}")
-    a.plan = buf.data_ptr(); a.plan_bytes = buf.nbytes
+    a.plan, a.plan_bytes = _memory(buf, dev, "buf")
     _launch(lib().ssd_packed_plan, a, dev, stream)
     return PackedPlan(buf, n, int(total), n_slots if slots is not None else max(n_slots, n), int(max_seqlen), slots is not None)
 

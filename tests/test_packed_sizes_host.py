@@ -35,3 +35,21 @@ def test_sized_on_the_plans_device(ssd, monkeypatch):
     assert ssd.packed_scan_backward_workspace(plan, 4, 64, 128) == 64
     assert ssd.gated_rmsnorm_backward_workspace(10, 64, device="cuda:1") == 64
     assert asked == dict.fromkeys(names, "cuda:1") and current == ["cuda:0"]
+
+
+def test_memory_that_is_not_there_is_refused(ssd):
+    """A workspace or a plan's buffer counts with the bytes that lie behind its pointer, not with its elements."""
+    cpu = torch.device("cpu")
+    a = types.SimpleNamespace()
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    ssd._set_ws(a, ws, cpu)
+    assert (a.workspace, a.workspace_bytes) == (ws.data_ptr(), 4096)
+    ssd._set_ws(a, torch.zeros(16, 8), cpu)
+    assert a.workspace_bytes == 512
+    for bad in (ws[:1].expand(4096), ws[::2], ws.view(64, 64).t()):
+        with pytest.raises(TypeError, match="contiguous"):
+            ssd._set_ws(a, bad, cpu)
+        with pytest.raises(TypeError, match="contiguous"):
+            ssd._memory(bad, cpu, "buf")
+    with pytest.raises(ValueError, match="workspace"):
+        ssd._set_ws(a, ws, torch.device("cuda", 0))
