@@ -45,8 +45,11 @@ template <> struct ConvVec<__nv_bfloat16> {
         for (int i = 0; i < 4; ++i) v.w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
         return v;
     }
-    // weights and bias halved (exact): the sum is h = z / 2 and z sigma(z) = h + h tanh(h), one
-    // hardware tanh (relative error about 2^-11) before the rounding to bf16 (2^-9)
+    // weights and bias halved (exact): the sum is h = z / 2 and z sigma(z) = h + h tanh(h), with one hardware
+    // tanh (relative error up to 2^-11).  What that costs v is absolute, up to 2^-11 |h|: less than the rounding to
+    // bf16 (half a step, 2^-9 to 2^-8 of v) for positive z, more than it where h and h tanh(h) cancel (at z = -4 up to
+    // 1.3 % of v, at z = -6, where v is -0.015, up to 10 %).  The layer's convolution has this form too, and a packed
+    // sequence gets its bits; the gradients and the slot step take the accurate sigma.
     static constexpr float kPre = 0.5f;
     __device__ __forceinline__ static float silu(float h)
     {

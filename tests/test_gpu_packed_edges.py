@@ -125,6 +125,31 @@ def test_step_of_many_groups(b, dtype):
     assert ((o["y"].cpu().double() - y).abs() <= near).all()
 
 
+def test_convolution_of_large_sums():
+    """bf16 v element by element, sums z of up to about 10 either way: z sigma(z) = h + h tanh(h), h = z / 2, by a hardware tanh
+    of relative error 2^-11 is off by 2^-11 |h|, by its fp32 sums 2^-20 of their terms, and by its rounding 2^-8 of what
+    is rounded."""
+    cch, total = 256, 700
+    g = torch.Generator().manual_seed(89)
+    u, w = 6 * torch.randn(total, cch, generator=g).to(torch.bfloat16), torch.rand(cch, 4, generator=g) - 0.5
+    bias = torch.randn(cch, generator=g)
+    plan = ssd.packed_plan(torch.tensor([0, 3, 400, total], **I32), total)
+    v, _ = ssd.packed_conv_forward(u.to(DEV), w.to(DEV), plan, bias.to(DEV))
+    ssd.sync_status()
+    small = 0
+    for a, b in ((0, 3), (3, 400), (400, total)):
+        rows = torch.cat((torch.zeros(3, cch, dtype=torch.float64), u[a:b].double()))
+        terms = torch.stack([rows[k:k + b - a] * w[:, k].double() for k in range(4)] + [bias.double().expand(b - a, -1)])
+        z = terms.sum(0)
+        want = z / (1 + torch.exp(-z))
+        near = 2.0 ** -11 * z.abs() / 2 + 2.0 ** -20 * terms.abs().sum(0)
+        near = near + 2.0 ** -8 * (want.abs() + near)
+        assert ((v[a:b].cpu().double() - want).abs() <= near).all()
+        small += int((z < -6).sum())
+    assert small > 100
+
+
+
 def _child():
     from test_gpu_slots import _pool, _step
     H, P, N, slots, dtype = 32, 64, 128, [4, 0, 2], torch.bfloat16
