@@ -18,6 +18,7 @@ import hashlib
 import json
 import math
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -115,17 +116,33 @@ def hbm_peak():
         return FALLBACK_HBM_GBS, "fallback"
 
 
+def code_digest(path):
+    """Digest of a source file and of the headers beside it that it includes (and they include), without comments
+    and white space: what can change the compiled kernel."""
+    texts, todo = {}, [path]
+    while todo:
+        p = os.path.normpath(todo.pop())
+        if p in texts or not os.path.exists(p):
+            continue
+        with open(p) as f:
+            text = re.sub(r"//[^\n]*|/\*.*?\*/", " ", f.read(), flags=re.S)
+        texts[p] = " ".join(text.split())
+        todo += [os.path.join(os.path.dirname(p), i) for i in re.findall(r'#\s*include\s*"([^"]+)"', text)]
+    h = hashlib.sha256()
+    for p in sorted(texts, key=os.path.basename):
+        h.update((os.path.basename(p) + "\n" + texts[p] + "\n").encode())
+    return h.hexdigest()[:16]
+
+
 def recorded_traffic(kernel):
     """DRAM bytes per token of `kernel` from the committed ncu summary, or None
-    when the kernel's source changed since those counters were taken."""
+    when the kernel's code changed since those counters were taken."""
     path = os.path.join(ROOT, "profiles", "traffic.json")
     try:
         with open(path) as f:
             d = json.load(f)
         rec = d[kernel]
-        src = os.path.join(ROOT, rec["source"])
-        digest = hashlib.sha256(open(src, "rb").read()).hexdigest()[:16]
-        if digest != rec["source_sha256_16"]:
+        if code_digest(os.path.join(ROOT, rec["source"])) != rec["code_sha256_16"]:
             return None
         return float(rec["dram_bytes_per_token"])
     except Exception:
