@@ -42,8 +42,11 @@ __device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t 
                  ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
 }
 
-// nq = N / 4: lanes of a state row
-template <typename T, int nq>
+constexpr int kKeep = 4;             // turns of a CTA over its share of B's and C's channels that it keeps in registers
+
+// nq = N / 4: lanes of a state row.  kLate: a share is longer than that.  (With the loop for the rest in every kernel 256
+// streams of one group took 105 us instead of 101: at four CTAs per SM there is no register to spare.)
+template <typename T, int nq, bool kLate>
 __global__ void __launch_bounds__(kSlotThreads) decode_slots_kernel(SlotDecodeParams p)
 {
     extern __shared__ __align__(128) uint8_t raw[];
@@ -133,10 +136,9 @@ __global__ void __launch_bounds__(kSlotThreads) decode_slots_kernel(SlotDecodePa
         reinterpret_cast<float4 *>(hv)[i] = make_float4(expf(dt * p.A[h]), dt, p.D ? p.D[h] : 0.0f, 0.0f);
     }
     // this CTA has read the old buffer's B and C rows; it writes its share of the new ones at the end.
-    // The values of the first kKeep turns are read here, ahead of their use; those of more (many groups) at the end: after the
-    // barrier no other CTA reads or writes them
+    // The values of the first kKeep turns are read here, ahead of their use; those of more (kLate, many groups) at the end:
+    // after the barrier no other CTA reads or writes them
     const int bcn = 2 * p.G * N, share = (bcn + ncta - 1) / ncta;
-    constexpr int kKeep = 4;
     T k1[kKeep], k2[kKeep], k3[kKeep];
 #pragma unroll
     for (int k = 0; k < kKeep; ++k) {
@@ -226,10 +228,15 @@ __global__ void __launch_bounds__(kSlotThreads) decode_slots_kernel(SlotDecodePa
         const int i = tid + k * kSlotThreads, c = din + rank * share + i;
         if (i < share && rank * share + i < bcn) { tout[c] = k1[k]; tout[C_ch + c] = k2[k]; tout[2 * C_ch + c] = k3[k]; }
     }
-    // x's channels, which no other CTA reads or writes, and what the share has beyond the values kept
-    const int more = min(share, bcn - rank * share) - kKeep * kSlotThreads;
-    for (int i = tid; i < nx + max(0, more); i += kSlotThreads) {
-        const int c = i < nx ? h0 * P + i : din + rank * share + kKeep * kSlotThreads + i - nx;
+    if (kLate) {
+        for (int i = tid + kKeep * kSlotThreads; i < share && rank * share + i < bcn; i += kSlotThreads) {
+            const int c = din + rank * share + i;
+            const T a = tin[C_ch + c], b = tin[2 * C_ch + c], n = u[c];
+            tout[c] = a; tout[C_ch + c] = b; tout[2 * C_ch + c] = n;
+        }
+    }
+    for (int i = tid; i < nx; i += kSlotThreads) {                // x's channels: no other CTA reads or writes them
+        const int c = h0 * P + i;
         const T a = tin[C_ch + c], b = tin[2 * C_ch + c], n = u[c];
         tout[c] = a; tout[C_ch + c] = b; tout[2 * C_ch + c] = n;
     }
@@ -239,11 +246,11 @@ __global__ void __launch_bounds__(kSlotThreads) decode_slots_kernel(SlotDecodePa
 constexpr int kNotWide = -1;
 constexpr int kRoom = 200 * 1024;         // shared memory of a CTA, at most
 
-template <typename T, int nq>
+template <typename T, int nq, bool kLate>
 int launch_slots_n(const SlotDecodeParams &p, int cluster, size_t smem, cudaStream_t st)
 {
     static SmemLimit done;
-    if (!allow_smem(decode_slots_kernel<T, nq>, cluster > 8 ? kRoom : (int)smem, done)) return 7;
+    if (!allow_smem(decode_slots_kernel<T, nq, kLate>, cluster > 8 ? kRoom : (int)smem, done)) return 7;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)p.b * (unsigned)cluster);
     cfg.blockDim = dim3(kSlotThreads);
@@ -267,8 +274,8 @@ int launch_slots_n(const SlotDecodeParams &p, int cluster, size_t smem, cudaStre
             int active = 0;
             cudaLaunchConfig_t most = cfg;
             most.dynamicSmemBytes = kRoom;
-            if (cudaFuncSetAttribute(decode_slots_kernel<T, nq>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-                cudaOccupancyMaxActiveClusters(&active, decode_slots_kernel<T, nq>, &most) != cudaSuccess) {
+            if (cudaFuncSetAttribute(decode_slots_kernel<T, nq, kLate>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+                cudaOccupancyMaxActiveClusters(&active, decode_slots_kernel<T, nq, kLate>, &most) != cudaSuccess) {
                 active = 0;
                 cudaGetLastError();
             }
@@ -278,19 +285,26 @@ int launch_slots_n(const SlotDecodeParams &p, int cluster, size_t smem, cudaStre
         if (p.b > w - 1) return kNotWide;
     }
     prof_begin(st, kKSlotDecode);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_slots_kernel<T, nq>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_slots_kernel<T, nq, kLate>, p);
     prof_end(st, kKSlotDecode);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 0 : 7;
+}
+
+template <typename T, int nq>
+int launch_slots_q(const SlotDecodeParams &p, int cluster, size_t smem, cudaStream_t st)
+{
+    const bool late = (2 * p.G * p.N + cluster - 1) / cluster > kKeep * kSlotThreads;
+    return late ? launch_slots_n<T, nq, true>(p, cluster, smem, st) : launch_slots_n<T, nq, false>(p, cluster, smem, st);
 }
 
 template <typename T>
 int launch_slots_t(const SlotDecodeParams &p, int cluster, size_t smem, cudaStream_t st)
 {
     switch (p.N) {
-    case 16: return launch_slots_n<T, 4>(p, cluster, smem, st);
-    case 32: return launch_slots_n<T, 8>(p, cluster, smem, st);
-    case 64: return launch_slots_n<T, 16>(p, cluster, smem, st);
-    default: return launch_slots_n<T, 32>(p, cluster, smem, st);
+    case 16: return launch_slots_q<T, 4>(p, cluster, smem, st);
+    case 32: return launch_slots_q<T, 8>(p, cluster, smem, st);
+    case 64: return launch_slots_q<T, 16>(p, cluster, smem, st);
+    default: return launch_slots_q<T, 32>(p, cluster, smem, st);
     }
 }
 
