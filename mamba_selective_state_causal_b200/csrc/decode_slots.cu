@@ -13,7 +13,7 @@
 // N = 128), three in flight per CTA and four CTAs per SM (all of them, up to 16, where the batch is so small
 // that a CTA has its SM to itself); a buffer is refilled one piece after its copy out was started, so that nobody waits for that
 // copy to have read it.  v is not rounded to the I/O type here: it stays in registers and shared memory, where
-// the layer's packed convolution stores it.  256 streams of 32 heads (P = 64, N = 128): 100 us, 0.8 of the copy
+// the layer's packed convolution stores it.  256 streams of 32 heads (P = 64, N = 128): 100 to 102 us, 0.8 of the copy
 // rate; two streams: the launch.
 #include <algorithm>
 

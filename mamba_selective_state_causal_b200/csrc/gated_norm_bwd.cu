@@ -7,7 +7,8 @@
 // slots of shared memory (48 KB per CTA, two CTAs per SM), so that loads never wait for the two sums
 // over the group (of v^2 and of g v, both at once, in a fixed order).  Its share of dw stays in 8 registers
 // over all the rows that its CTA walks, is written once per CTA, and is added over the CTAs by a second kernel
-// in a fixed order: no atomics, the same result every time.  65536 rows of 2048: 222 us, 0.92 of the copy rate.
+// in a fixed order: no atomics, the same result every time.  65536 rows of 2048: 222 to 253 us on
+// different machines, 0.81 to 0.92 of the copy rate.
 // Sums over a group: of 8 m channels, m threads.  m a power of two up to 32: shuffles among those
 // lanes.  m a multiple of 32: shuffles, then the warps' sums through shared memory.  Any other m: every
 // thread adds its group's m values in shared memory (rare widths, not tuned).
@@ -63,10 +64,10 @@ template <typename T> constexpr int kDepth = 96 / (3 * (int)sizeof(Vec8<T>)) * 2
 // One CTA: `teams` rows side by side, d / 8 threads each; it walks the rows blockIdx.x * teams + team, a grid apart.
 // kMode: 0 groups of a power of two up to 32 threads, 1 of a multiple of 32, 2 any.
 // kMost bounds the threads, and with them the registers.  Two CTAs of 256 threads per SM leave the 128 registers that
-// a thread needs: 222 us at 65536 rows of 2048 in bf16 (6.0 TB/s), against 294 with three (80 registers, a few of
-// them spilled) and 335 with four.  Wider rows take one CTA per SM of 512 threads (122 registers; 4096 channels 0.8 to
-// 0.9 of the copy rate), 640 (96; 5120 channels 0.7 to 0.8, with the 64 registers that 1024 threads leave 0.33) or up
-// to 1024 (spilled; 8192 channels 0.43).
+// a thread needs: 222 us at 65536 rows of 2048 in bf16 on one machine (6.0 TB/s), against 294 with three (80
+// registers, a few of them spilled) and 335 with four.  Wider rows take one CTA per SM of 512 threads (122 registers;
+// 4096 channels 0.8 to 0.9 of the copy rate), 640 (96; 5120 channels 0.7 to 0.8, with the 64 registers that 1024
+// threads leave 0.33) or up to 1024 (spilled; 8192 channels 0.44).
 template <typename T, int kMode, int kMost>
 __global__ void __launch_bounds__(kMost, kMost == 256 ? 2 : 1) gated_norm_bwd_kernel(NormBwdParams p, int teams)
 {

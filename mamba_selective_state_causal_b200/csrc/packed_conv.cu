@@ -7,7 +7,8 @@
 // Forward.  A thread owns one 16-byte vector of channels over the rows of a 64-row chunk; they stream
 // through its own kRing slots of shared memory by cp.async, which keeps 128 KB of loads in flight per SM
 // without holding registers.  Every row is read once, plus three rows of halo per thread, and
-// written once: the bound is the memory's rate (65536 rows of 2304 channels: 106 us, 0.87 of the copy rate).
+// written once: the bound is the memory's rate (65536 rows of 2304 channels: 106 to 111 us on different
+// machines, 0.83 to 0.87 of the copy rate; in fp32 0.81).
 // The arithmetic and its order are the layer's
 // convolution's, so that a packed sequence gets the same v bit for bit.  The thread of a sequence's
 // first rows also writes its buffer: nobody else reads the slot's old one, so that tail_out may be
@@ -212,7 +213,9 @@ int launch_conv_t(const PackedConvParams &p, int sms, cudaStream_t st)
 // their dz) instead of handing dz between threads.  Its rows of u and dv stream through its own kBack
 // slots of shared memory by cp.async (72 KB in flight per SM, no registers held).  dw and dbias are summed
 // over the thread's rows in fp32, written per chunk, and added over the chunks in a fixed order by a second
-// kernel.  16384 rows of 4352 channels: 138 us, 0.79 of the copy rate; the arithmetic is as long.
+// kernel.  16384 rows of 4352 channels: 140 to 154 us on different machines, 0.71 to 0.78 of the copy rate (8192 rows in
+// fp32: 0.72).  By its counters neither the memory (67 %) nor the issue slots (62 %) are full: an SM holds 11 warps of
+// 144 registers, which wait for their rows and for the sigma of one row after the other.
 constexpr int kBack = 8;
 constexpr int kConvBwdT = 128;
 

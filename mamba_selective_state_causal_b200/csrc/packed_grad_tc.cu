@@ -7,7 +7,7 @@
 //   dB_j  = sum_{t>=j} M_tj C_t + w_j x_j^T Gam           w_j = dt_j e^{lam-cs_j}
 //   dC_t  = sum_{j<=t} M_tj B_j + e^{cs_t} dy_t^T h
 //   with E_tj = e^{cs_t-cs_j}, CB = C B^T, M_tj = E_tj dt_j (dy_t . x_j)
-// Three kernels (16384 rows of 32 heads, 9 sequences, the longest of 7000: 453 us; the bytes that go in and out
+// Three kernels (16384 rows of 32 heads, 9 sequences, the longest of 7000: 451 to 482 us on different machines; the bytes that go in and out
 // would take 48, with h and Gam, which go through memory once, 210):
 //   walk      the states and the adjoints, chunk after chunk, from the first or the last of a sequence,
 //             kept in registers in fp32; only what the gradients multiply by leaves the kernel
@@ -39,10 +39,12 @@ constexpr uint32_t kPiece = 128 * 128;    // a state's bf16 part: rows n, column
 // A state as the gradient's operand: kParts bf16 parts, each the rounding of what those before it leave
 template <int kParts> constexpr uint32_t kImage = kParts * kPiece;
 // Two parts where dA, one number per head, is made of many rows of many heads, three elsewhere: among random batches of
-// few rows or few heads two parts left dA off by up to 1.3e-5 of 64 bits, three by 2.4e-6 (worst of 120); from 1024
-// rows of 16 heads on two are off by 2e-6 as well (16384 rows of 32 heads: 1.9e-6), and three take 553 us instead
-// of 453 there.  The rows are those of the sequences, which the device knows (the buffers of a captured batch may hold
-// many more), so where the tensors have the rows for it the kernels hold both forms and the plan decides.
+// few rows or few heads two parts left dA off by up to 1.3e-5 of 64 bits, three by 2.4e-6 (worst of 120).  From 1024
+// rows of 16 heads on two are off by 1.9e-6 at 16384 rows of 32 heads, and in the worst batches known, of one-token
+// sequences whose terms cancel, by 3.3e-6 in the middle and 9.7e-6 at most (4680 batches of 1024 to 4096 of them);
+// three take 553 us instead of 453 at 16384 rows.  The rows are those of the sequences, which the device knows (the buffers of a captured batch may hold
+// many more), so where the tensors have the rows for it the kernels hold both forms and the plan decides (9 sequences of
+// 16384 rows in all 442 -> 451 us, one sequence 546 -> 535, on one machine).
 constexpr int kManyRows = 1024, kManyHeads = 16;
 inline bool either_form(int64_t total, int H) { return total >= kManyRows && H >= kManyHeads; }
 template <bool kEither>
@@ -129,7 +131,7 @@ __device__ __forceinline__ int grad_chunks(const PackedGradParams &p) { return p
 // the product S[n][p] = sum_j B[j][n] (w_j x_j[p]) (adjoint: C, e^{cs_j} dy) gets both parts of the weighted
 // operand side by side as 128 columns, and the state follows in registers, h = e^lam h + S.  What enters each chunk
 // goes out as the gradient kernel's operand, one bulk copy each.  What bounds it is a chunk's chain of waits,
-// 1.2 us, times the chunks of the longest part (136 in that batch): 166 us, at 3.3 TB/s of states.
+// 1.2 us, times the chunks of the longest part (136 in that batch): 164 to 170 us, at 3.3 TB/s of states.
 // Warps 0..7 keep the state (lane = n, 32 of p each), warps 8..15 fetch rows three chunks ahead and weigh them, warp
 // 16 issues the products, warp 17 runs the sums of dt A, warp 18 the copies out.
 constexpr int kWalkState = 8, kWalkScale = 8, kWalkThreads = 32 * (kWalkState + kWalkScale + 3);
@@ -456,13 +458,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1) packed_grad_walk_kernel(const
 // Per item, on the tensor pipe: GX = dy x^T;  dxI = B Gam^T, YI = C h^T;  dB += Gam (w x), dC += h (e^{cs} dy);
 // dx = (E CB)^T dy, dB += C^T M, dC += B^T M^T.  Warps 0..7: (M) E o CB and M in two parts, the row and column sums of
 // M o CB; (A) x_j . dxI_j and dy_t . YI_t; (D) dx.  Warps 8..15, ahead of them: (S) w x and e^{cs} dy in two parts;
-// (F) <Gam, h>.  (All 16 warps on one step after the other took 4.2 us per item, each step waiting for its own
-// latencies; so 3.9.)
+// (F) <Gam, h>.  (All 16 warps on one step after the other, each step waiting for its own latencies: 5.2 us per item
+// and SM, 292 us for 8352 items; so 4.6 to 5.0.)
 // M = 64 accumulators use 16 of each 32 TMEM lanes: GX and CB keep columns 16 k .. 16 k + 7 in the lower and the eight
 // behind them in the upper 16, so that a warp's 16 rows and 16 columns lie on or off the triangle together; dxI and
 // YI share their columns that way.  The sums that make ddt are finished by a warp of their own.
 // TMEM: dB 0..63, dC 64..127 (lanes n, columns rows), dxI | YI 128..191 and 192..255, GX 256..287 and 288..319,
-// dx 320..383, CB 384..415.  261 us for 8352 items: 4.6 us per item and SM, the tensor pipe busy a third of it.  Dealt
+// dx 320..383, CB 384..415.  8352 items: 259 to 283 us on different machines, the tensor pipe active for 38 % of it.  Dealt
 // out to two issuing warps it took 290 (the registers of a 21st warp), with products under lane == 0 430.
 constexpr int kMathWarps = 8, kWeighWarps = 8, kGradWarps = kMathWarps + kWeighWarps, kGradThreads = 32 * (kGradWarps + 4);
 constexpr uint32_t kColB = 0, kColC = 64, kColI = 128, kColG = 256, kColDx = 320, kColCB = 384;

@@ -7,7 +7,8 @@
 // first of them: the sequences are entered into a hash table over the slots in shared memory, each
 // entry keeping the lowest sequence, and a sequence that does not find itself there loses its slot.
 // The second kernel writes the chunks, each found by a binary search over the sequences' first chunks.
-// Both are latency: at 256 sequences of 8191 rows the two take a few microseconds once per batch.
+// Both are latency, once per batch: 4 us for one sequence, 6 for 24, 9 for 256, 32 for 4096 and 108 for 16384 (slots
+// named; in a captured graph, a call of its own takes 10 to 14 of the host at least).
 #include <algorithm>
 
 #include "packed.cuh"

@@ -14,7 +14,7 @@
 // are not positive are exponentiated.
 // A thread forms 4 x 4 tiles of each product from shared memory.  The bound is the fp32 pipe and shared memory,
 // 64 (N + P) + 4 N P multiply-adds per row and head over both passes, not the rows' bytes: 4000 rows of 8 heads
-// (P = 64, N = 128) take 155 us, 331 rows of 2 heads (P = N = 16) 21, most of it two launches.
+// (P = 64, N = 128) take 155 to 180 us, as they fall into sequences, 331 rows of 2 heads (P = N = 16) 21, most of it two launches.
 #include <algorithm>
 
 #include "packed.cuh"

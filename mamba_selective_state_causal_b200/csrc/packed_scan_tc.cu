@@ -64,7 +64,7 @@ __device__ __forceinline__ void split8(uint4 v, float w, uint4 &hi, uint4 &lo)
 }
 
 // dt as the scan uses it (dt_effective), with softplus(v) = max(v, 0) + log(1 + e^-|v|) from one exponential and one
-// quotient: log(1 + e) = 2 artanh(s) = 2 (s + s^3 / 3 + s^5 / 5 + ..), s = e / (2 + e) <= 1/3, cut off at s^17 (2e-9 of
+// quotient: log(1 + e) = 2 artanh(s) = 2 (s + s^3 / 3 + s^5 / 5 + ..), s = e / (2 + e) <= 1/3, cut off at s^17 (1.4e-10 of
 // it).  The scan warps take eight of them per lane and step: with log1p they, not the products, set pass A's pace.
 __device__ __forceinline__ float dt_used(const PackedScanParams &p, float raw, float bias)
 {
@@ -139,7 +139,7 @@ __device__ __forceinline__ void chunk_sums(const float2 (&d)[4], float A2a, floa
 // backwards, 64 at a time, so that the decay from each to the window's end is known when it is scaled.
 // Warps 0..15 scale X into its two bf16 parts (the rounding in place, the rest beside it), warp 16 issues the
 // products, warp 17 the loads, warps 18 and 19 run the dt sums of a head each, ahead of the others.
-// 65536 rows of 32 heads: 97 us, 0.8 us per step of 64 rows and two heads, which the chain of load, scaling and
+// 65536 rows of 32 heads: 97 to 99 us, 0.8 us per step of 64 rows and two heads, which the chain of load, scaling and
 // product through five stages sets; the bytes (x and B once) would take 44.
 constexpr int kStagesA = 5;
 constexpr int kQA = 64;                  // rows of a step
@@ -407,8 +407,8 @@ packed_state_tc_kernel(const __grid_constant__ Maps maps, const PackedScanParams
 //       used those of chunk c; it also starts the slot's state of a sequence about to begin into L2
 // A chunk of fewer than 128 rows takes only the K-steps (of 16 rows) of Y and S that have rows.
 // What bounds it: the compute warps' chain of steps, 4.7 us per chunk and head pair (T 0.3, w o X 0.7, waiting for Y
-// 0.4, y 0.6, decay 1.3, state 0.9, waiting for Ys 0.3), with the tensor pipe busy for about half of it; the bytes
-// would take 1.6.  65536 rows of 32 heads: 261 us, of 8191 rows in 256 sequences 158.
+// 0.4, y 0.6, decay 1.3, state 0.9, waiting for Ys 0.3), with the tensor pipe active for 32 % of the time at 65536 rows
+// and 25 % at 12001; the bytes would take 1.6.  65536 rows of 32 heads: 258 us, 8191 rows in 256 sequences 157.
 // TMEM (512 columns): R0 = 0..127 G; R1 = 128..255 Pm_a | Pm_b (bf16); T = 256..383; H = 384..511 (rows n).
 constexpr int kComputeWarps = 16;
 constexpr int kThreadsC = 32 * (kComputeWarps + 4);

@@ -34,7 +34,7 @@
 // runs over the whole sequence, last chunk first, and ends in dh0.
 // Only non-positive differences of cs are exponentiated.
 // kPacked: sequences laid end to end (packed.cuh), the chunks from the plan, one chain per sequence; on CUDA cores
-// only (bf16 at P = 64, N = 128 has packed_grad_tc.cu).  2003 rows of 8 heads, P = 32, N = 64, fp32: 121 us, three
+// only (bf16 at P = 64, N = 128 has packed_grad_tc.cu).  2003 rows of 8 heads, P = 32, N = 64, fp32: 125 to 128 us, three
 // rounds of the gradient kernel's CTAs at one per SM.
 #include <algorithm>
 #include <type_traits>

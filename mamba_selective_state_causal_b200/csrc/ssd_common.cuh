@@ -200,8 +200,9 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return *reinterpret_cast<uint32_t *>(&r);
 }
 
-// sigma(z) through the hardware's exponential and reciprocal (2 units in the last place each); e^-z beyond the
-// range of fp32 is infinite, and sigma 0
+// sigma(z) through the hardware's exponential and reciprocal: off by 2^-22 (2 units in the last place each) and, by the
+// rounding of z log2 e, |z| 2^-24 of e^-z: for the convolution's and the norm's gradients, which are held to 1e-5.
+// e^-z beyond the range of fp32 is infinite, and sigma 0
 __device__ __forceinline__ float sigma_fast(float z)
 {
     float e, r;
